@@ -1,0 +1,386 @@
+"""What is measured of the training-step operators around the QLoRA linear
+layer: token embedding, layer norm (and its form without the mean), and
+distillation from a teacher's top logits, each forward and backward.
+
+`listed()` names the cases, `draw()` gives more of the same ranges,
+`prepare()` makes what a training program has in hand before the call,
+`run()` is one pass (the plain form in 32 bits, or with `own` the library's
+entry points), `work()` the bytes and operations a pass cannot do without and
+`exact()` the result in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DTYPES = {"bf16": torch.bfloat16, "f32": torch.float32}
+SIZES = {"bf16": 2, "f32": 4}
+EPS = 1e-5
+EMBED_SCALE = 1.75  # a scaled table, as tied embeddings use
+
+
+def listed():
+    return [
+        # One decoded token through a 4096-wide norm: latency is all there is.
+        dict(name="norm fwd, one token", op="norm_fwd", M=1, N=4096, center=True, bias=True,
+             x="bf16", w="bf16", y="bf16"),
+        # A training batch of 4 x 1024 tokens through a 4096-wide norm without
+        # the mean, statistics kept for the backward pass.
+        dict(name="norm fwd, training batch", op="norm_fwd", M=4096, N=4096, center=False, bias=False,
+             x="bf16", w="bf16", y="bf16"),
+        # The backward pass of an 8192-wide layer norm on 2048 tokens.
+        dict(name="norm bwd, training batch", op="norm_bwd", M=2048, N=8192, center=True, bias=True,
+             x="bf16", w="bf16", y="bf16"),
+        # An fp32 residual stream of odd width, gradients of the layer in bf16.
+        dict(name="norm bwd, odd width", op="norm_bwd", M=1001, N=5003, center=True, bias=True,
+             x="f32", w="f32", y="bf16"),
+        # The table lookup of a training batch.
+        dict(name="embed fwd, training batch", op="embed_fwd", M=4096, V=32000, D=4096, pad=0.0,
+             w="bf16", y="bf16", ids="int64"),
+        # An fp32 table with rows for added tokens, odd sizes, ragged batch
+        # whose padding has no row of the table.
+        dict(name="embed fwd, ragged", op="embed_fwd", M=1777, V=32003, D=1027, pad=0.2,
+             w="f32", y="bf16", ids="int32"),
+        # The dense gradient of a trained table.
+        dict(name="embed bwd, training batch", op="embed_bwd", M=4096, V=32000, D=4096, pad=0.0,
+             w="f32", y="bf16", ids="int64"),
+        # A padded batch: one id takes half of all tokens.
+        dict(name="embed bwd, padded batch", op="embed_bwd", M=16000, V=32003, D=1024, pad=0.5,
+             w="bf16", y="f32", ids="int64"),
+        # The last token of a few sequences scored against the teacher.
+        dict(name="distill fwd, few rows", op="distill_fwd", M=4, V=32000, k=16, empty=0.0,
+             x="bf16", t="f32", ids="int64"),
+        # A training batch over a large vocabulary, prompt tokens carry no loss.
+        dict(name="distill fwd, training batch", op="distill_fwd", M=2048, V=128000, k=64, empty=0.25,
+             x="bf16", t="bf16", ids="int32"),
+        # Its gradient, the largest of the cases.
+        dict(name="distill bwd, training batch", op="distill_bwd", M=2048, V=128000, k=64, empty=0.0,
+             x="bf16", t="bf16", ids="int32"),
+        # fp32 logits over a vocabulary with added tokens (odd rows).
+        dict(name="distill bwd, odd vocabulary", op="distill_bwd", M=333, V=32003, k=100, empty=0.3,
+             x="f32", t="f32", ids="int64"),
+    ]
+
+
+def _spread(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["norm_fwd", "norm_bwd", "embed_fwd", "embed_bwd", "distill_fwd", "distill_bwd"])
+    kind = lambda: rng.choice(["bf16", "f32"])  # noqa: E731
+    odd = rng.random() < 0.4
+    if op.startswith("norm"):
+        N = _spread(rng, 64, 16384)
+        N = N if odd else max(64, N // 64 * 64)
+        M = _spread(rng, 1, min(16384, (1 << 25) // N))
+        return dict(op=op, M=M, N=N, center=rng.random() < 0.5, bias=rng.random() < 0.5,
+                    x=kind(), w=kind(), y=kind())
+    if op.startswith("embed"):
+        D = _spread(rng, 64, 8192)
+        D = D if odd else max(64, D // 64 * 64)
+        V = _spread(rng, 256, min(128000, (1 << 27) // D))
+        M = _spread(rng, 1, min(32768, (1 << 26) // D))
+        return dict(op=op, M=M, V=V, D=D, pad=rng.choice([0.0, 0.1, 0.5]), w=kind(), y=kind(),
+                    ids=rng.choice(["int32", "int64"]))
+    V = _spread(rng, 256, 128000)
+    V = V if odd else max(256, V // 64 * 64)
+    M = _spread(rng, 1, min(8192, (1 << 27) // V))
+    return dict(op=op, M=M, V=V, k=_spread(rng, 4, 256), empty=rng.choice([0.0, 0.3]), x=kind(), t=kind(),
+                ids=rng.choice(["int32", "int64"]))
+
+
+# --------------------------------------------------------------------- inputs
+def _generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(g, shape, dtype, scale=1.0):
+    return torch.randn(shape, generator=g, device="cuda").mul_(scale).to(dtype)
+
+
+def _token_ids(g, M, V, kind):
+    """Token ids whose frequency falls as 1 / rank, as words do."""
+    u = torch.rand(M, generator=g, device="cuda", dtype=torch.float64)
+    return (torch.exp(u * math.log(V)).long() - 1).clamp_(0, V - 1).to(getattr(torch, kind))
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    c, op = dict(case), case["op"]
+    s = {"case": c}
+    if op.startswith("norm"):
+        M, N = c["M"], c["N"]
+        # Activations with a spread of row scales, a mean, and columns that
+        # stand out.
+        x = torch.randn(M, N, generator=g, device="cuda")
+        x = x * torch.exp(0.5 * torch.randn(M, 1, generator=g, device="cuda")) + 0.3
+        x = x * torch.exp(0.5 * torch.randn(1, N, generator=g, device="cuda"))
+        s["x"] = x.to(DTYPES[c["x"]])
+        s["gamma"] = (1.0 + 0.2 * torch.randn(N, generator=g, device="cuda")).to(DTYPES[c["w"]])
+        s["beta"] = _normal(g, N, DTYPES[c["w"]], 0.1) if c["bias"] else None
+        if op == "norm_bwd":
+            s["dY"] = _normal(g, (M, N), DTYPES[c["y"]])
+            # What the forward pass kept: the mean and the reciprocal
+            # standard deviation of each row.
+            xd = s["x"].double()
+            mean = xd.mean(1) if c["center"] else xd.new_zeros(M)
+            rstd = ((xd - mean[:, None]).square().mean(1) + EPS).rsqrt()
+            s["stats"] = torch.stack([mean, rstd]).float()
+    elif op.startswith("embed"):
+        M, V, D = c["M"], c["V"], c["D"]
+        ids = _token_ids(g, M, V, c["ids"])
+        if c["pad"] > 0:
+            padded = torch.rand(M, generator=g, device="cuda") < c["pad"]
+            # Padding is the id 0 for the gradient (one hot row), and an id
+            # outside of the table for the lookup.
+            ids = torch.where(padded, torch.full_like(ids, 0 if op == "embed_bwd" else -1), ids)
+        s["ids"] = ids
+        if op == "embed_fwd":
+            s["W"] = _normal(g, (V, D), DTYPES[c["w"]], 0.02)
+        else:
+            s["dY"] = _normal(g, (M, D), DTYPES[c["y"]], 1e-2)
+    else:
+        M, V, k = c["M"], c["V"], c["k"]
+        z = torch.randn(M, V, generator=g, device="cuda").mul_(2.0)
+        # The teacher agrees with the student in part; its top entries are
+        # kept in falling order.
+        top, ids = (z * 0.7 + 1.5 * torch.randn(M, V, generator=g, device="cuda")).topk(k, dim=1)
+        empty = torch.rand(M, generator=g, device="cuda") < c["empty"]
+        ids[empty] = -1
+        s["logits"] = z.to(DTYPES[c["x"]])
+        s["top_ids"] = ids.to(getattr(torch, c["ids"]))
+        s["top_logits"] = top.to(DTYPES[c["t"]])
+        s["temperature"] = 2.0
+        if op == "distill_bwd":
+            lse = torch.empty(M, device="cuda", dtype=torch.float32)
+            for a in range(0, M, 256):
+                zd = s["logits"][a:a + 256].double() / s["temperature"]
+                lse[a:a + 256] = torch.logsumexp(zd, 1).float()
+            s["lse"] = torch.where(empty, 0.0, lse)
+            # A mean over the tokens that carry loss, weighted by token.
+            w = 0.5 + torch.rand(M, generator=g, device="cuda")
+            s["dloss"] = w / max(1, M)
+    return s
+
+
+# ---------------------------------------------------------------- plain forms
+def _norm_fwd(s):
+    c = s["case"]
+    x = s["x"].float()
+    mean = x.mean(1) if c["center"] else x.new_zeros(x.shape[0])
+    xc = x - mean[:, None]
+    rstd = 1.0 / torch.sqrt(xc.square().mean(1) + EPS)
+    y = xc * rstd[:, None] * s["gamma"].float()
+    if s["beta"] is not None:
+        y = y + s["beta"].float()
+    return [y.to(DTYPES[c["y"]]), torch.stack([mean, rstd])]
+
+
+def _norm_bwd(s):
+    c = s["case"]
+    dy, (mean, rstd) = s["dY"].float(), s["stats"]
+    xh = (s["x"].float() - mean[:, None]) * rstd[:, None]
+    g = dy * s["gamma"].float()
+    c2 = (g * xh).mean(1, keepdim=True)
+    dx = g - xh * c2
+    if c["center"]:
+        dx = dx - g.mean(1, keepdim=True)
+    dx = dx * rstd[:, None]
+    out = [dx.to(s["x"].dtype), (dy * xh).sum(0)]
+    if c["bias"]:
+        out.append(dy.sum(0))
+    return out
+
+
+def _embed_fwd(s):
+    ids = s["ids"].long()
+    live = (ids >= 0) & (ids < s["W"].shape[0])
+    rows = s["W"][torch.where(live, ids, 0)].float() * EMBED_SCALE
+    return [torch.where(live[:, None], rows, 0.0).to(DTYPES[s["case"]["y"]])]
+
+
+def _embed_bwd(s):
+    c = s["case"]
+    # Rows of ids outside of the table fall into one more row, which is cut.
+    ids = s["ids"].long()
+    ids = torch.where((ids >= 0) & (ids < c["V"]), ids, c["V"])
+    dW = torch.zeros(c["V"] + 1, c["D"], device="cuda").index_add_(0, ids, s["dY"].float())
+    return [(dW[:-1] * EMBED_SCALE).to(DTYPES[c["w"]])]
+
+
+def _teacher(s, dtype):
+    """Probabilities of the teacher's entries, their indexes with 0 where
+    there is none, and whether the row has any."""
+    ids, t = s["top_ids"].long(), s["top_logits"].to(dtype) / s["temperature"]
+    live = (ids >= 0) & (ids < s["logits"].shape[1]) & (t > -math.inf)
+    some = live.any(1)
+    t = torch.where(live, t, -math.inf)
+    top = torch.where(some, t.amax(1), 0.0)
+    e = torch.exp(t - top[:, None])
+    total = torch.where(some, e.sum(1), 1.0)
+    logp = torch.where(live, t - top[:, None] - torch.log(total)[:, None], 0.0)
+    return e / total[:, None], logp, torch.where(live, ids, 0), some
+
+
+def _distill_fwd(s):
+    T = s["temperature"]
+    z = s["logits"].float() / T
+    top = z.amax(1)
+    lse = top + torch.log(torch.exp(z - top[:, None]).sum(1))
+    p, logp, ids, some = _teacher(s, torch.float32)
+    loss = T * T * (p * (logp - z.gather(1, ids) + lse[:, None])).sum(1)
+    return [torch.where(some, loss, 0.0), torch.where(some, lse, 0.0)]
+
+
+def _distill_bwd(s):
+    T = s["temperature"]
+    p, _, ids, some = _teacher(s, torch.float32)
+    d = torch.exp(s["logits"].float() / T - s["lse"][:, None])
+    d.scatter_add_(1, ids, -p)
+    d = d * (s["dloss"] * T)[:, None]
+    return [torch.where((some & (s["dloss"] != 0))[:, None], d, 0.0).to(s["logits"].dtype)]
+
+
+# ----------------------------------------------------------- the entry points
+def _library(s):
+    import qlora_fine_tuning_blockwise_amd as q
+
+    c, op = s["case"], s["case"]["op"]
+    if op == "norm_fwd":
+        stats = torch.empty(2, c["M"], device="cuda")
+        y = q.qlora_norm_fwd(s["x"], s["gamma"], s["beta"], eps=EPS,
+                             norm=q.NORM_LAYER if c["center"] else q.NORM_RMS,
+                             y_dtype=DTYPES[c["y"]], stats_out=stats)
+        return [y, stats]
+    if op == "norm_bwd":
+        dX, dgamma, dbeta = q.qlora_norm_bwd(s["dY"], s["x"], s["gamma"], eps=EPS,
+                                             norm=q.NORM_LAYER if c["center"] else q.NORM_RMS,
+                                             stats=s["stats"], want_dbeta=c["bias"])
+        return [dX, dgamma, dbeta] if c["bias"] else [dX, dgamma]
+    if op == "embed_fwd":
+        return [q.qlora_embed_fwd(s["W"], s["ids"], scale=EMBED_SCALE, out_dtype=DTYPES[c["y"]])]
+    if op == "embed_bwd":
+        return [q.qlora_embed_bwd(s["dY"], s["ids"], c["V"], scale=EMBED_SCALE,
+                                  grad_dtype=DTYPES[c["w"]])]
+    if op == "distill_fwd":
+        lse = torch.empty(c["M"], device="cuda")
+        loss = q.qlora_distill_fwd(s["logits"], s["top_ids"], s["top_logits"],
+                                   temperature=s["temperature"], lse_out=lse)
+        return [loss, lse]
+    return [q.qlora_distill_bwd(s["logits"], s["top_ids"], s["top_logits"], s["dloss"], s["lse"],
+                                temperature=s["temperature"])]
+
+
+PLAIN = {"norm_fwd": _norm_fwd, "norm_bwd": _norm_bwd, "embed_fwd": _embed_fwd,
+         "embed_bwd": _embed_bwd, "distill_fwd": _distill_fwd, "distill_bwd": _distill_bwd}
+
+
+def run(state):
+    if own:
+        return _library(state)
+    return PLAIN[state["case"]["op"]](state)
+
+
+# ----------------------------------------------------------------------- work
+def _distinct_rows(M, V):
+    """Expected number of distinct ids among M of _token_ids(): the sum over
+    the ids of 1 - (1 - P(id))^M."""
+    total, v = 0.0, 0
+    while v < V:
+        step = max(1, v // 64)  # ids far out differ little: taken in groups
+        n = min(step, V - v)
+        p = math.log((v + n + 1) / (v + 1)) / (math.log(V) * n)
+        total += n * -math.expm1(M * math.log1p(-min(p, 1 - 1e-12)))
+        v += n
+    return total
+
+
+def work(case):
+    c, op = case, case["op"]
+    if op == "norm_fwd":
+        M, N = c["M"], c["N"]
+        return {"bytes": M * N * (SIZES[c["x"]] + SIZES[c["y"]]) + N * SIZES[c["w"]] * (1 + c["bias"]) + 8 * M,
+                "flops": 8.0 * M * N}
+    if op == "norm_bwd":
+        M, N = c["M"], c["N"]
+        return {"bytes": M * N * (2 * SIZES[c["x"]] + SIZES[c["y"]]) + N * SIZES[c["w"]]
+                + 4 * N * (1 + c["bias"]) + 8 * M, "flops": 14.0 * M * N}
+    if op.startswith("embed"):
+        M, V, D, ids = c["M"], c["V"], c["D"], 4 if c["ids"] == "int32" else 8
+        if op == "embed_fwd":
+            rows = _distinct_rows(max(1, round(M * (1 - c["pad"]))), V)
+            return {"bytes": ids * M + rows * D * SIZES[c["w"]] + M * D * SIZES[c["y"]], "flops": float(M * D)}
+        return {"bytes": ids * M + M * D * SIZES[c["y"]] + V * D * SIZES[c["w"]], "flops": float(M * D)}
+    M, V, k, ids = c["M"], c["V"], c["k"], 4 if c["ids"] == "int32" else 8
+    live = M * (1 - c["empty"])
+    heads = M * k * (ids + SIZES[c["t"]])
+    if op == "distill_fwd":
+        return {"bytes": live * V * SIZES[c["x"]] + heads + 8 * M, "flops": 4.0 * live * V}
+    return {"bytes": (live + M) * V * SIZES[c["x"]] + heads + 8 * M, "flops": 5.0 * live * V}
+
+
+# ------------------------------------------------------------------- in 64 bits
+def exact(case, seed):
+    """From the operators' definitions: the norm by its mean and variance and
+    its gradient as the vector-Jacobian product written out, the table's
+    gradient as a sum by token, the loss as the divergence of two
+    distributions, and its gradient by the rule for a softmax."""
+    s = prepare(case, seed)
+    c, op = s["case"], case["op"]
+    f = torch.float64
+    if op.startswith("norm"):
+        x, gamma = s["x"].to(f), s["gamma"].to(f)
+        N = x.shape[1]
+        mean = x.sum(1, keepdim=True) / N if c["center"] else torch.zeros_like(x[:, :1])
+        var = (x - mean).pow(2).sum(1, keepdim=True) / N
+        sd = (var + EPS).sqrt()
+        if op == "norm_fwd":
+            beta = s["beta"].to(f) if c["bias"] else 0.0
+            return [(x - mean) / sd * gamma + beta, torch.cat([mean, 1 / sd], 1).t().contiguous()]
+        dy = s["dY"].to(f)
+        h = dy * gamma / sd
+        dvar = -(h * (x - mean)).sum(1, keepdim=True) / (2 * (var + EPS))
+        dx = h + 2 * dvar * (x - mean) / N
+        if c["center"]:
+            dx = dx - h.sum(1, keepdim=True) / N  # the deviations sum to 0: the variance adds nothing
+        out = [dx, (dy * (x - mean) / sd).sum(0)]
+        return out + [dy.sum(0)] if c["bias"] else out
+    if op == "embed_fwd":
+        out = torch.zeros(c["M"], c["D"], dtype=f, device="cuda")
+        at = ((s["ids"] >= 0) & (s["ids"] < c["V"])).nonzero()[:, 0]
+        out[at] = EMBED_SCALE * s["W"][s["ids"][at].long()].to(f)
+        return [out]
+    if op == "embed_bwd":
+        at = ((s["ids"] >= 0) & (s["ids"] < c["V"])).nonzero()[:, 0]
+        order = at[torch.argsort(s["ids"][at], stable=True)]
+        ids, count = torch.unique_consecutive(s["ids"][order].long(), return_counts=True)
+        sums = torch.cat([torch.zeros(1, c["D"], dtype=f, device="cuda"), s["dY"][order].to(f)]).cumsum(0)
+        last = count.cumsum(0)
+        dW = torch.zeros(c["V"], c["D"], dtype=f, device="cuda")
+        dW[ids] = EMBED_SCALE * (sums[last] - sums[last - count])
+        return [dW]
+    T, M, V = s["temperature"], c["M"], c["V"]
+    valid = (s["top_ids"] >= 0) & (s["top_ids"] < V)
+    loss, lse, grad = [], [], []
+    for a in range(0, M, 256):  # some rows at a time: 64 bits take room
+        z, ok = s["logits"][a:a + 256].to(f) / T, valid[a:a + 256]
+        ids = s["top_ids"][a:a + 256].long().clamp(0, V - 1)
+        t = (s["top_logits"][a:a + 256].to(f) / T).masked_fill(~ok, -math.inf)
+        some = ok.any(1, keepdim=True)
+        p = torch.softmax(t.masked_fill(~some, 0.0), 1) * some * ok
+        total = torch.logsumexp(z, 1, keepdim=True)
+        if op == "distill_fwd":
+            logq = z.gather(1, ids) - total
+            loss.append(T * T * (torch.special.xlogy(p, p) - p * logq).sum(1))
+            lse.append((total * some)[:, 0])
+        else:
+            d = torch.exp(z - total) * some
+            d.scatter_add_(1, ids, -p)
+            grad.append((d * T * s["dloss"][a:a + 256, None].to(f)).float())
+    if op == "distill_fwd":
+        return [torch.cat(loss), torch.cat(lse)]
+    return [torch.cat(grad)]
