@@ -156,11 +156,15 @@ def prepare(case, seed):
         s["top_logits"] = top.to(DTYPES[c["t"]])
         s["temperature"] = 2.0
         if op == "distill_bwd":
-            lse = torch.empty(M, device="cuda", dtype=torch.float32)
+            # What the forward pass kept of each row: its largest logit and the
+            # logarithm of the sum of the exponentials taken from there.
+            s["stats"] = torch.empty(2, M, device="cuda", dtype=torch.float32)
             for a in range(0, M, 256):
-                zd = s["logits"][a:a + 256].double() / s["temperature"]
-                lse[a:a + 256] = torch.logsumexp(zd, 1).float()
-            s["lse"] = torch.where(empty, 0.0, lse)
+                zd = s["logits"][a:a + 256].double()
+                most = zd.amax(1)
+                total = torch.exp((zd - most[:, None]) / s["temperature"]).sum(1)
+                s["stats"][:, a:a + 256] = torch.stack([most, torch.log(total)]).float()
+            s["stats"][:, empty] = 0.0
             # A mean over the tokens that carry loss, weighted by token.
             w = 0.5 + torch.rand(M, generator=g, device="cuda")
             s["dloss"] = w / max(1, M)
@@ -228,18 +232,20 @@ def _teacher(s, dtype):
 
 def _distill_fwd(s):
     T = s["temperature"]
-    z = s["logits"].float() / T
-    top = z.amax(1)
-    lse = top + torch.log(torch.exp(z - top[:, None]).sum(1))
+    z = s["logits"].float()
+    most = z.amax(1)
+    z = (z - most[:, None]) / T
+    total = torch.log(torch.exp(z).sum(1))
     p, logp, ids, some = _teacher(s, torch.float32)
-    loss = T * T * (p * (logp - z.gather(1, ids) + lse[:, None])).sum(1)
-    return [torch.where(some, loss, 0.0), torch.where(some, lse, 0.0)]
+    loss = T * T * (p * (logp - z.gather(1, ids) + total[:, None])).sum(1)
+    return [torch.where(some, loss, 0.0), torch.where(some, torch.stack([most, total]), 0.0)]
 
 
 def _distill_bwd(s):
     T = s["temperature"]
     p, _, ids, some = _teacher(s, torch.float32)
-    d = torch.exp(s["logits"].float() / T - s["lse"][:, None])
+    most, total = s["stats"]
+    d = torch.exp((s["logits"].float() - most[:, None]) / T - total[:, None])
     d.scatter_add_(1, ids, -p)
     d = d * (s["dloss"] * T)[:, None]
     return [torch.where((some & (s["dloss"] != 0))[:, None], d, 0.0).to(s["logits"].dtype)]
@@ -267,11 +273,11 @@ def _library(s):
         return [q.qlora_embed_bwd(s["dY"], s["ids"], c["V"], scale=EMBED_SCALE,
                                   grad_dtype=DTYPES[c["w"]])]
     if op == "distill_fwd":
-        lse = torch.empty(c["M"], device="cuda")
+        stats = torch.empty(2, c["M"], device="cuda")
         loss = q.qlora_distill_fwd(s["logits"], s["top_ids"], s["top_logits"],
-                                   temperature=s["temperature"], lse_out=lse)
-        return [loss, lse]
-    return [q.qlora_distill_bwd(s["logits"], s["top_ids"], s["top_logits"], s["dloss"], s["lse"],
+                                   temperature=s["temperature"], stats_out=stats)
+        return [loss, stats]
+    return [q.qlora_distill_bwd(s["logits"], s["top_ids"], s["top_logits"], s["dloss"], s["stats"],
                                 temperature=s["temperature"])]
 
 
@@ -319,8 +325,8 @@ def work(case):
     live = M * (1 - c["empty"])
     heads = M * k * (ids + SIZES[c["t"]])
     if op == "distill_fwd":
-        return {"bytes": live * V * SIZES[c["x"]] + heads + 8 * M, "flops": 4.0 * live * V}
-    return {"bytes": (live + M) * V * SIZES[c["x"]] + heads + 8 * M, "flops": 5.0 * live * V}
+        return {"bytes": live * V * SIZES[c["x"]] + heads + 12 * M, "flops": 4.0 * live * V}
+    return {"bytes": (live + M) * V * SIZES[c["x"]] + heads + 12 * M, "flops": 5.0 * live * V}
 
 
 # ------------------------------------------------------------------- in 64 bits
@@ -365,7 +371,7 @@ def exact(case, seed):
         return [dW]
     T, M, V = s["temperature"], c["M"], c["V"]
     valid = (s["top_ids"] >= 0) & (s["top_ids"] < V)
-    loss, lse, grad = [], [], []
+    loss, stats, grad = [], [], []
     for a in range(0, M, 256):  # some rows at a time: 64 bits take room
         z, ok = s["logits"][a:a + 256].to(f) / T, valid[a:a + 256]
         ids = s["top_ids"][a:a + 256].long().clamp(0, V - 1)
@@ -376,11 +382,12 @@ def exact(case, seed):
         if op == "distill_fwd":
             logq = z.gather(1, ids) - total
             loss.append(T * T * (torch.special.xlogy(p, p) - p * logq).sum(1))
-            lse.append((total * some)[:, 0])
+            most = s["logits"][a:a + 256].to(f).amax(1, keepdim=True)
+            stats.append((torch.cat([most, total - most / T], 1) * some).t())
         else:
             d = torch.exp(z - total) * some
             d.scatter_add_(1, ids, -p)
             grad.append((d * T * s["dloss"][a:a + 256, None].to(f)).float())
     if op == "distill_fwd":
-        return [torch.cat(loss), torch.cat(lse)]
+        return [torch.cat(loss), torch.cat(stats, 1)]
     return [torch.cat(grad)]
