@@ -48,7 +48,8 @@
  *   - bf16 tensors are passed as uint16_t bit patterns.
  *   - `stream` is a hipStream_t (NULL = the default stream). Every compute
  *     entry point only enqueues work on it and returns without synchronizing.
- *   - Device pointers must be 16-byte aligned. Outputs must not alias inputs.
+ *   - Device pointers must be 16-byte aligned (the row operators at the end of
+ *     this header say where less is enough). Outputs must not alias inputs.
  *   - Return value: QLORA_OK (0) or a status below. Argument errors are
  *     detected on the host before anything is enqueued. No C++ exception
  *     crosses the ABI.
@@ -69,8 +70,11 @@ extern "C" {
 #define QLORA_OK 0
 #define QLORA_ERR_INVALID_ARG 1 /* NULL pointer, negative size, bad enum */
 #define QLORA_ERR_SHAPE 2       /* K % 64 != 0, N or K < 1, or two of M, N, K
-                                   whose product passes 2^40 elements */
-#define QLORA_ERR_ALIGN 3       /* a device pointer is not 16-byte aligned */
+                                   whose product passes 2^40 elements; a row
+                                   operator's size or stride out of its range */
+#define QLORA_ERR_ALIGN 3       /* a device pointer is not 16-byte aligned (the
+                                   row operators' matrices and vectors: not
+                                   aligned to their elements) */
 #define QLORA_ERR_DTYPE 4       /* unsupported dtype enum */
 #define QLORA_ERR_RANK 5        /* r not a positive multiple of 16, or r > 256 */
 #define QLORA_ERR_WORKSPACE 6   /* workspace smaller than qlora_workspace_bytes() */
@@ -84,6 +88,9 @@ extern "C" {
 /* Element types. */
 #define QLORA_DTYPE_F32 0
 #define QLORA_DTYPE_BF16 1
+/* Index types (token ids of the row operators). */
+#define QLORA_DTYPE_I32 2
+#define QLORA_DTYPE_I64 3
 
 /* Second-level formats of absmax_q (see STORAGE FORMAT). */
 #define QLORA_DQ_INT8 0
@@ -107,6 +114,15 @@ extern "C" {
 #define QLORA_OP_MERGE 2
 #define QLORA_OP_FWD_LEAN 3 /* the forward without a bf16 copy of the weight */
 #define QLORA_OP_BWD_LEAN 4 /* the backward without a bf16 copy of the weight */
+
+/* Forms of the norm. */
+#define QLORA_NORM_LAYER 0 /* around the row's mean */
+#define QLORA_NORM_RMS 1   /* without the mean */
+
+/* Limits of the row operators (QLORA_ERR_SHAPE beyond them). */
+#define QLORA_MAX_ROWS (1 << 24)       /* rows or tokens of a call */
+#define QLORA_MAX_NORM_WIDTH 16384     /* elements of a normed row */
+#define QLORA_MAX_TOP 1024             /* teacher entries of a row */
 
 /* Format version of the storage layout above. */
 #define QLORA_FORMAT_VERSION 1u
@@ -380,6 +396,132 @@ int qlora_gemm_bf16_nt(const uint16_t* a, int64_t lda, const uint16_t* b, int64_
 int qlora_linear_fwd_noalloc(const qlora_nf4* w, const uint16_t* x, int64_t M,
                              const uint16_t* A, const uint16_t* B, int r, float alpha, void* y,
                              int y_dtype, float* u_out, void* stream);
+
+/* ROW OPERATORS: what a training step runs before and after the linear
+ * layers - the token embedding, the norms, and a distillation loss - each
+ * with its gradient. The pages keep these parts in 16-bit and out of the
+ * quantized base ([P3] "How it works"); their bf16 outputs are the x, and
+ * their bf16 gradients the dY, of the linear entry points.
+ *   - Matrices are row-major with a row stride ld* in elements (ld* >= the
+ *     row's width; elements between the width and the stride are neither read
+ *     nor written) and are fp32 or bf16 by their *_dtype. They, the id arrays
+ *     and the vectors need the alignment of their elements only; dW and the
+ *     workspace are 16-byte aligned.
+ *   - Sums, statistics and losses are fp32; a bf16 output is rounded once, to
+ *     nearest even.
+ *   - Results do not depend on the launch or on earlier calls: no
+ *     floating-point atomics, and sums are taken in a fixed order.
+ *   - M == 0 is a successful no-op (gradients over the rows become zero).
+ *   - Like the other entry points they allocate nothing, do not synchronise
+ *     and may be captured into a HIP graph. */
+
+/* Token embedding ([P3] "How it works" keeps embeddings in 16-bit):
+ *   out[m] = scale * W[ids[m]]
+ *   W    [V,D] (w_dtype), ids [M] QLORA_DTYPE_I32 or QLORA_DTYPE_I64;
+ *   out  [M,D] (out_dtype).
+ * An id outside of [0, V) gives a row of zeros (padding). QLORA_ERR_SHAPE
+ * unless 1 <= V < 2^31 - 1, 1 <= D <= 2^24, V*D <= 2^40, M <= QLORA_MAX_ROWS,
+ * and the strides hold their rows; QLORA_ERR_DTYPE for another type;
+ * QLORA_ERR_INVALID_ARG for M < 0, a NULL array or a non-finite scale. */
+int qlora_embed_fwd(const void* W, int64_t ldw, int w_dtype, int64_t V, int64_t D,
+                    const void* ids, int ids_dtype, int64_t M, float scale, void* out,
+                    int64_t ldo, int out_dtype, void* stream);
+
+/* Device workspace, in bytes, of qlora_embed_bwd. Host only; 0 on invalid
+ * sizes. */
+size_t qlora_embed_bwd_workspace_bytes(int64_t M, int64_t D);
+
+/* Gradient of the embedding's table, dense:
+ *   dW[v] = scale * sum over m with ids[m] = v of dY[m]   (in token order)
+ *   dY  [M,D] (dy_dtype); dW [V,D] contiguous (grad_dtype), zero for ids that
+ *   do not occur. accumulate != 0: the sums are added to dW instead (one
+ *   rounding), and rows whose id does not occur are left as they were.
+ * Tokens whose id lies outside of [0, V) add nothing, and their dY is not
+ * read. Errors as qlora_embed_fwd; QLORA_ERR_WORKSPACE for a workspace
+ * smaller than qlora_embed_bwd_workspace_bytes(M, D). */
+int qlora_embed_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* ids, int ids_dtype,
+                    int64_t M, int64_t V, int64_t D, float scale, void* dW, int grad_dtype,
+                    int accumulate, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norm of each row ([P3] "How it works" keeps norms in 16-bit). norm =
+ * QLORA_NORM_LAYER:
+ *   y = (x - mean) * rstd * gamma + beta,
+ *   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps);
+ * QLORA_NORM_RMS: the same with mean = 0.
+ *   x [M,N] (x_dtype); gamma, beta [N] (w_dtype), each may be NULL (1 and 0);
+ *   y [M,N] (y_dtype).
+ *   stats  fp32 [2,M] or NULL; when given it receives the means, then the
+ *          rstd (for the backward).
+ * QLORA_ERR_SHAPE unless 1 <= N <= QLORA_MAX_NORM_WIDTH, M <= QLORA_MAX_ROWS
+ * and the strides hold their rows; QLORA_ERR_INVALID_ARG for another norm,
+ * M < 0, a NULL x or y, or an eps that is negative or not finite. */
+int qlora_norm_fwd(const void* x, int64_t ldx, int x_dtype, int64_t M, int64_t N, int norm,
+                   const void* gamma, const void* beta, int w_dtype, float eps, void* y,
+                   int64_t ldy, int y_dtype, float* stats, void* stream);
+
+/* Device workspace, in bytes, of qlora_norm_bwd. Host only; 0 on invalid
+ * sizes. */
+size_t qlora_norm_bwd_workspace_bytes(int64_t M, int64_t N);
+
+/* Gradients of the norm: with xh = (x - mean) * rstd and g = dY * gamma,
+ *   dX     = rstd * (g - mean(g) - xh * mean(g * xh))   (no mean(g) for RMS)
+ *   dgamma = sum over the rows of dY * xh,  dbeta = sum over the rows of dY
+ *   dY [M,N] (dy_dtype), x, gamma, eps as in the forward; stats from the
+ *   forward, or NULL to recompute them.
+ *   dX [M,N] (dx_dtype), dgamma, dbeta [N] (grad_dtype) may each be NULL to
+ *   skip that output.
+ * M == 0 writes zero dgamma and dbeta. Errors as qlora_norm_fwd;
+ * QLORA_ERR_WORKSPACE for a workspace smaller than
+ * qlora_norm_bwd_workspace_bytes(M, N) (not needed, and may be NULL, without
+ * dgamma and dbeta). */
+int qlora_norm_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* x, int64_t ldx,
+                   int x_dtype, int64_t M, int64_t N, int norm, const void* gamma, int w_dtype,
+                   float eps, const float* stats, void* dX, int64_t lddx, int dx_dtype,
+                   void* dgamma, void* dbeta, int grad_dtype, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Device workspace, in bytes, of qlora_distill_fwd. Host only; 0 on invalid
+ * sizes. */
+size_t qlora_distill_fwd_workspace_bytes(int64_t M, int64_t V);
+
+/* Distillation loss of each row against a teacher's top logits ([P1]'s
+ * introduction mentions distillation beside the method): the divergence of
+ * the student's distribution from the teacher's, both at a temperature T.
+ *   logits     [M,V] (z_dtype), the student's z;
+ *   top_ids    [M,k] contiguous (QLORA_DTYPE_I32 or QLORA_DTYPE_I64) and
+ *   top_logits [M,k] contiguous (t_dtype): the vocabulary entries that the
+ *              teacher gave, in any order. An entry is live if its id lies in
+ *              [0, V) and its logit is above -infinity; the teacher's
+ *              distribution p is the softmax of t/T over the live ones.
+ *   loss[m]  = T^2 * sum_j p_j (log p_j - log q[id_j]),  q = softmax(z / T)
+ *   stats      fp32 [2,M] or NULL; when given it receives the rows' largest
+ *              logits, then log sum_v exp((z_v - largest) / T) (for the
+ *              backward).
+ * A row with no live entry has loss 0 and stats 0, and its logits are not
+ * read. An id that stands more than once in a row counts each time. A live
+ * entry whose student logit is -infinity makes the loss +infinity; NaN
+ * spreads to its row. QLORA_ERR_SHAPE unless 1 <= V < 2^31 - 1, 1 <= k <=
+ * QLORA_MAX_TOP, M <= QLORA_MAX_ROWS, M*V <= 2^40 and ldz >= V;
+ * QLORA_ERR_INVALID_ARG for M < 0, a NULL array or a temperature outside of
+ * [2^-20, 2^20]; QLORA_ERR_WORKSPACE for a workspace smaller than
+ * qlora_distill_fwd_workspace_bytes(M, V). */
+int qlora_distill_fwd(const void* logits, int64_t ldz, int z_dtype, int64_t M, int64_t V,
+                      const void* top_ids, int ids_dtype, const void* top_logits, int t_dtype,
+                      int k, float temperature, float* loss, float* stats, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* Gradient of the losses with respect to the logits:
+ *   dlogits[m][v] = dloss[m] * T * (q_v - sum over j with id_j = v of p_j)
+ *   dloss    fp32 [M], the gradient of each row's loss; a row with dloss 0 or
+ *            without a live entry gets zeros, whatever its logits hold;
+ *   stats    fp32 [2,M] from qlora_distill_fwd with the same logits and
+ *            temperature;
+ *   dlogits  [M,V] (grad_dtype), row stride ldg >= V.
+ * The other arguments and errors as in the forward. */
+int qlora_distill_bwd(const void* logits, int64_t ldz, int z_dtype, int64_t M, int64_t V,
+                      const void* top_ids, int ids_dtype, const void* top_logits, int t_dtype,
+                      int k, float temperature, const float* stats, const float* dloss,
+                      void* dlogits, int64_t ldg, int grad_dtype, void* stream);
 
 #ifdef __cplusplus
 }

@@ -6,9 +6,16 @@ The functions below carry the names of the C entry points
 (include/qlora_amd.h). They only marshal arguments: torch supplies device
 memory and the current stream, and every step of the computation runs in
 libqlora_amd.so. Tensors must be contiguous and on a ROCm device.
+
+The row operators (qlora_embed_*, qlora_norm_*, qlora_distill_*) take
+matrices whose rows are contiguous, at any row stride (views of wider or
+longer tensors), and run on the device of their tensors whichever is current.
+Without `stream` they use that device's current stream; with it, what they
+allocate belongs to that stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -21,6 +28,10 @@ __all__ = [
     "qlora_codebook_id", "qlora_setup_id", "qlora_nf4_check",
     "qlora_workspace_bytes", "qlora_quantize_nf4_dq", "qlora_dequant_bf16",
     "qlora_linear_fwd", "qlora_linear_bwd", "qlora_linear_fwd_noalloc", "qlora_gemm_bf16_nt", "qlora_merge_lora", "qlora_adamw_step",
+    "qlora_embed_fwd", "qlora_embed_bwd", "qlora_embed_bwd_workspace_bytes",
+    "qlora_norm_fwd", "qlora_norm_bwd", "qlora_norm_bwd_workspace_bytes",
+    "qlora_distill_fwd", "qlora_distill_bwd", "qlora_distill_fwd_workspace_bytes",
+    "NORM_LAYER", "NORM_RMS",
     "NF4Weight", "DQ_INT8", "DQ_UINT8", "DQ_E4M3", "LAYOUT_ROWS", "LAYOUT_KSLAB32",
 ]
 
@@ -65,6 +76,7 @@ def _dtype_code(dt) -> int:
 
 DQ_INT8, DQ_UINT8, DQ_E4M3 = _lib.DQ_INT8, _lib.DQ_UINT8, _lib.DQ_E4M3
 LAYOUT_ROWS, LAYOUT_KSLAB32 = _lib.LAYOUT_ROWS, _lib.LAYOUT_KSLAB32
+NORM_LAYER, NORM_RMS = _lib.NORM_LAYER, _lib.NORM_RMS
 
 
 class NF4Weight:
@@ -351,3 +363,249 @@ def qlora_adamw_step(param: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Ten
                                       float(lr), float(beta1), float(beta2), float(eps),
                                       float(weight_decay), int(step), _stream(stream))
     _lib.check(st, "qlora_adamw_step")
+
+
+# ------------------------------------------------------------ row operators
+_FLOATS = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
+_INDEXES = {torch.int32: _lib.DTYPE_I32, torch.int64: _lib.DTYPE_I64}
+_HERE = contextlib.nullcontext()
+
+
+def _place(t, stream):
+    """Context in which a row operator on t's device allocates and launches."""
+    dev = t.device
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a ROCm device, got {dev}")
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _here(dev):
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _matrix(t, name, shape, device) -> int:
+    """Row stride of a [rows, width] fp32 or bf16 matrix whose rows are
+    contiguous; shape and device checked."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in _FLOATS:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected fp32 or bf16")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    M, N = shape
+    if N > 1 and M > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name}: rows must be contiguous")
+    if M <= 1:
+        return max(N, 1)
+    if t.stride(0) < N:
+        raise ValueError(f"{name}: row stride {t.stride(0)} below the width {N}")
+    return t.stride(0)
+
+
+def _indexes(t, name, shape, device) -> int:
+    _need(t, name, shape, tuple(_INDEXES), device)
+    return _INDEXES[t.dtype]
+
+
+def _bytes(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.dim() != 1 or not workspace.is_contiguous() \
+            or workspace.device != device:
+        raise ValueError("workspace: a contiguous 1-D uint8 tensor on the tensors' device")
+    return workspace
+
+
+def _two_dims(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: must have two dimensions, has {t.dim()}")
+    return t.shape
+
+
+def qlora_embed_bwd_workspace_bytes(M: int, D: int) -> int:
+    return int(_lib.load().qlora_embed_bwd_workspace_bytes(M, D))
+
+
+def qlora_norm_bwd_workspace_bytes(M: int, N: int) -> int:
+    return int(_lib.load().qlora_norm_bwd_workspace_bytes(M, N))
+
+
+def qlora_distill_fwd_workspace_bytes(M: int, V: int) -> int:
+    return int(_lib.load().qlora_distill_fwd_workspace_bytes(M, V))
+
+
+def qlora_embed_fwd(W: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
+                    out: torch.Tensor | None = None, out_dtype=None, stream=None) -> torch.Tensor:
+    """out[m] = scale * W[ids[m]]: W [V,D] fp32 or bf16, ids [M] int32 or
+    int64 (an id outside of [0, V) gives zeros), out [M,D] (W's dtype by
+    default)."""
+    V, D = _two_dims(W, "W")
+    dev = W.device
+    M = ids.numel()
+    ldw = _matrix(W, "W", (V, D), dev)
+    ids_dtype = _indexes(ids, "ids", (M,), dev)
+    with _place(W, stream):
+        if out is None:
+            out = torch.empty((M, D), dtype=W.dtype if out_dtype is None else out_dtype, device=dev)
+        ldo = _matrix(out, "out", (M, D), dev)
+        st = _lib.load().qlora_embed_fwd(_at(W), ldw, _FLOATS[W.dtype], V, D, _at(ids), ids_dtype,
+                                         M, scale, _at(out), ldo, _FLOATS[out.dtype], _here(dev))
+    _lib.check(st, "qlora_embed_fwd")
+    return out
+
+
+def qlora_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 1.0,
+                    grad_dtype=torch.float32, dW: torch.Tensor | None = None,
+                    accumulate: bool = False, workspace: torch.Tensor | None = None,
+                    stream=None) -> torch.Tensor:
+    """The dense gradient of the table: dW[v] = scale * sum of dY's rows with
+    id v, [V,D] (grad_dtype, or a given dW's); with accumulate the sums are
+    added to the given dW."""
+    M, D = _two_dims(dY, "dY")
+    dev = dY.device
+    ldy = _matrix(dY, "dY", (M, D), dev)
+    ids_dtype = _indexes(ids, "ids", (M,), dev)
+    if accumulate and dW is None:
+        raise ValueError("qlora_embed_bwd: accumulate needs dW")
+    _need(dW, "dW", (V, D), tuple(_FLOATS), dev)
+    with _place(dY, stream):
+        if dW is None:
+            dW = torch.empty((V, D), dtype=grad_dtype, device=dev)
+            _need(dW, "dW", (V, D), tuple(_FLOATS), dev)
+        workspace = _bytes(workspace, qlora_embed_bwd_workspace_bytes(M, D), dev)
+        st = _lib.load().qlora_embed_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(ids), ids_dtype, M, V,
+                                         D, scale, _at(dW), _FLOATS[dW.dtype], int(accumulate),
+                                         _at(workspace), workspace.numel(), _here(dev))
+    _lib.check(st, "qlora_embed_bwd")
+    return dW
+
+
+def _norm_vectors(N, dev, *named):
+    """Dtype code of the affine vectors (they share one; fp32 without any)."""
+    code = None
+    for t, name in named:
+        if t is None:
+            continue
+        _need(t, name, (N,), tuple(_FLOATS), dev)
+        if code is not None and code != _FLOATS[t.dtype]:
+            raise ValueError(f"{name}: the affine vectors must share one dtype")
+        code = _FLOATS[t.dtype]
+    return _lib.DTYPE_F32 if code is None else code
+
+
+def qlora_norm_fwd(x: torch.Tensor, gamma: torch.Tensor | None = None,
+                   beta: torch.Tensor | None = None, eps: float = 1e-5, norm: int = NORM_LAYER,
+                   y: torch.Tensor | None = None, y_dtype=None,
+                   stats_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Layer norm (NORM_LAYER) or its form without the mean (NORM_RMS) of the
+    rows of x [M,N]; y in x's dtype by default. stats_out: fp32 [2,M], receives
+    the rows' means and reciprocal standard deviations for the backward."""
+    M, N = _two_dims(x, "x")
+    dev = x.device
+    ldx = _matrix(x, "x", (M, N), dev)
+    w_dtype = _norm_vectors(N, dev, (gamma, "gamma"), (beta, "beta"))
+    _need(stats_out, "stats_out", (2, M), torch.float32, dev)
+    with _place(x, stream):
+        if y is None:
+            y = torch.empty((M, N), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
+        ldy = _matrix(y, "y", (M, N), dev)
+        st = _lib.load().qlora_norm_fwd(_at(x), ldx, _FLOATS[x.dtype], M, N, norm, _at(gamma),
+                                        _at(beta), w_dtype, eps, _at(y), ldy, _FLOATS[y.dtype],
+                                        _at(stats_out), _here(dev))
+    _lib.check(st, "qlora_norm_fwd")
+    return y
+
+
+def qlora_norm_bwd(dY: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None = None,
+                   eps: float = 1e-5, norm: int = NORM_LAYER, stats: torch.Tensor | None = None,
+                   want_dx: bool = True, want_dgamma: bool = True, want_dbeta: bool = True,
+                   dx_dtype=None, grad_dtype=torch.float32, workspace: torch.Tensor | None = None,
+                   stream=None):
+    """Returns (dX or None, dgamma or None, dbeta or None) of the norm: dX in
+    x's dtype by default. stats: the forward's stats_out, or None to recompute
+    them."""
+    M, N = _two_dims(x, "x")
+    dev = x.device
+    ldx = _matrix(x, "x", (M, N), dev)
+    ldy = _matrix(dY, "dY", (M, N), dev)
+    w_dtype = _norm_vectors(N, dev, (gamma, "gamma"))
+    _need(stats, "stats", (2, M), torch.float32, dev)
+    dx_dtype = x.dtype if dx_dtype is None else dx_dtype
+    if dx_dtype not in _FLOATS or grad_dtype not in _FLOATS:
+        raise ValueError("qlora_norm_bwd: gradients are fp32 or bf16")
+    with _place(x, stream):
+        dX = torch.empty((M, N), dtype=dx_dtype, device=dev) if want_dx else None
+        dgamma = torch.empty(N, dtype=grad_dtype, device=dev) if want_dgamma else None
+        dbeta = torch.empty(N, dtype=grad_dtype, device=dev) if want_dbeta else None
+        need = qlora_norm_bwd_workspace_bytes(M, N) if want_dgamma or want_dbeta else 0
+        workspace = _bytes(workspace, need, dev)
+        st = _lib.load().qlora_norm_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(x), ldx,
+                                        _FLOATS[x.dtype], M, N, norm, _at(gamma), w_dtype, eps,
+                                        _at(stats), _at(dX), N, _FLOATS[dx_dtype], _at(dgamma),
+                                        _at(dbeta), _FLOATS[grad_dtype], _at(workspace),
+                                        workspace.numel(), _here(dev))
+    _lib.check(st, "qlora_norm_bwd")
+    return dX, dgamma, dbeta
+
+
+def _top(logits, top_ids, top_logits):
+    M, V = _two_dims(logits, "logits")
+    k = _two_dims(top_ids, "top_ids")[1]
+    dev = logits.device
+    ldz = _matrix(logits, "logits", (M, V), dev)
+    ids_dtype = _indexes(top_ids, "top_ids", (M, k), dev)
+    _need(top_logits, "top_logits", (M, k), tuple(_FLOATS), dev)
+    return (_at(logits), ldz, _FLOATS[logits.dtype], M, V, _at(top_ids), ids_dtype,
+            _at(top_logits), _FLOATS[top_logits.dtype], k)
+
+
+def qlora_distill_fwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: torch.Tensor,
+                      temperature: float = 1.0, loss: torch.Tensor | None = None,
+                      stats_out: torch.Tensor | None = None,
+                      workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Loss of each row (fp32 [M]): the divergence of softmax(logits / T) from
+    the teacher's softmax over its top logits, times T^2. logits [M,V] fp32 or
+    bf16; top_ids [M,k] int32 or int64 (an id outside of [0, V) is no entry),
+    top_logits [M,k]. stats_out: fp32 [2,M] for the backward."""
+    heads = _top(logits, top_ids, top_logits)
+    M, V, dev = heads[3], heads[4], logits.device
+    _need(stats_out, "stats_out", (2, M), torch.float32, dev)
+    _need(loss, "loss", (M,), torch.float32, dev)
+    with _place(logits, stream):
+        if loss is None:
+            loss = torch.empty(M, dtype=torch.float32, device=dev)
+        workspace = _bytes(workspace, qlora_distill_fwd_workspace_bytes(M, V), dev)
+        st = _lib.load().qlora_distill_fwd(*heads, temperature, _at(loss), _at(stats_out),
+                                           _at(workspace), workspace.numel(), _here(dev))
+    _lib.check(st, "qlora_distill_fwd")
+    return loss
+
+
+def qlora_distill_bwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: torch.Tensor,
+                      dloss: torch.Tensor, stats: torch.Tensor, temperature: float = 1.0,
+                      dlogits: torch.Tensor | None = None, grad_dtype=None,
+                      stream=None) -> torch.Tensor:
+    """Gradient of the rows' losses with respect to the logits, [M,V] (the
+    logits' dtype by default), for the rows' gradients dloss (fp32 [M]) and the
+    forward's stats_out."""
+    heads = _top(logits, top_ids, top_logits)
+    M, V, dev = heads[3], heads[4], logits.device
+    _need(stats, "stats", (2, M), torch.float32, dev)
+    _need(dloss, "dloss", (M,), torch.float32, dev)
+    with _place(logits, stream):
+        if dlogits is None:
+            dtype = logits.dtype if grad_dtype is None else grad_dtype
+            dlogits = torch.empty((M, V), dtype=dtype, device=dev)
+        ldg = _matrix(dlogits, "dlogits", (M, V), dev)
+        st = _lib.load().qlora_distill_bwd(*heads, temperature, _at(stats), _at(dloss),
+                                           _at(dlogits), ldg, _FLOATS[dlogits.dtype], _here(dev))
+    _lib.check(st, "qlora_distill_bwd")
+    return dlogits

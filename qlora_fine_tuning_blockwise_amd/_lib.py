@@ -16,6 +16,10 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "qlora_amd.h")
 OK = 0
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_I32 = 2
+DTYPE_I64 = 3
+NORM_LAYER = 0
+NORM_RMS = 1
 LAYOUT_ROWS = 0
 LAYOUT_KSLAB32 = 1
 DQ_INT8 = 0
@@ -62,6 +66,17 @@ SIGNATURES = {
     "qlora_gemm_bf16_nt": (INT, [P, I64, P, I64, INT, P, P, I64, I64, I64, INT, P, INT, P]),
     "qlora_merge_lora": (INT, [DESC, P, I64, I64, P, P, INT, FLT, P, P, SZ, P]),
     "qlora_adamw_step": (INT, [P, P, INT, P, P, P, I64, DBL, DBL, DBL, DBL, DBL, I64, P]),
+    "qlora_embed_fwd": (INT, [P, I64, INT, I64, I64, P, INT, I64, FLT, P, I64, INT, P]),
+    "qlora_embed_bwd_workspace_bytes": (SZ, [I64, I64]),
+    "qlora_embed_bwd": (INT, [P, I64, INT, P, INT, I64, I64, I64, FLT, P, INT, INT, P, SZ, P]),
+    "qlora_norm_fwd": (INT, [P, I64, INT, I64, I64, INT, P, P, INT, FLT, P, I64, INT, P, P]),
+    "qlora_norm_bwd_workspace_bytes": (SZ, [I64, I64]),
+    "qlora_norm_bwd": (INT, [P, I64, INT, P, I64, INT, I64, I64, INT, P, INT, FLT, P, P, I64, INT,
+                             P, P, INT, P, SZ, P]),
+    "qlora_distill_fwd_workspace_bytes": (SZ, [I64, I64]),
+    "qlora_distill_fwd": (INT, [P, I64, INT, I64, I64, P, INT, P, INT, INT, FLT, P, P, P, SZ, P]),
+    "qlora_distill_bwd": (INT, [P, I64, INT, I64, I64, P, INT, P, INT, INT, FLT, P, P, P, I64, INT,
+                                P]),
 }
 
 _lib = None

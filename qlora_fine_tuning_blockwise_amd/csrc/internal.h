@@ -210,4 +210,43 @@ hipError_t launch_colred_finalize2(const float* part0, int64_t C0, bool transpos
                                    bool out_bf16, hipStream_t st);
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t st);
 
+// ------------------------------------------------------------ row operators
+// Matrices are row-major with a row stride in elements and need only their
+// elements' alignment; sizes are pre-validated and not zero unless noted.
+hipError_t launch_embed_fwd(const void* W, int64_t ldw, bool w_bf16, int64_t V, int64_t D,
+                            const void* ids, bool ids64, int64_t M, float scale, void* out,
+                            int64_t ldo, bool out_bf16, hipStream_t st);
+// dW [V, D] contiguous, 16-byte aligned. sorted: 4 * round_up(M, 64) int32;
+// part: ceil(M / embed_tile(M)) * 2 * round_up(D, 8) floats. M = 0 is allowed.
+int embed_tile(int64_t M);
+hipError_t launch_embed_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void* ids, bool ids64,
+                            int64_t M, int64_t V, int64_t D, float scale, void* dW, bool grad_bf16,
+                            bool accumulate, int32_t* sorted, float* part, hipStream_t st);
+
+// center: layer norm, else the form without the mean. gamma, beta, stats may
+// be NULL.
+hipError_t launch_norm_fwd(const void* x, int64_t ldx, bool x_bf16, int64_t M, int64_t N,
+                           bool center, const void* gamma, const void* beta, bool w_bf16,
+                           float eps, void* y, int64_t ldy, bool y_bf16, float* stats,
+                           hipStream_t st);
+// part: norm_bwd_parts(M, N) * 2 * round_up(N, 8) floats (with dgamma or
+// dbeta). dX, dgamma, dbeta, gamma, stats may be NULL.
+int norm_bwd_parts(int64_t M, int64_t N);
+hipError_t launch_norm_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void* x, int64_t ldx,
+                           bool x_bf16, int64_t M, int64_t N, bool center, const void* gamma,
+                           bool w_bf16, float eps, const float* stats, void* dX, int64_t lddx,
+                           bool dx_bf16, void* dgamma, void* dbeta, bool grad_bf16, float* part,
+                           hipStream_t st);
+
+// part: with distill_splits(M, V) = s > 1, M * s * 2 floats. stats of the
+// forward may be NULL.
+int distill_splits(int64_t M, int64_t V);
+hipError_t launch_distill_fwd(const void* z, int64_t ldz, bool z_bf16, int64_t M, int64_t V,
+                              const void* ids, bool ids64, const void* t, bool t_bf16, int k,
+                              float T, float* loss, float* stats, float* part, hipStream_t st);
+hipError_t launch_distill_bwd(const void* z, int64_t ldz, bool z_bf16, int64_t M, int64_t V,
+                              const void* ids, bool ids64, const void* t, bool t_bf16, int k,
+                              float T, const float* stats, const float* dloss, void* dz,
+                              int64_t ldg, bool g_bf16, hipStream_t st);
+
 }  // namespace qlora
