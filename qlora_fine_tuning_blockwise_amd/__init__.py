@@ -368,6 +368,7 @@ def qlora_adamw_step(param: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Ten
 # ------------------------------------------------------------ row operators
 _FLOATS = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
 _INDEXES = {torch.int32: _lib.DTYPE_I32, torch.int64: _lib.DTYPE_I64}
+_F32 = (torch.float32,)
 _HERE = contextlib.nullcontext()
 
 
@@ -387,7 +388,15 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
+# The handle of a device's current stream. torch's own short way to it (0.1 us
+# against 1.9 us for current_stream(), of about 8 us for a whole small call)
+# is taken where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _here(dev):
+    if _raw_stream is not None:
+        return _raw_stream(dev.index)
     return torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -401,17 +410,34 @@ def _matrix(t, name, shape, device) -> int:
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
     M, N = shape
-    if N > 1 and M > 0 and t.stride(1) != 1:
+    ld, step = t.stride()
+    if step != 1 and N > 1 and M > 0:
         raise ValueError(f"{name}: rows must be contiguous")
     if M <= 1:
         return max(N, 1)
-    if t.stride(0) < N:
-        raise ValueError(f"{name}: row stride {t.stride(0)} below the width {N}")
-    return t.stride(0)
+    if ld < N:
+        raise ValueError(f"{name}: row stride {ld} below the width {N}")
+    return ld
+
+
+def _vector(t, name, shape, dtypes, device):
+    """_need for an argument that is there, without its conversions: on a
+    small call the checks are a part of its time."""
+    if t.shape != shape or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+        _need(t, name, shape, tuple(dtypes), device)
+
+
+def _new(like, M, N, dtype):
+    """A matrix on like's device, in its type by default, and its row stride."""
+    if dtype is None:
+        dtype = like.dtype
+    elif dtype not in _FLOATS:
+        raise ValueError(f"dtype {dtype}, expected fp32 or bf16")
+    return like.new_empty((M, N), dtype=dtype), max(N, 1)
 
 
 def _indexes(t, name, shape, device) -> int:
-    _need(t, name, shape, tuple(_INDEXES), device)
+    _vector(t, name, shape, _INDEXES, device)
     return _INDEXES[t.dtype]
 
 
@@ -454,8 +480,9 @@ def qlora_embed_fwd(W: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
     ids_dtype = _indexes(ids, "ids", (M,), dev)
     with _place(W, stream):
         if out is None:
-            out = torch.empty((M, D), dtype=W.dtype if out_dtype is None else out_dtype, device=dev)
-        ldo = _matrix(out, "out", (M, D), dev)
+            out, ldo = _new(W, M, D, out_dtype)
+        else:
+            ldo = _matrix(out, "out", (M, D), dev)
         st = _lib.load().qlora_embed_fwd(_at(W), ldw, _FLOATS[W.dtype], V, D, _at(ids), ids_dtype,
                                          M, scale, _at(out), ldo, _FLOATS[out.dtype], _here(dev))
     _lib.check(st, "qlora_embed_fwd")
@@ -478,8 +505,7 @@ def qlora_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 
     _need(dW, "dW", (V, D), tuple(_FLOATS), dev)
     with _place(dY, stream):
         if dW is None:
-            dW = torch.empty((V, D), dtype=grad_dtype, device=dev)
-            _need(dW, "dW", (V, D), tuple(_FLOATS), dev)
+            dW, _ = _new(dY, V, D, grad_dtype)
         workspace = _bytes(workspace, qlora_embed_bwd_workspace_bytes(M, D), dev)
         st = _lib.load().qlora_embed_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(ids), ids_dtype, M, V,
                                          D, scale, _at(dW), _FLOATS[dW.dtype], int(accumulate),
@@ -494,7 +520,7 @@ def _norm_vectors(N, dev, *named):
     for t, name in named:
         if t is None:
             continue
-        _need(t, name, (N,), tuple(_FLOATS), dev)
+        _vector(t, name, (N,), _FLOATS, dev)
         if code is not None and code != _FLOATS[t.dtype]:
             raise ValueError(f"{name}: the affine vectors must share one dtype")
         code = _FLOATS[t.dtype]
@@ -512,11 +538,13 @@ def qlora_norm_fwd(x: torch.Tensor, gamma: torch.Tensor | None = None,
     dev = x.device
     ldx = _matrix(x, "x", (M, N), dev)
     w_dtype = _norm_vectors(N, dev, (gamma, "gamma"), (beta, "beta"))
-    _need(stats_out, "stats_out", (2, M), torch.float32, dev)
+    if stats_out is not None:
+        _vector(stats_out, "stats_out", (2, M), _F32, dev)
     with _place(x, stream):
         if y is None:
-            y = torch.empty((M, N), dtype=x.dtype if y_dtype is None else y_dtype, device=dev)
-        ldy = _matrix(y, "y", (M, N), dev)
+            y, ldy = _new(x, M, N, y_dtype)
+        else:
+            ldy = _matrix(y, "y", (M, N), dev)
         st = _lib.load().qlora_norm_fwd(_at(x), ldx, _FLOATS[x.dtype], M, N, norm, _at(gamma),
                                         _at(beta), w_dtype, eps, _at(y), ldy, _FLOATS[y.dtype],
                                         _at(stats_out), _here(dev))
@@ -537,7 +565,8 @@ def qlora_norm_bwd(dY: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None
     ldx = _matrix(x, "x", (M, N), dev)
     ldy = _matrix(dY, "dY", (M, N), dev)
     w_dtype = _norm_vectors(N, dev, (gamma, "gamma"))
-    _need(stats, "stats", (2, M), torch.float32, dev)
+    if stats is not None:
+        _vector(stats, "stats", (2, M), _F32, dev)
     dx_dtype = x.dtype if dx_dtype is None else dx_dtype
     if dx_dtype not in _FLOATS or grad_dtype not in _FLOATS:
         raise ValueError("qlora_norm_bwd: gradients are fp32 or bf16")
@@ -546,12 +575,13 @@ def qlora_norm_bwd(dY: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None
         dgamma = torch.empty(N, dtype=grad_dtype, device=dev) if want_dgamma else None
         dbeta = torch.empty(N, dtype=grad_dtype, device=dev) if want_dbeta else None
         need = qlora_norm_bwd_workspace_bytes(M, N) if want_dgamma or want_dbeta else 0
-        workspace = _bytes(workspace, need, dev)
+        if need or workspace is not None:
+            workspace = _bytes(workspace, need, dev)
         st = _lib.load().qlora_norm_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(x), ldx,
                                         _FLOATS[x.dtype], M, N, norm, _at(gamma), w_dtype, eps,
                                         _at(stats), _at(dX), N, _FLOATS[dx_dtype], _at(dgamma),
                                         _at(dbeta), _FLOATS[grad_dtype], _at(workspace),
-                                        workspace.numel(), _here(dev))
+                                        0 if workspace is None else workspace.numel(), _here(dev))
     _lib.check(st, "qlora_norm_bwd")
     return dX, dgamma, dbeta
 
@@ -562,7 +592,7 @@ def _top(logits, top_ids, top_logits):
     dev = logits.device
     ldz = _matrix(logits, "logits", (M, V), dev)
     ids_dtype = _indexes(top_ids, "top_ids", (M, k), dev)
-    _need(top_logits, "top_logits", (M, k), tuple(_FLOATS), dev)
+    _vector(top_logits, "top_logits", (M, k), _FLOATS, dev)
     return (_at(logits), ldz, _FLOATS[logits.dtype], M, V, _at(top_ids), ids_dtype,
             _at(top_logits), _FLOATS[top_logits.dtype], k)
 
@@ -577,14 +607,18 @@ def qlora_distill_fwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: t
     top_logits [M,k]. stats_out: fp32 [2,M] for the backward."""
     heads = _top(logits, top_ids, top_logits)
     M, V, dev = heads[3], heads[4], logits.device
-    _need(stats_out, "stats_out", (2, M), torch.float32, dev)
+    if stats_out is not None:
+        _vector(stats_out, "stats_out", (2, M), _F32, dev)
     _need(loss, "loss", (M,), torch.float32, dev)
     with _place(logits, stream):
         if loss is None:
             loss = torch.empty(M, dtype=torch.float32, device=dev)
-        workspace = _bytes(workspace, qlora_distill_fwd_workspace_bytes(M, V), dev)
+        need = qlora_distill_fwd_workspace_bytes(M, V)
+        if need or workspace is not None:
+            workspace = _bytes(workspace, need, dev)
         st = _lib.load().qlora_distill_fwd(*heads, temperature, _at(loss), _at(stats_out),
-                                           _at(workspace), workspace.numel(), _here(dev))
+                                           _at(workspace),
+                                           0 if workspace is None else workspace.numel(), _here(dev))
     _lib.check(st, "qlora_distill_fwd")
     return loss
 
@@ -598,13 +632,13 @@ def qlora_distill_bwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: t
     forward's stats_out."""
     heads = _top(logits, top_ids, top_logits)
     M, V, dev = heads[3], heads[4], logits.device
-    _need(stats, "stats", (2, M), torch.float32, dev)
-    _need(dloss, "dloss", (M,), torch.float32, dev)
+    _vector(stats, "stats", (2, M), _F32, dev)
+    _vector(dloss, "dloss", (M,), _F32, dev)
     with _place(logits, stream):
         if dlogits is None:
-            dtype = logits.dtype if grad_dtype is None else grad_dtype
-            dlogits = torch.empty((M, V), dtype=dtype, device=dev)
-        ldg = _matrix(dlogits, "dlogits", (M, V), dev)
+            dlogits, ldg = _new(logits, M, V, grad_dtype)
+        else:
+            ldg = _matrix(dlogits, "dlogits", (M, V), dev)
         st = _lib.load().qlora_distill_bwd(*heads, temperature, _at(stats), _at(dloss),
                                            _at(dlogits), ldg, _FLOATS[dlogits.dtype], _here(dev))
     _lib.check(st, "qlora_distill_bwd")
