@@ -254,8 +254,7 @@ size_t norm_bwd_bytes(int64_t M, int64_t N) {
 }
 
 size_t distill_fwd_bytes(int64_t M, int64_t V) {
-  const int s = M == 0 ? 1 : distill_splits(M, V);
-  return s > 1 ? round_up((size_t)M * s * 2 * sizeof(float)) : 0;
+  return M == 0 ? 0 : round_up((size_t)M * distill_parts(V) * 2 * sizeof(float));
 }
 
 // The checks that both directions of the distillation share.

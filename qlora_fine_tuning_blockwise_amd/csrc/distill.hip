@@ -14,10 +14,13 @@
 // large. The difference z - m is formed before the scaling, so a row of
 // the type's lowest values is a uniform distribution and not a NaN.
 //
-// The forward reads each logit once: a thread keeps a running maximum and the
-// sum of exponentials taken from it, and joins eight or more logits at a
+// The forward reads each logit once: a lane keeps a running maximum and the
+// sum of exponentials taken from it, and joins 32 (bf16) or 16 logits at a
 // time. The backward streams the row and then rewrites the few entries the
-// teacher names.
+// teacher names. Waves work alone (no barriers in the streams): each reads
+// the teacher's entries itself and, in the backward, rewrites those whose
+// logits it has written. The logits pass through once, so they are read and
+// their gradients written with the nontemporal hint.
 #include <type_traits>
 
 #include "rows.h"
@@ -26,6 +29,8 @@ namespace qlora {
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
+constexpr int kFwdRound = 8192;  // logits a workgroup holds at once: 32 a thread
+constexpr int kBwdUnroll = 8;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
@@ -37,39 +42,84 @@ struct Teacher {
   int k;
 };
 
-// The teacher's distribution of one row in LDS: id[j] (-1 where entry j is
-// not live) and p[j]; every thread gets log sum exp((t - top) / T) in `logsum`
-// and the top. Returns whether any entry is live. All threads call it; ends
-// with a barrier.
-__device__ __forceinline__ bool teacher_row(const Teacher& a, int64_t row, int64_t V, float invT,
-                                            int32_t* id, float* p, float* red, int& par,
-                                            float& top, float& logsum) {
-  float m[1] = {-INFINITY};
+// Orders a wave's LDS accesses of different lanes (they are issued in program
+// order; only the compiler must keep it).
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// The teacher's entries of one row in the wave's LDS: id[j] (-1 where entry j
+// is not live) and t[j]. Returns whether any entry is live, the largest live
+// t in `top`. With `logit` the student's logits at the live entries as well,
+// requested before anything waits for the entries' values.
+template <bool ZB>
+__device__ __forceinline__ bool teacher_load(const Teacher& a, int64_t row, int64_t V, int lane,
+                                             int32_t* id, float* t, float& top,
+                                             const elem_t<ZB>* z = nullptr,
+                                             float* logit = nullptr) {
+  constexpr int kBatch = 4;  // entries of a lane whose loads are in flight together
+  float m = -INFINITY;
   bool some = false;
-  for (int j = threadIdx.x; j < a.k; j += kThreads) {
-    const int64_t i = load_index(a.ids, a.ids64, row * a.k + j);
-    const float t = load_any(a.t, a.t_bf16, row * a.k + j);
-    const bool live = i >= 0 && i < V && !(t == -INFINITY);  // a NaN is live and spreads
-    id[j] = live ? (int32_t)i : -1;
-    p[j] = t;
-    some |= live;
-    if (live) m[0] = fmaxf(m[0], t);
+  const int64_t first = row * a.k;
+  for (int j0 = lane; j0 < a.k; j0 += 64 * kBatch) {
+    int64_t i[kBatch];
+    float v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) i[b] = -1, v[b] = 0.0f;
+    if (a.ids64) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (j0 + 64 * b < a.k) i[b] = static_cast<const int64_t*>(a.ids)[first + j0 + 64 * b];
+    } else {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (j0 + 64 * b < a.k) i[b] = static_cast<const int32_t*>(a.ids)[first + j0 + 64 * b];
+    }
+    if (a.t_bf16) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (j0 + 64 * b < a.k) v[b] = load_any(a.t, true, first + j0 + 64 * b);
+    } else {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (j0 + 64 * b < a.k) v[b] = load_any(a.t, false, first + j0 + 64 * b);
+    }
+    float zb[kBatch];
+    if (logit) {
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        zb[b] = i[b] >= 0 && i[b] < V ? load_any(z, ZB, i[b]) : 0.0f;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const bool live = i[b] >= 0 && i[b] < V && !(v[b] == -INFINITY);  // a NaN is live and spreads
+      if (j0 + 64 * b < a.k) {
+        id[j0 + 64 * b] = live ? (int32_t)i[b] : -1;
+        t[j0 + 64 * b] = v[b];
+        if (logit) logit[j0 + 64 * b] = zb[b];
+      }
+      some |= live;
+      if (live) m = fmaxf(m, v[b]);
+    }
   }
-  if (!__syncthreads_or(some)) return false;
-  group_reduce<kThreads, 1>(m, red, kWaves, par, OpMax());
-  top = m[0] == -INFINITY ? 0.0f : m[0];  // every live entry is a NaN
-  float s[1] = {0.0f};
-  for (int j = threadIdx.x; j < a.k; j += kThreads) {
-    const float e = id[j] < 0 ? 0.0f : expf((p[j] - top) * invT);
-    s[0] += e;
-  }
-  group_reduce<kThreads, 1>(s, red, kWaves, par, OpSum());
-  logsum = logf(s[0]);
+  if (!__ballot(some)) return false;
+  m = wave_reduce(m, OpMax());
+  top = m == -INFINITY ? 0.0f : m;  // every live entry is a NaN
   return true;
 }
 
-// Running maximum and sum of a thread joined with another pair: sums are
-// taken from max(m, the lowest finite), so a part of -inf alone adds 0.
+// log sum over the live entries of exp((t - top) / T).
+__device__ __forceinline__ float teacher_logsum(int k, int lane, const int32_t* id, const float* t,
+                                                float top, float invT) {
+  float s = 0.0f;
+  for (int j = lane; j < k; j += 64) s += id[j] < 0 ? 0.0f : expf((t[j] - top) * invT);
+  return logf(wave_reduce(s, OpSum()));
+}
+
+// A maximum and the sum of exponentials taken from it; from 0 where the
+// maximum is -inf, so that a part of -inf alone adds 0.
 struct MaxSum {
   float m, s;
 };
@@ -84,26 +134,83 @@ __device__ __forceinline__ MaxSum join(MaxSum a, MaxSum b, float c) {
   return r;
 }
 
-__device__ __forceinline__ void take(MaxSum& a, const float (&v)[8], int n, float c) {
-  float m = a.m;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) m = fmaxf(m, e < n ? v[e] : -INFINITY);
-  const float base = finite_base(m);
-  float s = a.s * exp2_fast((a.m - base) * c);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) s += e < n ? exp2_fast((v[e] - base) * c) : 0.0f;
-  a.m = m;
-  a.s = s;
+__device__ __forceinline__ MaxSum wave_join(MaxSum a, float c) {
+  MaxSum r;
+  r.m = wave_reduce(a.m, OpMax());
+  r.s = wave_reduce(a.s * exp2_fast((a.m - finite_base(r.m)) * c), OpSum());
+  return r;
 }
 
-// The pair of the whole workgroup, in every thread.
-__device__ __forceinline__ MaxSum group_join(MaxSum a, float c, float* red, int& par) {
-  float m[1] = {a.m};
-  group_reduce<kThreads, 1>(m, red, kWaves, par, OpMax());
-  const float base = finite_base(m[0]);
-  float s[1] = {a.s * exp2_fast((a.m - base) * c)};
-  group_reduce<kThreads, 1>(s, red, kWaves, par, OpSum());
-  return MaxSum{m[0], s[0]};
+// U vectors of logits into the pair. -inf adds nothing: it fills the places
+// of a vector that lie outside of the row.
+template <bool ZB, int E, int U>
+__device__ __forceinline__ void take(MaxSum& a, const Vec<ZB, E> (&q)[U], float c) {
+  float v[U][E];
+  float m = a.m;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    to_float<ZB, E>(q[u], v[u]);
+#pragma unroll
+    for (int e = 0; e < E; ++e) m = fmaxf(m, v[u][e]);
+  }
+  const float base = finite_base(m);
+  float s[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) s[u] = 0.0f;
+  float fix = 1.0f;
+  if (__builtin_fabsf(base) <= 0x1p64f) {
+    // (v - base) c as one operation: v c - base c, whose second term is rounded
+    // alike for all of them; the rounding is taken out of the sum.
+    const float bc = base * c;
+    fix = exp2_fast(-fmaf(base, c, -bc));
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[u] += exp2_fast(fmaf(v[u][e], c, -bc));
+  } else {  // base c may not be finite
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[u] += exp2_fast((v[u][e] - base) * c);
+  }
+#pragma unroll
+  for (int u = 1; u < U; ++u) s[0] += s[u];
+  a.s = fmaf(a.s, exp2_fast((a.m - base) * c), fix * s[0]);
+  a.m = m;
+}
+
+// How a row is dealt out. Its logits are taken from `origin` <= 0 on, the
+// place of the 128-byte line in which the row begins, so that every access of
+// a wave but a row's first and last covers whole lines; a piece is a run of
+// rounds, and in a round thread i of the workgroup holds the vectors at
+// (u kThreads + i) E, u < U.
+template <bool kBf16>
+__device__ __forceinline__ int row_origin(const void* row) {
+  constexpr uintptr_t kSize = kBf16 ? 2 : 4;
+  return -(int)((reinterpret_cast<uintptr_t>(row) & 127) / kSize);
+}
+
+template <bool ZB, int E, int U>
+__device__ __forceinline__ void load_round(const elem_t<ZB>* z, int64_t at, Vec<ZB, E> (&q)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) q[u] = load_vec<ZB, E, true>(z + at + u * kThreads * E);
+}
+
+// A round that leaves [0, V): the logits [first, n) of each vector.
+template <bool ZB, int E, int U>
+__device__ __forceinline__ void load_ends(const elem_t<ZB>* z, int64_t at, int64_t V,
+                                          Vec<ZB, E> (&q)[U], int (&first)[U], int (&n)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int64_t v = at + u * kThreads * E;
+    n[u] = count_below<E>(v, V);
+    first[u] = v >= 0 ? 0 : v <= -E ? E : (int)-v;
+    q[u] = first[u] == 0 && n[u] == E ? load_vec<ZB, E, true>(z + v) : fill_vec<ZB, E, kNegInf>();
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (first[u] < n[u] && (first[u] > 0 || n[u] < E))
+      q[u] = load_part<ZB, E, kNegInf>(z + at + u * kThreads * E, n[u], first[u]);
 }
 
 struct DistillFwd {
@@ -113,28 +220,27 @@ struct DistillFwd {
   float T, invT;
   float* loss;
   float* stats;
-  MaxSum* part;  // [M][splits]
+  MaxSum* part;  // [M][splits][kWaves]
   int splits;
-  int64_t per;  // logits of a split
+  int rounds;  // of a split
 };
 
-// loss and statistics of a row from its joined pair.
-template <bool ZB>
-__device__ __forceinline__ void finish_row(const DistillFwd& a, int64_t row, MaxSum r,
-                                           const int32_t* id, const float* t, float top,
-                                           float logsum, float* red, int& par) {
+// loss and statistics of a row from its joined pair, by one wave.
+__device__ __forceinline__ void finish_row(const DistillFwd& a, int64_t row, int lane, MaxSum r,
+                                           const int32_t* id, const float* t, const float* logit,
+                                           float top) {
   const float L = logf(r.s);
-  float s[1] = {0.0f};
-  for (int j = threadIdx.x; j < a.teacher.k; j += kThreads) {
+  const float logsum = teacher_logsum(a.teacher.k, lane, id, t, top, a.invT);
+  float s = 0.0f;
+  for (int j = lane; j < a.teacher.k; j += 64) {
     if (id[j] < 0) continue;
     const float logp = (t[j] - top) * a.invT - logsum;
     const float p = expf(logp);
-    const float z = load_any(a.z, ZB, row * a.ldz + id[j]);
-    if (p != 0.0f) s[0] += p * (logp - ((z - r.m) * a.invT - L));
+    if (p != 0.0f) s += p * (logp - ((logit[j] - r.m) * a.invT - L));
   }
-  group_reduce<kThreads, 1>(s, red, kWaves, par, OpSum());
-  if (threadIdx.x == 0) {
-    a.loss[row] = a.T * a.T * s[0];
+  s = wave_reduce(s, OpSum());
+  if (lane == 0) {
+    a.loss[row] = a.T * a.T * s;
     if (a.stats) {
       a.stats[row] = r.m;
       a.stats[a.M + row] = L;
@@ -142,76 +248,83 @@ __device__ __forceinline__ void finish_row(const DistillFwd& a, int64_t row, Max
   }
 }
 
-// Workgroup (row, split): its part of the row. With one split it also
-// finishes the row; otherwise distill_finish_kernel does.
+__device__ __forceinline__ void empty_row(const DistillFwd& a, int64_t row) {
+  a.loss[row] = 0.0f;
+  if (a.stats) a.stats[row] = a.stats[a.M + row] = 0.0f;
+}
+
+// Workgroup (row, split): its part of the row. With one split its first wave
+// also finishes the row; otherwise distill_finish_kernel does.
 template <bool ZB>
 __global__ __launch_bounds__(kThreads) void distill_fwd_kernel(DistillFwd a) {
-  extern __shared__ float lds[];  // id[k], t[k]
-  __shared__ float red[2 * kWaves];
-  int32_t* id = reinterpret_cast<int32_t*>(lds);
-  float* t = lds + a.teacher.k;
-  int par = 0;
+  constexpr int E = ZB ? 8 : 4, U = kFwdRound / (kThreads * E);
+  extern __shared__ float lds[];  // of each wave: id[k], t[k], the logits at the ids
+  __shared__ MaxSum pair[kWaves];
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  int32_t* id = reinterpret_cast<int32_t*>(lds) + wave * 3 * a.teacher.k;
+  float* t = reinterpret_cast<float*>(id) + a.teacher.k;
+  float* logit = t + a.teacher.k;
   const float c = a.invT * kLog2e;
   for (int64_t item = blockIdx.x; item < a.M * a.splits; item += gridDim.x) {
     const int64_t row = item / a.splits;
-    const int split = (int)(item % a.splits);
-    float top = 0.0f, logsum = 0.0f;
-    if (!teacher_row(a.teacher, row, a.V, a.invT, id, t, red, par, top, logsum)) {
-      if (threadIdx.x == 0 && split == 0) {
-        a.loss[row] = 0.0f;
-        if (a.stats) a.stats[row] = a.stats[a.M + row] = 0.0f;
-      }
+    const int split = (int)(item - row * a.splits);
+    float top = 0.0f;
+    const elem_t<ZB>* z = static_cast<const elem_t<ZB>*>(a.z) + row * a.ldz;
+    // every wave finds the same answer: the barriers below are reached by all
+    if (!teacher_load<ZB>(a.teacher, row, a.V, lane, id, t, top, z,
+                          a.splits == 1 && wave == 0 ? logit : nullptr)) {
+      if (threadIdx.x == 0 && split == 0) empty_row(a, row);
       continue;
     }
-    const elem_t<ZB>* z = static_cast<const elem_t<ZB>*>(a.z) + row * a.ldz;
-    const int64_t from = split * a.per, to = from + a.per < a.V ? from + a.per : a.V;
+    const int64_t base = row_origin<ZB>(z) + (int64_t)split * a.rounds * kFwdRound;
     MaxSum r{-INFINITY, 0.0f};
-    constexpr int U = 4;
-    for (int64_t v0 = from + threadIdx.x * 8; v0 < to; v0 += U * kThreads * 8) {
-      Row8<ZB> q[U];
-      int n[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t left = to - (v0 + u * kThreads * 8);
-        n[u] = left >= 8 ? 8 : left < 0 ? 0 : (int)left;
-        q[u] = zero8<ZB>();
-        if (n[u] == 8)
-          q[u] = load8<ZB>(z + v0 + u * kThreads * 8);
-        else if (n[u] > 0)
-          q[u] = load8_part<ZB>(z + v0 + u * kThreads * 8, n[u]);
+    const auto load = [&](int i, Vec<ZB, E>(&q)[U]) {
+      const int64_t at = base + (int64_t)i * kFwdRound;
+      if (at >= 0 && at + kFwdRound <= a.V) {
+        load_round<ZB, E>(z, at + threadIdx.x * E, q);
+      } else {
+        int first[U], n[U];
+        load_ends<ZB, E>(z, at + threadIdx.x * E, a.V, q, first, n);
       }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        float v[8];
-        to_float<ZB>(q[u], v);
-        if (n[u] > 0) take(r, v, n[u], c);
-      }
+    };
+    Vec<ZB, E> q[U];
+    for (int i = 0; i < a.rounds; ++i) {
+      load(i, q);
+      take<ZB, E, U>(r, q, c);
     }
-    r = group_join(r, c, red, par);
-    if (a.splits == 1)
-      finish_row<ZB>(a, row, r, id, t, top, logsum, red, par);
-    else if (threadIdx.x == 0)
-      a.part[item] = r;
-    __syncthreads();  // id and t are written anew for the next item
+    r = wave_join(r, c);
+    if (a.splits > 1) {
+      if (lane == 0) a.part[item * kWaves + wave] = r;
+      continue;
+    }
+    if (lane == 0) pair[wave] = r;
+    __syncthreads();
+    if (wave == 0) {
+      r = pair[0];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) r = join(r, pair[w], c);
+      finish_row(a, row, lane, r, id, t, logit, top);
+    }
+    __syncthreads();  // `pair` is written anew for the next item
   }
 }
 
 template <bool ZB>
-__global__ __launch_bounds__(kThreads) void distill_finish_kernel(DistillFwd a) {
+__global__ __launch_bounds__(64) void distill_finish_kernel(DistillFwd a) {
   extern __shared__ float lds[];
-  __shared__ float red[2 * kWaves];
+  const int lane = threadIdx.x;
   int32_t* id = reinterpret_cast<int32_t*>(lds);
-  float* t = lds + a.teacher.k;
-  int par = 0;
+  float *t = lds + a.teacher.k, *logit = t + a.teacher.k;
   const float c = a.invT * kLog2e;
+  const int parts = a.splits * kWaves;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
-    float top = 0.0f, logsum = 0.0f;
-    if (!teacher_row(a.teacher, row, a.V, a.invT, id, t, red, par, top, logsum)) continue;
-    MaxSum r{-INFINITY, 0.0f};
-    for (int i = threadIdx.x; i < a.splits; i += kThreads) r = join(r, a.part[row * a.splits + i], c);
-    r = group_join(r, c, red, par);
-    finish_row<ZB>(a, row, r, id, t, top, logsum, red, par);
-    __syncthreads();
+    const elem_t<ZB>* z = static_cast<const elem_t<ZB>*>(a.z) + row * a.ldz;
+    // an empty row's parts were not written; they are not used
+    MaxSum r = lane < parts ? a.part[row * parts + lane] : MaxSum{-INFINITY, 0.0f};
+    float top = 0.0f;
+    if (!teacher_load<ZB>(a.teacher, row, a.V, lane, id, t, top, z, logit)) continue;
+    for (int i = lane + 64; i < parts; i += 64) r = join(r, a.part[row * parts + i], c);
+    finish_row(a, row, lane, wave_join(r, c), id, t, logit, top);
   }
 }
 
@@ -225,114 +338,159 @@ struct DistillBwd {
   void* dz;
   int64_t ldg;
   int chunks;
-  int64_t per;  // logits of a chunk, a multiple of eight
 };
 
+// Workgroup (row, chunk): one round of the row. Rounds of 32 KB a workgroup,
+// all of it in flight at once, measured best: 2048 x 128000 bf16 in 177 us
+// (5.9 TB/s of the 6.5 TB/s that a copy in the same pattern reaches), 193 us
+// with two rounds a workgroup, 190 us with rounds of half the size; without
+// the nontemporal hint 200 us, and on rows that do not begin on a line (V =
+// 128008) 208 us where the rounds begin with the row instead of its line.
 template <bool ZB, bool GB>
 __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillBwd a) {
-  extern __shared__ float lds[];
-  __shared__ float red[2 * kWaves];
-  int32_t* id = reinterpret_cast<int32_t*>(lds);
-  float* p = lds + a.teacher.k;
-  int par = 0;
+  constexpr int E = ZB && GB ? 8 : 4, U = kBwdUnroll, kRound = U * kThreads * E;
+  extern __shared__ float lds[];  // of each wave: id[k], t[k], then its own entries' id and p
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int k = a.teacher.k;
+  int32_t* id = reinterpret_cast<int32_t*>(lds) + wave * 2 * k;
+  float* t = reinterpret_cast<float*>(id) + k;
   for (int64_t item = blockIdx.x; item < a.M * a.chunks; item += gridDim.x) {
     const int64_t row = item / a.chunks;
-    const int chunk = (int)(item % a.chunks);
-    const int64_t from = chunk * a.per, to = from + a.per < a.V ? from + a.per : a.V;
+    const int chunk = (int)(item - row * a.chunks);
     const elem_t<ZB>* z = static_cast<const elem_t<ZB>*>(a.z) + row * a.ldz;
     elem_t<GB>* g = static_cast<elem_t<GB>*>(a.dz) + row * a.ldg;
     const float dl = a.dloss[row];
-    float top = 0.0f, logsum = 0.0f;
-    // dl is the row's: all threads take the same side
-    if (dl == 0.0f || !teacher_row(a.teacher, row, a.V, a.invT, id, p, red, par, top, logsum)) {
-      const float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-      for (int64_t v0 = from + threadIdx.x * 8; v0 < to; v0 += kThreads * 8) {
-        if (to - v0 >= 8)
-          store8<GB>(g + v0, v);
-        else
-          store8_part<GB>(g + v0, v, (int)(to - v0));
+    float top = 0.0f;
+    const int64_t begin = row_origin<GB>(g) + (int64_t)chunk * kRound;
+    const int64_t at = begin + threadIdx.x * E;
+    if (dl == 0.0f || !teacher_load<ZB>(a.teacher, row, a.V, lane, id, t, top)) {
+      float v[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t i = at + u * kThreads * E;
+        const int n = count_below<E>(i, a.V);
+        if (i >= 0 && n == E)
+          store_vec<GB, E, true>(g + i, v);
+        else if (i > -E && n > 0)
+          store_part<GB, E>(g + i, v, n, i < 0 ? (int)-i : 0);
       }
-      __syncthreads();
       continue;
     }
     const float scale = dl * a.T;
     const float m = a.stats[row], L = a.stats[a.M + row];
-    for (int j = threadIdx.x; j < a.teacher.k; j += kThreads)
-      p[j] = id[j] < 0 ? 0.0f : expf((p[j] - top) * a.invT - logsum);
-    constexpr int U = 4;
-    for (int64_t v0 = from + threadIdx.x * 8; v0 < to; v0 += U * kThreads * 8) {
-      Row8<ZB> q[U];
-      int n[U];
+    Vec<ZB, E> q[U];
+    if (begin >= 0 && begin + kRound <= a.V) {
+      load_round<ZB, E>(z, at, q);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t left = to - (v0 + u * kThreads * 8);
-        n[u] = left >= 8 ? 8 : left < 0 ? 0 : (int)left;
-        q[u] = zero8<ZB>();
-        if (n[u] == 8)
-          q[u] = load8<ZB>(z + v0 + u * kThreads * 8);
-        else if (n[u] > 0)
-          q[u] = load8_part<ZB>(z + v0 + u * kThreads * 8, n[u]);
+        float v[E];
+        to_float<ZB, E>(q[u], v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = scale * exp2_fast(fmaf(v[e] - m, a.invT, -L) * kLog2e);
+        store_vec<GB, E, true>(g + at + u * kThreads * E, v);
       }
+    } else {
+      int first[U], n[U];
+      load_ends<ZB, E>(z, at, a.V, q, first, n);
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        float v[8];
-        to_float<ZB>(q[u], v);
+        float v[E];
+        to_float<ZB, E>(q[u], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = scale * exp2_fast(fmaf(v[e] - m, a.invT, -L) * kLog2e);
-        if (n[u] == 8)
-          store8<GB>(g + v0 + u * kThreads * 8, v);
-        else if (n[u] > 0)
-          store8_part<GB>(g + v0 + u * kThreads * 8, v, n[u]);
+        for (int e = 0; e < E; ++e) v[e] = scale * exp2_fast(fmaf(v[e] - m, a.invT, -L) * kLog2e);
+        if (first[u] == 0 && n[u] == E)
+          store_vec<GB, E, true>(g + at + u * kThreads * E, v);
+        else if (first[u] < n[u])
+          store_part<GB, E>(g + at + u * kThreads * E, v, n[u], first[u]);
       }
     }
-    __syncthreads();  // the row's values are written before the teacher's entries are, and p is whole
-    for (int j = threadIdx.x; j < a.teacher.k; j += kThreads) {
+    const float logsum = teacher_logsum(k, lane, id, t, top, a.invT);
+    // The entries whose logits this wave has written, moved to the front.
+    int own = 0;
+    for (int j0 = 0; j0 < k; j0 += 64) {
+      const int j = j0 + lane;
+      const int32_t v = j < k ? id[j] : -1;
+      const float p = v < 0 ? 0.0f : expf((t[j] - top) * a.invT - logsum);
+      const bool mine = v >= 0 && v >= begin && v < begin + kRound &&
+                        ((v - begin) / (64 * E)) % kWaves == wave;
+      const uint64_t all = __ballot(mine);
+      wave_sync();  // the reads above come before the writes below, which are not past them
+      if (mine) {
+        const int at = own + __popcll(all & ((1ull << lane) - 1));
+        id[at] = v;
+        t[at] = p;
+      }
+      own += __popcll(all);
+    }
+    wave_sync();  // the list is whole, and the wave's gradients are written before its entries are
+    for (int j = lane; j < own; j += 64) {
       const int32_t v = id[j];
-      if (v < from || v >= to) continue;
       float sum = 0.0f;
       bool again = false;
-      for (int i = 0; i < a.teacher.k; ++i) {
+#pragma unroll 8
+      for (int i = 0; i < own; ++i) {
         const bool same = id[i] == v;
-        sum += same ? p[i] : 0.0f;
+        sum += same ? t[i] : 0.0f;
         again |= same && i < j;
       }
       if (again) continue;  // the first entry of an id writes it
-      const float q = exp2_fast(fmaf(load_any(z, ZB, v) - m, a.invT, -L) * kLog2e);
-      store1<GB>(g + v, scale * (q - sum));
+      const float e = exp2_fast(fmaf(load_any(z, ZB, v) - m, a.invT, -L) * kLog2e);
+      store1<GB>(g + v, scale * (e - sum));
     }
-    __syncthreads();
+    wave_sync();  // the lists are written anew for the next item
   }
 }
 
-int64_t round8(int64_t v) { return (v + 7) / 8 * 8; }
+// A row of V logits as pieces of `rounds` rounds of `round` logits. (A row
+// may begin up to a line after its first piece's place.)
+struct Pieces {
+  int count, rounds;
+};
+
+// Forward: up to eight rounds (64K logits) a row is one workgroup's and the
+// call is one launch; longer rows are cut into pieces of four rounds, which
+// costs the finishing launch but keeps the workgroups short, so that rows
+// without a live entry leave no hole at the end. Measured with bf16 logits,
+// in one launch against pieces of four rounds: 1 x 64000 10.9 against 14.8 us,
+// 2048 x 64000 (fp32) 84.3 against 87.4 us, but 64 x 128000 19.7 against
+// 14.9 us; pieces of two, four and eight rounds on 2048 x 128000 with a
+// quarter of the rows empty: 76, 69 and 71 us.
+Pieces fwd_pieces(int64_t V) {
+  const int64_t n = (V + 63 + kFwdRound - 1) / kFwdRound;
+  if (n <= 8) return {1, (int)n};
+  const int64_t p = (n + 3) / 4;
+  return {(int)p, (int)((n + p - 1) / p)};
+}
 
 }  // namespace
 
-int distill_splits(int64_t M, int64_t V) {
-  const int64_t want = M > 0 ? 1024 / M : 1, most = (V + 8191) / 8192;
-  const int64_t s = want < most ? want : most;
-  return (int)(s < 1 ? 1 : s);
+int distill_parts(int64_t V) {
+  const int s = fwd_pieces(V).count;
+  return s > 1 ? s * kWaves : 0;
 }
 
 hipError_t launch_distill_fwd(const void* z, int64_t ldz, bool z_bf16, int64_t M, int64_t V,
                               const void* ids, bool ids64, const void* t, bool t_bf16, int k,
                               float T, float* loss, float* stats, float* part, hipStream_t st) {
-  const int splits = distill_splits(M, V);
+  const Pieces p = fwd_pieces(V);
+  const int splits = p.count;
   const DistillFwd a{z, ldz, M, V, {ids, t, ids64, t_bf16, k}, T, 1.0f / T, loss, stats,
-                     reinterpret_cast<MaxSum*>(part), splits, round8((V + splits - 1) / splits)};
+                     reinterpret_cast<MaxSum*>(part), splits, p.rounds};
   const int64_t items = M * splits;
   const dim3 grid((unsigned)(items < 65536 ? items : 65536)), rows((unsigned)(M < 65536 ? M : 65536));
-  const size_t lds = (size_t)k * 8;
+  const size_t lds = (size_t)k * 12;
   if (z_bf16)
-    hipLaunchKernelGGL(distill_fwd_kernel<true>, grid, dim3(kThreads), lds, st, a);
+    hipLaunchKernelGGL(distill_fwd_kernel<true>, grid, dim3(kThreads), lds * kWaves, st, a);
   else
-    hipLaunchKernelGGL(distill_fwd_kernel<false>, grid, dim3(kThreads), lds, st, a);
+    hipLaunchKernelGGL(distill_fwd_kernel<false>, grid, dim3(kThreads), lds * kWaves, st, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && splits > 1) {
     if (z_bf16)
-      hipLaunchKernelGGL(distill_finish_kernel<true>, rows, dim3(kThreads), lds, st, a);
+      hipLaunchKernelGGL(distill_finish_kernel<true>, rows, dim3(64), lds, st, a);
     else
-      hipLaunchKernelGGL(distill_finish_kernel<false>, rows, dim3(kThreads), lds, st, a);
+      hipLaunchKernelGGL(distill_finish_kernel<false>, rows, dim3(64), lds, st, a);
     e = hipGetLastError();
   }
   return e;
@@ -342,12 +500,13 @@ hipError_t launch_distill_bwd(const void* z, int64_t ldz, bool z_bf16, int64_t M
                               const void* ids, bool ids64, const void* t, bool t_bf16, int k,
                               float T, const float* stats, const float* dloss, void* dz,
                               int64_t ldg, bool g_bf16, hipStream_t st) {
-  const int chunks = (int)((V + 32767) / 32768);
+  const int round = kBwdUnroll * kThreads * (z_bf16 && g_bf16 ? 8 : 4);
+  const int chunks = (int)((V + 63 + round - 1) / round);
   const DistillBwd a{z, ldz, M, V, {ids, t, ids64, t_bf16, k}, T, 1.0f / T, stats, dloss, dz, ldg,
-                     chunks, round8((V + chunks - 1) / chunks)};
+                     chunks};
   const int64_t items = M * chunks;
   const dim3 grid((unsigned)(items < 65536 ? items : 65536)), block(kThreads);
-  const size_t lds = (size_t)k * 8;
+  const size_t lds = (size_t)k * 8 * kWaves;
   if (z_bf16 && g_bf16)
     hipLaunchKernelGGL((distill_bwd_kernel<true, true>), grid, block, lds, st, a);
   else if (z_bf16)

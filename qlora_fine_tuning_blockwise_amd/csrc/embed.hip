@@ -52,18 +52,18 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedFwd a) {
     const elem_t<WB>* w = static_cast<const elem_t<WB>*>(a.W) + (live ? id : 0) * a.ldw;
     elem_t<OB>* o = static_cast<elem_t<OB>*>(a.out) + m * a.ldo;
     for (int c0 = t; c0 < full; c0 += 4 * T) {
-      Row8<WB> r[4];
+      Vec<WB, 8> r[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u)
-        r[u] = live && c0 + u * T < full ? load8<WB>(w + (c0 + u * T) * 8) : zero8<WB>();
+        r[u] = live && c0 + u * T < full ? load_vec<WB, 8>(w + (c0 + u * T) * 8) : zero_vec<WB, 8>();
 #pragma unroll
       for (int u = 0; u < 4; ++u)
         if (c0 + u * T < full) {
           float v[8];
-          to_float<WB>(r[u], v);
+          to_float<WB, 8>(r[u], v);
 #pragma unroll
           for (int e = 0; e < 8; ++e) v[e] = live ? v[e] * a.scale : 0.0f;
-          store8<OB>(o + (c0 + u * T) * 8, v);
+          store_vec<OB, 8>(o + (c0 + u * T) * 8, v);
         }
     }
     if (t < tail) {
@@ -167,21 +167,21 @@ struct EmbedBwd {
 
 template <bool GB>
 __device__ __forceinline__ void write_row(const EmbedBwd& a, int32_t id, int c, int n,
-                                          const float acc[8]) {
+                                          const float (&acc)[8]) {
   elem_t<GB>* p = static_cast<elem_t<GB>*>(a.dW) + (int64_t)id * a.D + c;
   float v[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] = acc[e] * a.scale;
   if (a.accumulate) {
     float old[8];
-    to_float<GB>(n >= 8 ? load8<GB>(p) : load8_part<GB>(p, n), old);
+    to_float<GB, 8>(n >= 8 ? load_vec<GB, 8>(p) : load_part<GB, 8>(p, n), old);
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += old[e];
   }
   if (n >= 8)
-    store8<GB>(p, v);
+    store_vec<GB, 8>(p, v);
   else
-    store8_part<GB>(p, v, n);
+    store_part<GB, 8>(p, v, n);
 }
 
 template <bool YB, bool GB>
@@ -201,18 +201,18 @@ __global__ __launch_bounds__(64) void embed_sum_kernel(EmbedBwd a) {
   for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
   constexpr int U = 8;
   for (int i0 = 0; i0 < n; i0 += U) {
-    Row8<YB> r[U];
+    Vec<YB, 8> r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      r[u] = zero8<YB>();
+      r[u] = zero_vec<YB, 8>();
       const int i = i0 + u;
       if (i >= n || __builtin_amdgcn_readlane(keys, i + 1) == kDead) continue;
       const elem_t<YB>* p = static_cast<const elem_t<YB>*>(a.dY) +
                             (int64_t)__builtin_amdgcn_readlane(poss, i) * a.ldy + c;
       if (left == 8)
-        r[u] = load8<YB>(p);
+        r[u] = load_vec<YB, 8>(p);
       else if (left > 0)
-        r[u] = load8_part<YB>(p, left);
+        r[u] = load_part<YB, 8>(p, left);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -221,7 +221,7 @@ __global__ __launch_bounds__(64) void embed_sum_kernel(EmbedBwd a) {
       const int32_t id = __builtin_amdgcn_readlane(keys, i + 1);
       if (id == kDead) break;  // sorted last: nothing follows
       float v[8];
-      to_float<YB>(r[u], v);
+      to_float<YB, 8>(r[u], v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += v[e];
       const bool ends = __builtin_amdgcn_readlane(keys, i + 2) != id;
@@ -233,7 +233,7 @@ __global__ __launch_bounds__(64) void embed_sum_kernel(EmbedBwd a) {
         } else {
           // a sum that covers the whole tile counts as one that began before it
           float* p = a.part + (tile * 2 + (begins ? 1 : 0)) * a.ldp + c;
-          store8<false>(p, acc);
+          store_vec<false, 8>(p, acc);
         }
       }
 #pragma unroll
@@ -276,7 +276,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedBwd a,
 #pragma unroll 4
     for (int64_t i = wave * per; i < stop; ++i) {
       float v[8];
-      to_float<false>(load8<false>(a.part + (tile + 1 + i) * 2 * a.ldp + c), v);
+      to_float<false, 8>(load_vec<false, 8>(a.part + (tile + 1 + i) * 2 * a.ldp + c), v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) acc[e] += v[e];
     }
@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedBwd a,
   __syncthreads();
   if (wave || !left) return;
   float v[8];
-  to_float<false>(load8<false>(a.part + (tile * 2 + 1) * a.ldp + c), v);
+  to_float<false, 8>(load_vec<false, 8>(a.part + (tile * 2 + 1) * a.ldp + c), v);
   for (int w = 0; w < kJoinWaves; ++w)
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] += join[w][lane * 8 + e];

@@ -238,9 +238,9 @@ hipError_t launch_norm_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void
                            bool dx_bf16, void* dgamma, void* dbeta, bool grad_bf16, float* part,
                            hipStream_t st);
 
-// part: with distill_splits(M, V) = s > 1, M * s * 2 floats. stats of the
-// forward may be NULL.
-int distill_splits(int64_t M, int64_t V);
+// part: M * distill_parts(V) * 2 floats (none where that is 0). stats of
+// the forward may be NULL.
+int distill_parts(int64_t V);
 hipError_t launch_distill_fwd(const void* z, int64_t ldz, bool z_bf16, int64_t M, int64_t V,
                               const void* ids, bool ids64, const void* t, bool t_bf16, int k,
                               float T, float* loss, float* stats, float* part, hipStream_t st);

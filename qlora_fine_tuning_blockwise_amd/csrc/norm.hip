@@ -51,13 +51,13 @@ __device__ __forceinline__ void row_stats(const float (&v)[NV][8], const int (&c
 
 template <bool kBf16, int NV, int T>
 __device__ __forceinline__ void load_row(const elem_t<kBf16>* row, int t, int N,
-                                         const int (&cnt)[NV], Row8<kBf16> (&r)[NV]) {
+                                         const int (&cnt)[NV], Vec<kBf16, 8> (&r)[NV]) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) r[i] = cnt[i] == 8 ? load8<kBf16>(row + (t + i * T) * 8) : zero8<kBf16>();
+  for (int i = 0; i < NV; ++i) r[i] = cnt[i] == 8 ? load_vec<kBf16, 8>(row + (t + i * T) * 8) : zero_vec<kBf16, 8>();
   if (N % 8) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (cnt[i] > 0 && cnt[i] < 8) r[i] = load8_part<kBf16>(row + (t + i * T) * 8, cnt[i]);
+      if (cnt[i] > 0 && cnt[i] < 8) r[i] = load_part<kBf16, 8>(row + (t + i * T) * 8, cnt[i]);
   }
 }
 
@@ -94,18 +94,18 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormFwd a) 
       g[i][e] = 1.0f;
       b[i][e] = 0.0f;
     }
-    if (a.gamma && cnt[i]) load_any8(a.gamma, a.w_bf16, (t + i * T) * 8, cnt[i], g[i]);
-    if (a.beta && cnt[i]) load_any8(a.beta, a.w_bf16, (t + i * T) * 8, cnt[i], b[i]);
+    if (a.gamma && cnt[i]) load_any_vec<8>(a.gamma, a.w_bf16, (t + i * T) * 8, cnt[i], g[i]);
+    if (a.beta && cnt[i]) load_any_vec<8>(a.beta, a.w_bf16, (t + i * T) * 8, cnt[i], b[i]);
   }
   const float invN = 1.0f / (float)a.N;
   int par = 0;
   for (int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T; row < a.M;
        row += (int64_t)gridDim.x * kGroups) {
-    Row8<XB> raw[NV];
+    Vec<XB, 8> raw[NV];
     load_row<XB, NV, T>(static_cast<const elem_t<XB>*>(a.x) + row * a.ldx, t, a.N, cnt, raw);
     float v[NV][8];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) to_float<XB>(raw[i], v[i]);
+    for (int i = 0; i < NV; ++i) to_float<XB, 8>(raw[i], v[i]);
     float mean, rstd;
     row_stats<T, NV>(v, cnt, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
     elem_t<YB>* out = static_cast<elem_t<YB>*>(a.y) + row * a.ldy;
@@ -114,9 +114,9 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormFwd a) 
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] = fmaf((v[i][e] - mean) * rstd, g[i][e], b[i][e]);
       if (cnt[i] == 8)
-        store8<YB>(out + (t + i * T) * 8, v[i]);
+        store_vec<YB, 8>(out + (t + i * T) * 8, v[i]);
       else if (cnt[i] > 0)
-        store8_part<YB>(out + (t + i * T) * 8, v[i], cnt[i]);
+        store_part<YB, 8>(out + (t + i * T) * 8, v[i], cnt[i]);
     }
     if (a.stats && t == 0) {
       a.stats[row] = mean;
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
       g[i][e] = 1.0f;
       ag[i][e] = ab[i][e] = 0.0f;
     }
-    if (a.gamma && cnt[i]) load_any8(a.gamma, a.w_bf16, (t + i * T) * 8, cnt[i], g[i]);
+    if (a.gamma && cnt[i]) load_any_vec<8>(a.gamma, a.w_bf16, (t + i * T) * 8, cnt[i], g[i]);
   }
   const float invN = 1.0f / (float)a.N;
   int par = 0;
@@ -171,13 +171,13 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
        row0 += (int64_t)gridDim.x * kGroups) {
     const int64_t row = row0 + group;
     const bool live = row < a.M;  // the barriers below are reached either way
-    Row8<XB> rx[NV];
-    Row8<YB> ry[NV];
+    Vec<XB, 8> rx[NV];
+    Vec<YB, 8> ry[NV];
     float mean = 0.0f, rstd = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      rx[i] = zero8<XB>();
-      ry[i] = zero8<YB>();
+      rx[i] = zero_vec<XB, 8>();
+      ry[i] = zero_vec<YB, 8>();
     }
     if (live) {
       load_row<XB, NV, T>(static_cast<const elem_t<XB>*>(a.x) + row * a.ldx, t, a.N, cnt, rx);
@@ -190,8 +190,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
     float x[NV][8], dy[NV][8];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      to_float<XB>(rx[i], x[i]);
-      to_float<YB>(ry[i], dy[i]);
+      to_float<XB, 8>(rx[i], x[i]);
+      to_float<YB, 8>(ry[i], dy[i]);
     }
     if (!a.stats) row_stats<T, NV>(x, cnt, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
     float s[2] = {0.0f, 0.0f};
@@ -219,9 +219,9 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) dy[i][e] = (dy[i][e] - c1 - x[i][e] * c2) * rstd;
           if (cnt[i] == 8)
-            store8<DB>(out + (t + i * T) * 8, dy[i]);
+            store_vec<DB, 8>(out + (t + i * T) * 8, dy[i]);
           else if (cnt[i] > 0)
-            store8_part<DB>(out + (t + i * T) * 8, dy[i], cnt[i]);
+            store_part<DB, 8>(out + (t + i * T) * 8, dy[i], cnt[i]);
         }
       }
     }
@@ -250,8 +250,8 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (cnt[i]) {  // ldp is a multiple of eight
-        store8<false>(out + (t + i * T) * 8, ag[i]);
-        store8<false>(out + a.ldp + (t + i * T) * 8, ab[i]);
+        store_vec<false, 8>(out + (t + i * T) * 8, ag[i]);
+        store_vec<false, 8>(out + a.ldp + (t + i * T) * 8, ab[i]);
       }
   }
 }

@@ -7,79 +7,102 @@
 
 namespace qlora {
 
-// 16-byte accesses that need only their element's alignment: gfx950 takes a
-// global access of four dwords at any byte address, so rows of odd width or
-// stride run the same code as aligned ones.
+// Accesses of 8 and 16 bytes that need only their element's alignment: gfx950
+// takes a global access of several dwords at any byte address, so rows of odd
+// width or stride run the same code as aligned ones.
+typedef uint32_t u32x2_a2 __attribute__((ext_vector_type(2), aligned(2)));
 typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));
-
-// Eight consecutive elements of a row as they lie in memory.
-template <bool kBf16>
-struct Row8 {
-  u32x4_t q[kBf16 ? 1 : 2];
-};
 
 template <bool kBf16>
 using elem_t = typename std::conditional<kBf16, uint16_t, float>::type;
 
-template <bool kBf16, bool kNt = false>
-__device__ __forceinline__ Row8<kBf16> load8(const elem_t<kBf16>* p) {
-  Row8<kBf16> r;
-  if constexpr (kBf16) {
-    const u32x4_a2* v = reinterpret_cast<const u32x4_a2*>(p);
-    r.q[0] = kNt ? __builtin_nontemporal_load(v) : *v;
+// E consecutive elements of a row as they lie in memory: 8 bf16 in 16 bytes,
+// or 4 elements (a row operator that touches fp32 takes all its rows by four,
+// so that every access of a wave is one run without gaps).
+template <bool kBf16, int E>
+struct Vec {
+  static_assert(E == 8 || E == 4, "elements of a vector");
+  static constexpr int kWords = kBf16 ? E / 2 : E;
+  uint32_t w[kWords];
+};
+
+template <bool kBf16, int E, bool kNt = false>
+__device__ __forceinline__ Vec<kBf16, E> load_vec(const elem_t<kBf16>* p) {
+  Vec<kBf16, E> r;
+  if constexpr (kBf16 && E == 4) {
+    const u32x2_a2* v = reinterpret_cast<const u32x2_a2*>(p);
+    const u32x2_a2 q = kNt ? __builtin_nontemporal_load(v) : *v;
+    r.w[0] = q[0];
+    r.w[1] = q[1];
   } else {
-    const u32x4_a4* v = reinterpret_cast<const u32x4_a4*>(p);
-    r.q[0] = kNt ? __builtin_nontemporal_load(v) : v[0];
-    r.q[1] = kNt ? __builtin_nontemporal_load(v + 1) : v[1];
+    using V = typename std::conditional<kBf16, u32x4_a2, u32x4_a4>::type;
+#pragma unroll
+    for (int h = 0; h < Vec<kBf16, E>::kWords / 4; ++h) {
+      const V* v = reinterpret_cast<const V*>(p) + h;
+      const V q = kNt ? __builtin_nontemporal_load(v) : *v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) r.w[4 * h + i] = q[i];
+    }
   }
   return r;
 }
 
-template <bool kBf16>
-__device__ __forceinline__ Row8<kBf16> zero8() {
-  Row8<kBf16> r;
-  r.q[0] = zero4();
-  if constexpr (!kBf16) r.q[1] = zero4();
+// A vector of one value, given by its bits: 0, or -infinity for a maximum.
+constexpr uint32_t kNegInf = 0xFF800000u;
+
+template <bool kBf16, int E, uint32_t kFill = 0u>
+__device__ __forceinline__ Vec<kBf16, E> fill_vec() {
+  Vec<kBf16, E> r;
+#pragma unroll
+  for (int i = 0; i < Vec<kBf16, E>::kWords; ++i)
+    r.w[i] = kBf16 ? (kFill & 0xFFFF0000u) | kFill >> 16 : kFill;
   return r;
 }
+template <bool kBf16, int E>
+__device__ __forceinline__ Vec<kBf16, E> zero_vec() {
+  return fill_vec<kBf16, E>();
+}
 
-// The first n < 8 of the eight (the rest +0): a row's last elements.
-template <bool kBf16>
-__device__ __forceinline__ Row8<kBf16> load8_part(const elem_t<kBf16>* p, int n) {
-  uint32_t w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+// The elements first <= e < n of the vector (the others the fill value): a
+// row's ends.
+template <bool kBf16, int E, uint32_t kFill = 0u>
+__device__ __forceinline__ Vec<kBf16, E> load_part(const elem_t<kBf16>* p, int n, int first = 0) {
+  Vec<kBf16, E> r = fill_vec<kBf16, E, kFill>();
 #pragma unroll
-  for (int e = 0; e < 7; ++e)
-    if (e < n) {
+  for (int e = 0; e < E; ++e)
+    if (e >= first && e < n) {
       if constexpr (kBf16)
-        w[e / 2] |= (uint32_t)p[e] << (16 * (e & 1));
+        r.w[e / 2] = e & 1 ? (r.w[e / 2] & 0xFFFFu) | (uint32_t)p[e] << 16
+                           : (r.w[e / 2] & 0xFFFF0000u) | p[e];
       else
-        w[e] = __float_as_uint(p[e]);
+        r.w[e] = __float_as_uint(p[e]);
     }
-  Row8<kBf16> r;
-  r.q[0] = u32x4_t{w[0], w[1], w[2], w[3]};
-  if constexpr (!kBf16) r.q[1] = u32x4_t{w[4], w[5], w[6], w[7]};
   return r;
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void to_float(const Row8<kBf16>& r, float v[8]) {
-  if constexpr (kBf16) {
+template <bool kBf16, int E>
+__device__ __forceinline__ void to_float(const Vec<kBf16, E>& r, float (&v)[E]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = bf16_lo(r.q[0][i]);
-      v[2 * i + 1] = bf16_hi(r.q[0][i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.q[i / 4][i % 4]);
+  for (int i = 0; i < E; ++i) {
+    if constexpr (kBf16)
+      v[i] = i & 1 ? bf16_hi(r.w[i / 2]) : bf16_lo(r.w[i / 2]);
+    else
+      v[i] = __uint_as_float(r.w[i]);
   }
 }
 
 // Stores round to nearest even, once.
-template <bool kBf16, bool kNt = false>
-__device__ __forceinline__ void store8(elem_t<kBf16>* p, const float v[8]) {
-  if constexpr (kBf16) {
+template <bool kBf16, int E, bool kNt = false>
+__device__ __forceinline__ void store_vec(elem_t<kBf16>* p, const float (&v)[E]) {
+  if constexpr (kBf16 && E == 4) {
+    const u32x2_t q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    u32x2_a2* d = reinterpret_cast<u32x2_a2*>(p);
+    if (kNt)
+      __builtin_nontemporal_store(q, d);
+    else
+      *d = q;
+  } else if constexpr (kBf16) {
     const u32x4_t q = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
                        pack_bf16x2(v[6], v[7])};
     u32x4_a2* d = reinterpret_cast<u32x4_a2*>(p);
@@ -89,7 +112,7 @@ __device__ __forceinline__ void store8(elem_t<kBf16>* p, const float v[8]) {
       *d = q;
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < E / 4; ++h) {
       const u32x4_t q = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]),
                          __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
       u32x4_a4* d = reinterpret_cast<u32x4_a4*>(p) + h;
@@ -109,21 +132,31 @@ __device__ __forceinline__ void store1(elem_t<kBf16>* p, float v) {
     *p = v;
 }
 
-template <bool kBf16>
-__device__ __forceinline__ void store8_part(elem_t<kBf16>* p, const float v[8], int n) {
+template <bool kBf16, int E>
+__device__ __forceinline__ void store_part(elem_t<kBf16>* p, const float (&v)[E], int n,
+                                           int first = 0) {
 #pragma unroll
-  for (int e = 0; e < 7; ++e)
-    if (e < n) store1<kBf16>(p + e, v[e]);
+  for (int e = 0; e < E; ++e)
+    if (e >= first && e < n) store1<kBf16>(p + e, v[e]);
 }
 
-// Eight elements (or the first n) of an array whose type is a run-time value.
-__device__ __forceinline__ void load_any8(const void* p, bool bf16, int64_t at, int n, float v[8]) {
+// How many of a vector's E elements at `at` lie below `end`.
+template <int E>
+__device__ __forceinline__ int count_below(int64_t at, int64_t end) {
+  const int64_t left = end - at;
+  return left >= E ? E : left < 0 ? 0 : (int)left;
+}
+
+// E elements (or the first n) of an array whose type is a run-time value.
+template <int E>
+__device__ __forceinline__ void load_any_vec(const void* p, bool bf16, int64_t at, int n,
+                                             float (&v)[E]) {
   if (bf16) {
     const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-    to_float<true>(n >= 8 ? load8<true>(q) : load8_part<true>(q, n), v);
+    to_float<true, E>(n >= E ? load_vec<true, E>(q) : load_part<true, E>(q, n), v);
   } else {
     const float* q = static_cast<const float*>(p) + at;
-    to_float<false>(n >= 8 ? load8<false>(q) : load8_part<false>(q, n), v);
+    to_float<false, E>(n >= E ? load_vec<false, E>(q) : load_part<false, E>(q, n), v);
   }
 }
 

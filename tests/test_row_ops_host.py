@@ -185,7 +185,7 @@ def test_distill_validation(lib):
     assert call(0, _p(FAKE + 1)) == 3 and call(5, _p(FAKE + 2)) == 3 and call(12, _p(FAKE + 1)) == 3
     assert call(3, 0) == 0
     assert q.qlora_distill_fwd_workspace_bytes(-1, 100) == 0
-    assert q.qlora_distill_fwd_workspace_bytes(1 << 20, 100) == 0   # rows enough: no split
+    assert q.qlora_distill_fwd_workspace_bytes(1 << 20, 100) == 0   # one workgroup a row
     need = q.qlora_distill_fwd_workspace_bytes(4, 100000)
     assert need > 0
     assert call(4, 100000, a1=100000) == 6
