@@ -238,9 +238,9 @@ EmbedLayout embed_layout(int64_t M, int64_t D) {
   EmbedLayout L;
   if (M == 0) return L;
   Carve c;
-  L.sorted = c.take(4 * (size_t)((M + 63) / 64 * 64) * 4);
-  const int64_t tile = embed_tile(M);
-  L.part = c.take((size_t)((M + tile - 1) / tile) * 2 * (size_t)((D + 7) / 8 * 8) * 4);
+  const size_t tiles = (size_t)((M + embed_tile(M) - 1) / embed_tile(M));
+  L.sorted = c.take((4 * (size_t)((M + 63) / 64 * 64) + 1 + tiles) * 4);
+  L.part = c.take(tiles * 2 * (size_t)((D + 7) / 8 * 8) * 4);
   L.total = c.off;
   return L;
 }

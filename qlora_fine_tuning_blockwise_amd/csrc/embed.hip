@@ -6,17 +6,18 @@
 // its dY row is not read.
 //
 // The gradient sorts the tokens by id (ties by position), so that each table
-// row is one sum in token order, whatever the launch: no atomics, the same
-// bits every time.
-//   1. Workgroups of the first launch sort runs of kRun tokens in LDS; the
-//      others fill dW with zeros, which is most of the call's traffic and
-//      hides the sort.
-//   2. With more than one run, a token's place is its place in its own run
-//      plus, by binary search, the count of smaller keys in the others.
+// row is one sum in token order, whatever the launch: no floating-point
+// atomics, the same bits every time.
+//   1. The first launch fills dW with zeros, which is most of the call's
+//      traffic; beside the fill, small workgroups count for each token how many
+//      tokens of its run come before it, which is its place in the run.
+//   2. With more than one run, a token's place among all is its place in its
+//      own run plus, by binary search, the count of smaller keys in the others.
 //   3. The sorted tokens are cut into tiles. A wave adds one tile's rows over
-//      512 columns in fp32 and writes each id whose tokens all lie in the
-//      tile; a sum that passes a tile's border goes to the workspace.
-//   4. The tile in which such a sum begins collects its parts in tile order.
+//      64 vectors of columns in fp32 and writes each id whose tokens all lie in
+//      the tile; a sum that passes a tile's border goes to the workspace, and
+//      the tile in which it begins is noted in a list.
+//   4. Workgroups take the list's sums and collect their parts in tile order.
 #include <type_traits>
 
 #include "rows.h"
@@ -24,8 +25,15 @@
 namespace qlora {
 namespace {
 
-constexpr int kRun = 4096;           // tokens sorted in one workgroup
-constexpr int32_t kDead = 0x7fffffff;  // sort key of an id outside of the table
+constexpr int32_t kDead = 0x7fffffff;  // key of an id outside of the table: sorted last
+
+// Tokens of a run. Counting costs run * M comparisons, a second run the launch
+// of the search: up to kMaxRun tokens are one run (4096 tokens: the count is
+// hidden by any fill from 20 MB on, the search took 5.8 us), more are runs of
+// kRun (at 16000 tokens the count of 1024-token runs and the search take 2 and
+// 7 us, the count over all tokens would take 15).
+constexpr int kMaxRun = 4096, kRun = 1024;
+int run_length(int64_t M) { return M <= kMaxRun ? kMaxRun : kRun; }
 
 // ------------------------------------------------------------------ lookup
 struct EmbedFwd {
@@ -74,84 +82,113 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedFwd a) {
 }
 
 // ---------------------------------------------------------------- the sort
-__device__ __forceinline__ int32_t sort_key(const void* ids, bool i64, int64_t m, int64_t V) {
-  const int64_t id = load_index(ids, i64, m);
-  return id >= 0 && id < V ? (int32_t)id : kDead;
-}
+// The first workgroups order 16 tokens each (sixteen threads a token, each of
+// which compares it with every sixteenth group of four of its run's keys); the
+// others write zeros over dW (`halves` two-byte units, its base 16-byte
+// aligned). The fill is nontemporal: with plain stores it leaves the Infinity
+// Cache full of lines that have yet to reach memory, and the sums that follow
+// wait for them (4096 tokens, 32000 x 4096 fp32: the sums take 23 against 13.7
+// us, the call 115 against 99 us). A workgroup writes 4 KB and ends: with a
+// quarter as many, four stores a thread, the call takes 101 us, with 8192 and
+// sixteen stores 130 us.
+constexpr int kOrderTokens = 16, kOrderThreads = 256;
 
-// Workgroup b < runs sorts tokens [b kRun, (b + 1) kRun) by (key, position)
-// with a bitonic network in LDS; the rest write zeros over dW.
-__global__ __launch_bounds__(1024) void embed_sort_kernel(const void* ids, bool i64, int64_t M,
-                                                          int64_t V, int runs, int32_t* key,
-                                                          int32_t* pos, u32x4_t* dW,
-                                                          int64_t halves) {
-  __shared__ uint64_t s[kRun];
-  if ((int)blockIdx.x >= runs) {
-    // halves: two-byte units of dW, whose base is 16-byte aligned
-    const int64_t quads = halves / 8, stride = (int64_t)(gridDim.x - runs) * 1024;
-    const int64_t first = (int64_t)(blockIdx.x - runs) * 1024 + threadIdx.x;
-    for (int64_t i = first; i < quads; i += stride) dW[i] = zero4();
+__global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
+    const void* ids, bool i64, int64_t M, int64_t V, int run, int orders, int32_t* key, int32_t* pos,
+    int32_t* count, u32x4_t* dW, int64_t halves) {
+  __shared__ __align__(16) int32_t keys[kMaxRun];
+  const int t = threadIdx.x;
+  if ((int)blockIdx.x >= orders) {
+    const int64_t quads = halves / 8, stride = (int64_t)(gridDim.x - orders) * kOrderThreads;
+    const int64_t first = (int64_t)(blockIdx.x - orders) * kOrderThreads + t;
+    for (int64_t i = first; i < quads; i += stride) __builtin_nontemporal_store(zero4(), dW + i);
     if (first < halves % 8) reinterpret_cast<uint16_t*>(dW)[quads * 8 + first] = 0;
     return;
   }
-  const int64_t base = (int64_t)blockIdx.x * kRun;
-  const int n = (int)(M - base < kRun ? M - base : kRun);
-  int n2 = 2;
-  while (n2 < n) n2 *= 2;
-  for (int i = threadIdx.x; i < n2; i += 1024)
-    s[i] = i < n ? (uint64_t)(uint32_t)sort_key(ids, i64, base + i, V) << 32 | (uint32_t)i
-                 : ~(uint64_t)0;
-  __syncthreads();
-  for (int k = 2; k <= n2; k *= 2)
-    for (int j = k / 2; j > 0; j /= 2) {
-      for (int p = threadIdx.x; p < n2 / 2; p += 1024) {
-        const int i = (p & ~(j - 1)) * 2 + (p & (j - 1));
-        const uint64_t a = s[i], b = s[i + j];
-        if ((a > b) == ((i & k) == 0)) {
-          s[i] = b;
-          s[i + j] = a;
-        }
-      }
-      __syncthreads();
+  if (blockIdx.x == 0 && t == 0) *count = 0;  // the list of embed_sum_kernel is empty
+  const int64_t token = (int64_t)blockIdx.x * kOrderTokens;  // run is a multiple of kOrderTokens
+  const int64_t base = token / run * run;
+  const int n = (int)(M - base < run ? M - base : run);
+  for (int i = t; i < (n + 3) / 4 * 4; i += kOrderThreads) {
+    int32_t k = kDead;  // behind the last token: after every token, as its place is later
+    if (i < n) {
+      const int64_t id = load_index(ids, i64, base + i);
+      if (id >= 0 && id < V) k = (int32_t)id;
     }
-  for (int i = threadIdx.x; i < n; i += 1024) {
-    key[base + i] = (int32_t)(s[i] >> 32);
-    pos[base + i] = (int32_t)(base + (int32_t)(uint32_t)s[i]);
+    keys[i] = k;
+  }
+  __syncthreads();
+  const int own = (int)(token - base) + t / 16, part = t % 16;
+  const bool live = own < n;
+  const int32_t k = live ? keys[own] : 0;
+  int before = 0;
+  for (int i = part * 4; i < n; i += 64) {
+    const u32x4_t q = *reinterpret_cast<const u32x4_t*>(keys + i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)  // below k, or its equal at an earlier place
+      before += q[e] < (uint32_t)k + (uint32_t)(i + e < own);
+  }
+#pragma unroll
+  for (int m = 1; m < 16; m *= 2) before += __shfl_xor(before, m, 64);
+  if (live && part == 0) {
+    key[base + before] = k;
+    pos[base + before] = (int32_t)(base + own);
   }
 }
+
+// The place of each token among all: its place in its run and, for every
+// other run, the count of keys before it by binary search. Sixteen lanes work
+// on a token, each on four runs at a time, so that the searches' loads fly
+// together.
+constexpr int kRankLanes = 16;
 
 __global__ __launch_bounds__(256) void embed_rank_kernel(const int32_t* __restrict__ key,
                                                          const int32_t* __restrict__ pos,
                                                          int64_t M, int runs,
                                                          int32_t* __restrict__ key_out,
                                                          int32_t* __restrict__ pos_out) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= M) return;
-  const int own = (int)(i / kRun);
-  const int32_t k = key[i];
-  int64_t rank = i - (int64_t)own * kRun;
-  for (int r = 0; r < runs; ++r) {
-    if (r == own) continue;
-    // keys before k: those below it, and in an earlier run its equals too
-    const int32_t* p = key + (int64_t)r * kRun;
-    const int n = (int)(M - (int64_t)r * kRun < kRun ? M - (int64_t)r * kRun : kRun);
-    const bool equals = r < own;
-    int lo = 0, hi = n;
-    while (lo < hi) {
-      const int mid = (lo + hi) / 2;
-      const int32_t v = p[mid];
-      if (v < k || (equals && v == k))
-        lo = mid + 1;
-      else
-        hi = mid;
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kRankLanes;
+  const int part = threadIdx.x % kRankLanes;
+  const bool live = i < M;
+  const int own = live ? (int)(i / kRun) : 0;
+  const int32_t k = live ? key[i] : 0;
+  int count = 0;
+  constexpr int B = 4;
+  for (int r0 = part; live && r0 < runs; r0 += B * kRankLanes) {
+    int lo[B], n[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int r = r0 + b * kRankLanes;
+      const int64_t left = M - (int64_t)r * kRun;
+      n[b] = r == own || left < 0 ? 0 : left < kRun ? (int)left : kRun;
+      lo[b] = 0;
     }
-    rank += lo;
+    for (int step = kRun; step > 0; step /= 2)
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int at = lo[b] + step, r = r0 + b * kRankLanes;
+        if (at > n[b]) continue;
+        const int32_t v = key[(int64_t)r * kRun + at - 1];
+        // before k: what is below it, and in an earlier run its equals too
+        if (v < k || (r < own && v == k)) lo[b] = at;
+      }
+#pragma unroll
+    for (int b = 0; b < B; ++b) count += lo[b];
   }
-  key_out[rank] = k;
-  pos_out[rank] = pos[i];
+#pragma unroll
+  for (int m = 1; m < kRankLanes; m *= 2) count += __shfl_xor(count, m, 64);
+  if (live && part == 0) {
+    const int64_t rank = i - (int64_t)own * kRun + count;
+    key_out[rank] = k;
+    pos_out[rank] = pos[i];
+  }
 }
 
 // ---------------------------------------------------------------- the sums
+// Four, eight and sixteen waves: 16000 tokens, half of them one id, 50, 46 and
+// 47 us; 4096 tokens of 4096 columns, many short sums, 128, 130 and 137 us.
+constexpr int kJoinWaves = 8;
+
 struct EmbedBwd {
   const void* dY;
   int64_t ldy, M;
@@ -161,136 +198,144 @@ struct EmbedBwd {
   void* dW;
   const int32_t* key;
   const int32_t* pos;
-  float* part;  // [tiles][2][ldp]: the sum that began before the tile, the one that passes its end
+  int32_t* list;  // [0]: count, then the tiles in which a sum begins that passes their end
+  float* part;    // [tiles][2][ldp]: the sum that began before the tile, the one that passes its end
   int ldp, tile;
 };
 
-template <bool GB>
+template <bool GB, int E>
 __device__ __forceinline__ void write_row(const EmbedBwd& a, int32_t id, int c, int n,
-                                          const float (&acc)[8]) {
+                                          const float (&acc)[E]) {
   elem_t<GB>* p = static_cast<elem_t<GB>*>(a.dW) + (int64_t)id * a.D + c;
-  float v[8];
+  float v[E];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) v[e] = acc[e] * a.scale;
+  for (int e = 0; e < E; ++e) v[e] = acc[e] * a.scale;
   if (a.accumulate) {
-    float old[8];
-    to_float<GB, 8>(n >= 8 ? load_vec<GB, 8>(p) : load_part<GB, 8>(p, n), old);
+    float old[E];
+    to_float<GB, E>(n >= E ? load_vec<GB, E>(p) : load_part<GB, E>(p, n), old);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += old[e];
+    for (int e = 0; e < E; ++e) v[e] += old[e];
   }
-  if (n >= 8)
-    store_vec<GB, 8>(p, v);
+  if (n >= E)
+    store_vec<GB, E>(p, v);
   else
-    store_part<GB, 8>(p, v, n);
+    store_part<GB, E>(p, v, n);
 }
 
+// Wave (64 E columns, tile). The loads of kRows rows fly together.
 template <bool YB, bool GB>
 __global__ __launch_bounds__(64) void embed_sum_kernel(EmbedBwd a) {
-  const int64_t tile = blockIdx.x;
-  const int64_t first = tile * a.tile;
-  const int n = (int)(a.M - first < a.tile ? a.M - first : a.tile);  // at most 62
+  constexpr int E = YB && GB ? 8 : 4, kRows = 8;
+  const int64_t tile = blockIdx.y;
+  const int64_t begin = tile * a.tile;
   const int lane = threadIdx.x;
-  // lane i holds the key before, at (1..n) and after the tile's tokens
-  const int64_t at = first + lane - 1;
-  const int32_t keys = at >= 0 && at < a.M && lane < n + 2 ? a.key[at] : -1;
-  const int32_t poss = lane < n ? a.pos[first + lane] : 0;
-  const int c = (blockIdx.y * 64 + lane) * 8;
-  const int left = a.D - c < 0 ? 0 : a.D - c < 8 ? a.D - c : 8;
-  float acc[8];
+  // Lane i < n holds token i of the tile and its key; `before` and `after` are
+  // the keys next to the tile.
+  const int size = (int)(a.M - begin < a.tile ? a.M - begin : a.tile);
+  const int32_t key = lane < size ? a.key[begin + lane] : kDead;
+  const int32_t pos = lane < size ? a.pos[begin + lane] : 0;
+  const int32_t before = tile > 0 ? a.key[begin - 1] : -1;
+  const int32_t after = begin + size < a.M ? a.key[begin + size] : -1;
+  const int n = __popcll(__ballot(key != kDead));  // the dead come last
+  if (n == 0) return;
+  const int32_t next = __shfl_down(key, 1);
+  // bit i: the sum that token i belongs to ends with it
+  const uint64_t ends = __ballot(lane < n && (lane + 1 < size ? next : after) != key);
+  bool open = __builtin_amdgcn_readfirstlane(key) == before;  // the sum began before the tile
+  const int c = ((int)blockIdx.x * 64 + lane) * E;
+  const int left = count_below<E>(c, a.D);
+  const elem_t<YB>* dY = static_cast<const elem_t<YB>*>(a.dY) + c;
+  float acc[E];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-  constexpr int U = 8;
-  for (int i0 = 0; i0 < n; i0 += U) {
-    Vec<YB, 8> r[U];
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+  for (int i0 = 0; i0 < n; i0 += kRows) {
+    Vec<YB, E> r[kRows];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      r[u] = zero_vec<YB, 8>();
-      const int i = i0 + u;
-      if (i >= n || __builtin_amdgcn_readlane(keys, i + 1) == kDead) continue;
-      const elem_t<YB>* p = static_cast<const elem_t<YB>*>(a.dY) +
-                            (int64_t)__builtin_amdgcn_readlane(poss, i) * a.ldy + c;
-      if (left == 8)
-        r[u] = load_vec<YB, 8>(p);
-      else if (left > 0)
-        r[u] = load_part<YB, 8>(p, left);
+    for (int u = 0; u < kRows; ++u) {  // behind the last token its row again
+      const int i = i0 + u < n ? i0 + u : n - 1;
+      const elem_t<YB>* p = dY + (int64_t)__builtin_amdgcn_readlane(pos, i) * a.ldy;
+      r[u] = left == E ? load_vec<YB, E>(p) : zero_vec<YB, E>();
+      if (a.D % E && left > 0 && left < E) r[u] = load_part<YB, E>(p, left);
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
+    for (int u = 0; u < kRows; ++u) {
       const int i = i0 + u;
       if (i >= n) break;
-      const int32_t id = __builtin_amdgcn_readlane(keys, i + 1);
-      if (id == kDead) break;  // sorted last: nothing follows
-      float v[8];
-      to_float<YB, 8>(r[u], v);
+      float v[E];
+      to_float<YB, E>(r[u], v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[e];
-      const bool ends = __builtin_amdgcn_readlane(keys, i + 2) != id;
-      if (!ends && i + 1 < n) continue;
-      const bool begins = __builtin_amdgcn_readlane(keys, 0) != id;
-      if (left > 0) {
-        if (ends && begins) {
-          write_row<GB>(a, id, c, left, acc);
-        } else {
-          // a sum that covers the whole tile counts as one that began before it
-          float* p = a.part + (tile * 2 + (begins ? 1 : 0)) * a.ldp + c;
-          store_vec<false, 8>(p, acc);
-        }
+      for (int e = 0; e < E; ++e) acc[e] += v[e];
+      const bool end = ends >> i & 1;
+      if (!end && i + 1 < size) continue;
+      if (end && !open) {
+        if (left > 0) write_row<GB, E>(a, __builtin_amdgcn_readlane(key, i), c, left, acc);
+      } else {
+        // a sum that covers the whole tile counts as one that began before it
+        if (left > 0) store_vec<false, E>(a.part + (tile * 2 + (open ? 0 : 1)) * a.ldp + c, acc);
+        if (!open && blockIdx.x == 0 && lane == 0)
+          a.list[1 + atomicAdd(a.list, 1)] = (int32_t)tile;  // its order does not matter
       }
+      open = false;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+      for (int e = 0; e < E; ++e) acc[e] = 0.0f;
     }
   }
 }
 
-// Workgroup (tile, 512 columns): if a sum begins in the tile and passes its
-// end, it is this workgroup's. The following tiles' parts are dealt to the
-// waves in consecutive ranges, whose sums are added in order.
-constexpr int kJoinWaves = 4;
-
+// Workgroup (256 columns, some of the list): a sum that begins in a tile and
+// passes its end. The following tiles' parts are dealt to the waves in
+// consecutive ranges, whose sums are added in order.
 template <bool GB>
-__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedBwd a, int64_t tiles) {
-  __shared__ float join[kJoinWaves][64 * 8];
-  const int64_t tile = blockIdx.x;
-  const int64_t end = (tile + 1) * a.tile;  // the last tile is not launched: end < M
-  const int32_t id = a.key[end - 1];
-  if (id == kDead || a.key[end] != id) return;
-  if (a.key[tile * a.tile] == id && tile > 0 && a.key[tile * a.tile - 1] == id) return;
+__global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedBwd a) {
+  __shared__ float join[kJoinWaves][64 * 4];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  // The tiles after this one that begin with the id.
-  int64_t n = 0;
-  for (;;) {
-    const int64_t f = (tile + 1 + n + lane) * a.tile;
-    const uint64_t yes = __ballot(f < a.M && a.key[f < a.M ? f : 0] == id);
-    const int run = yes == ~(uint64_t)0 ? 64 : __builtin_ctzll(~yes);
-    n += run;
-    if (run < 64) break;
-  }
-  const int c = (blockIdx.y * 64 + lane) * 8;
-  const int left = a.D - c < 0 ? 0 : a.D - c < 8 ? a.D - c : 8;
-  float acc[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-  const int64_t per = (n + kJoinWaves - 1) / kJoinWaves;
-  const int64_t stop = (wave + 1) * per < n ? (wave + 1) * per : n;
-  if (left > 0) {
-#pragma unroll 4
-    for (int64_t i = wave * per; i < stop; ++i) {
-      float v[8];
-      to_float<false, 8>(load_vec<false, 8>(a.part + (tile + 1 + i) * 2 * a.ldp + c), v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) acc[e] += v[e];
+  const int c = ((int)blockIdx.x * 64 + lane) * 4;
+  const int left = count_below<4>(c, a.D);
+  const int sums = a.list[0];
+  for (int at = blockIdx.y; at < sums; at += gridDim.y) {
+    const int64_t tile = a.list[1 + at];
+    const int32_t id = a.key[(tile + 1) * a.tile - 1];
+    // The tiles after this one that begin with the id.
+    int64_t n = 0;
+    for (;;) {
+      const int64_t f = (tile + 1 + n + lane) * a.tile;
+      const uint64_t yes = __ballot(f < a.M && a.key[f < a.M ? f : 0] == id);
+      const int run = yes == ~(uint64_t)0 ? 64 : __builtin_ctzll(~yes);
+      n += run;
+      if (run < 64) break;
     }
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int64_t per = (n + kJoinWaves - 1) / kJoinWaves;
+    const int64_t stop = (wave + 1) * per < n ? (wave + 1) * per : n;
+    if (left > 0) {
+      const float* p = a.part + (tile + 1) * 2 * a.ldp + c;
+      for (int64_t i0 = wave * per; i0 < stop; i0 += 8) {
+        Vec<false, 4> r[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          r[u] = i0 + u < stop ? load_vec<false, 4>(p + (i0 + u) * 2 * a.ldp) : zero_vec<false, 4>();
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          float v[4];
+          to_float<false, 4>(r[u], v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[e] += v[e];
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) join[wave][lane * 4 + e] = acc[e];
+    __syncthreads();
+    if (wave == 0 && left > 0) {
+      float v[4];
+      to_float<false, 4>(load_vec<false, 4>(a.part + (tile * 2 + 1) * a.ldp + c), v);
+      for (int w = 0; w < kJoinWaves; ++w)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] += join[w][lane * 4 + e];
+      write_row<GB, 4>(a, id, c, left, v);
+    }
+    __syncthreads();  // `join` is written anew for the next sum
   }
-#pragma unroll
-  for (int e = 0; e < 8; ++e) join[wave][lane * 8 + e] = acc[e];
-  __syncthreads();
-  if (wave || !left) return;
-  float v[8];
-  to_float<false, 8>(load_vec<false, 8>(a.part + (tile * 2 + 1) * a.ldp + c), v);
-  for (int w = 0; w < kJoinWaves; ++w)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += join[w][lane * 8 + e];
-  write_row<GB>(a, id, c, left, v);
 }
 
 template <bool WB, bool OB>
@@ -308,12 +353,14 @@ hipError_t fwd(const EmbedFwd& a, hipStream_t st) {
 template <bool YB, bool GB>
 hipError_t sums(const EmbedBwd& a, hipStream_t st) {
   const unsigned tiles = (unsigned)((a.M + a.tile - 1) / a.tile);
-  const unsigned cols = (unsigned)((a.D + 511) / 512);
-  hipLaunchKernelGGL((embed_sum_kernel<YB, GB>), dim3(tiles, cols), dim3(64), 0, st, a);
+  constexpr int kCols = 64 * (YB && GB ? 8 : 4);
+  hipLaunchKernelGGL((embed_sum_kernel<YB, GB>), dim3((unsigned)((a.D + kCols - 1) / kCols), tiles),
+                     dim3(64), 0, st, a);
   hipError_t e = hipGetLastError();
   if (e == hipSuccess && tiles > 1) {
-    hipLaunchKernelGGL((embed_join_kernel<GB>), dim3(tiles - 1, cols), dim3(64 * kJoinWaves), 0, st,
-                       a, (int64_t)tiles);
+    hipLaunchKernelGGL((embed_join_kernel<GB>),
+                       dim3((unsigned)((a.D + 255) / 256), tiles < 256 ? tiles : 256),
+                       dim3(64 * kJoinWaves), 0, st, a);
     e = hipGetLastError();
   }
   return e;
@@ -321,7 +368,12 @@ hipError_t sums(const EmbedBwd& a, hipStream_t st) {
 
 }  // namespace
 
-int embed_tile(int64_t M) { return M <= 512 ? 4 : M <= 4096 ? 16 : 32; }
+// Tokens of a tile (at most 62, which a wave's lanes hold). Up to 32 tokens are
+// one tile, so that nothing is left to join (20 tokens of 4096 columns: 14.3
+// against 16.8 us); above, shorter tiles give more waves and longer ones fewer
+// parts (tiles of 8, 16 and 32: 4096 x 256 24.8, 24.1 and 27.6 us, 16000 x 1024
+// 54, 46 and 44 us, 32768 x 2048 109, 98 and 96 us).
+int embed_tile(int64_t M) { return M <= 32 ? 32 : M <= 4096 ? 16 : 32; }
 
 hipError_t launch_embed_fwd(const void* W, int64_t ldw, bool w_bf16, int64_t V, int64_t D,
                             const void* ids, bool ids64, int64_t M, float scale, void* out,
@@ -334,26 +386,29 @@ hipError_t launch_embed_fwd(const void* W, int64_t ldw, bool w_bf16, int64_t V, 
 hipError_t launch_embed_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void* ids, bool ids64,
                             int64_t M, int64_t V, int64_t D, float scale, void* dW, bool grad_bf16,
                             bool accumulate, int32_t* sorted, float* part, hipStream_t st) {
-  const int runs = (int)((M + kRun - 1) / kRun);
+  const int run = run_length(M);
+  const int runs = (int)((M + run - 1) / run);
   const int64_t Mp = (M + 63) / 64 * 64;
-  int32_t *key = sorted, *pos = sorted + Mp;
+  int32_t *key = sorted, *pos = sorted + Mp, *list = sorted + 4 * Mp;
   const int64_t halves = accumulate ? 0 : V * D * (grad_bf16 ? 1 : 2);
-  const int64_t fills = (halves / 8 + 4095) / 4096;
-  const int64_t fill = halves ? (fills < 1 ? 1 : fills > 2048 ? 2048 : fills) : 0;
-  if (runs + fill > 0) {
-    hipLaunchKernelGGL(embed_sort_kernel, dim3((unsigned)(runs + fill)), dim3(1024), 0, st, ids,
-                       ids64, M, V, runs, key, pos, static_cast<u32x4_t*>(dW), halves);
+  const int64_t fills = (halves / 8 + kOrderThreads - 1) / kOrderThreads;
+  const int64_t fill = halves ? (fills < 1 ? 1 : fills > (1 << 20) ? (1 << 20) : fills) : 0;
+  const int orders = (int)((M + kOrderTokens - 1) / kOrderTokens);
+  if (orders + fill > 0) {
+    hipLaunchKernelGGL(embed_order_kernel, dim3((unsigned)(orders + fill)), dim3(kOrderThreads), 0,
+                       st, ids, ids64, M, V, run, orders, key, pos, list, static_cast<u32x4_t*>(dW),
+                       halves);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   if (M == 0) return hipSuccess;
   if (runs > 1) {
-    hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)((M + 255) / 256)), dim3(256), 0, st, key,
-                       pos, M, runs, sorted + 2 * Mp, sorted + 3 * Mp);
+    hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)((M * kRankLanes + 255) / 256)), dim3(256),
+                       0, st, key, pos, M, runs, sorted + 2 * Mp, sorted + 3 * Mp);
     if (const hipError_t e = hipGetLastError()) return e;
     key = sorted + 2 * Mp;
     pos = sorted + 3 * Mp;
   }
-  const EmbedBwd a{dY, ldy, M, (int)D, scale, accumulate, dW, key, pos, part,
+  const EmbedBwd a{dY, ldy, M, (int)D, scale, accumulate, dW, key, pos, list, part,
                    (int)((D + 7) / 8 * 8), embed_tile(M)};
   if (dy_bf16) return grad_bf16 ? sums<true, true>(a, st) : sums<true, false>(a, st);
   return grad_bf16 ? sums<false, true>(a, st) : sums<false, false>(a, st);

@@ -216,8 +216,8 @@ hipError_t launch_zero(void* p, size_t bytes, hipStream_t st);
 hipError_t launch_embed_fwd(const void* W, int64_t ldw, bool w_bf16, int64_t V, int64_t D,
                             const void* ids, bool ids64, int64_t M, float scale, void* out,
                             int64_t ldo, bool out_bf16, hipStream_t st);
-// dW [V, D] contiguous, 16-byte aligned. sorted: 4 * round_up(M, 64) int32;
-// part: ceil(M / embed_tile(M)) * 2 * round_up(D, 8) floats. M = 0 is allowed.
+// dW [V, D] contiguous, 16-byte aligned. sorted: 4 * round_up(M, 64) + 1 +
+// ceil(M / embed_tile(M)) int32; part: ceil(M / embed_tile(M)) * 2 * round_up(D, 8) floats. M = 0 is allowed.
 int embed_tile(int64_t M);
 hipError_t launch_embed_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void* ids, bool ids64,
                             int64_t M, int64_t V, int64_t D, float scale, void* dW, bool grad_bf16,
