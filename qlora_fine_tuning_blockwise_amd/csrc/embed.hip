@@ -93,6 +93,24 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedFwd a) {
 // sixteen stores 130 us.
 constexpr int kOrderTokens = 16, kOrderThreads = 256;
 
+// The keys of a run's n tokens into LDS, up to the next multiple of four, with
+// the loads of eight rounds of the workgroup in flight. What lies behind the
+// last token counts as dead: it comes after every token, its place is later.
+template <typename T>
+__device__ __forceinline__ void stage_keys(const T* ids, int n, int64_t V, int32_t* keys) {
+  constexpr int B = 8;
+  const int end = (n + 3) / 4 * 4;
+  for (int i0 = threadIdx.x; i0 < end; i0 += B * kOrderThreads) {
+    T id[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) id[b] = i0 + b * kOrderThreads < n ? ids[i0 + b * kOrderThreads] : -1;
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      if (i0 + b * kOrderThreads < end)
+        keys[i0 + b * kOrderThreads] = id[b] >= 0 && id[b] < V ? (int32_t)id[b] : kDead;
+  }
+}
+
 __global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
     const void* ids, bool i64, int64_t M, int64_t V, int run, int orders, int32_t* key, int32_t* pos,
     int32_t* count, u32x4_t* dW, int64_t halves) {
@@ -109,19 +127,16 @@ __global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
   const int64_t token = (int64_t)blockIdx.x * kOrderTokens;  // run is a multiple of kOrderTokens
   const int64_t base = token / run * run;
   const int n = (int)(M - base < run ? M - base : run);
-  for (int i = t; i < (n + 3) / 4 * 4; i += kOrderThreads) {
-    int32_t k = kDead;  // behind the last token: after every token, as its place is later
-    if (i < n) {
-      const int64_t id = load_index(ids, i64, base + i);
-      if (id >= 0 && id < V) k = (int32_t)id;
-    }
-    keys[i] = k;
-  }
+  if (i64)
+    stage_keys(static_cast<const int64_t*>(ids) + base, n, V, keys);
+  else
+    stage_keys(static_cast<const int32_t*>(ids) + base, n, V, keys);
   __syncthreads();
   const int own = (int)(token - base) + t / 16, part = t % 16;
   const bool live = own < n;
   const int32_t k = live ? keys[own] : 0;
   int before = 0;
+#pragma unroll 4
   for (int i = part * 4; i < n; i += 64) {
     const u32x4_t q = *reinterpret_cast<const u32x4_t*>(keys + i);
 #pragma unroll
