@@ -12,8 +12,8 @@
 // with sum x^2 cancels when the mean is large against the deviation). All
 // statistics and sums are fp32.
 //
-// T threads hold a row, NV vectors of eight elements each; a wave alone needs
-// no barrier.
+// T threads hold a row (NV vectors of E elements each, T vectors apart, so that
+// a wave's access is one run); a wave alone needs no barrier.
 #include <type_traits>
 
 #include "rows.h"
@@ -21,19 +21,85 @@
 namespace qlora {
 namespace {
 
-// The statistics of the rows in v (n elements of it count, from column 0 on
-// in steps of T vectors).
-template <int T, int NV>
-__device__ __forceinline__ void row_stats(const float (&v)[NV][8], const int (&cnt)[NV], float invN,
-                                          bool center, float eps, float* red, int waves, int& par,
-                                          float& mean, float& rstd) {
+// Where a thread's vectors lie in a row of N elements. A row that is no whole
+// number of vectors ends in a vector that is moved back to end with it: its
+// first `skip` elements are the neighbour's too. Both hold the same values and
+// store the same results; in the row's sums they count once. (Rows shorter
+// than a vector, kShort, are read and written element by element.)
+template <int T, int NV, int E>
+struct Place {
+  int at[NV];    // first element
+  int skip[NV];  // elements that do not count; E: no vector
+  __device__ __forceinline__ Place(int t, int N) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int first = (t + i * T) * E;
+      at[i] = first + E <= N || N < E ? first : N - E;
+      skip[i] = first >= N ? E : N < E ? 0 : first - at[i];
+    }
+  }
+  __device__ __forceinline__ bool any(int i) const { return skip[i] < E; }
+};
+
+template <bool kBf16, bool kShort, int T, int NV, int E>
+__device__ __forceinline__ void load_row(const elem_t<kBf16>* row, int N, const Place<T, NV, E>& p,
+                                         Vec<kBf16, E> (&r)[NV]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    r[i] = zero_vec<kBf16, E>();
+    if (p.any(i)) r[i] = kShort ? load_part<kBf16, E>(row, N) : load_vec<kBf16, E>(row + p.at[i]);
+  }
+}
+
+template <bool kBf16, bool kShort, int T, int NV, int E>
+__device__ __forceinline__ void store_row(elem_t<kBf16>* row, int N, const Place<T, NV, E>& p,
+                                          const float (&v)[NV][E]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    if (!p.any(i)) continue;
+    if (kShort)
+      store_part<kBf16, E>(row, v[i], N);
+    else
+      store_vec<kBf16, E>(row + p.at[i], v[i]);
+  }
+}
+
+// The affine vectors, whose type is a run-time value.
+template <bool kShort, int T, int NV, int E>
+__device__ __forceinline__ void load_affine(const void* w, bool bf16, int N,
+                                            const Place<T, NV, E>& p, float other,
+                                            float (&v)[NV][E]) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[i][e] = other;
+  if (!w) return;
+  if (bf16) {
+    Vec<true, E> r[NV];
+    load_row<true, kShort, T, NV, E>(static_cast<const uint16_t*>(w), N, p, r);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) to_float<true, E>(r[i], v[i]);
+  } else {
+    Vec<false, E> r[NV];
+    load_row<false, kShort, T, NV, E>(static_cast<const float*>(w), N, p, r);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) to_float<false, E>(r[i], v[i]);
+  }
+}
+
+// The statistics of the row in v.
+template <bool kShort, int T, int NV, int E>
+__device__ __forceinline__ void row_stats(const float (&v)[NV][E], const Place<T, NV, E>& p, int N,
+                                          float invN, bool center, float eps, float* red, int waves,
+                                          int& par, float& mean, float& rstd) {
+  const auto counts = [&](int i, int e) { return e >= p.skip[i] && (!kShort || e < N); };
   mean = 0.0f;
   if (center) {
     float s[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += v[i][e];
+      for (int e = 0; e < E; ++e) s[0] += counts(i, e) ? v[i][e] : 0.0f;
     group_reduce<T, 1>(s, red, waves, par, OpSum());
     mean = s[0] * invN;
   }
@@ -41,24 +107,12 @@ __device__ __forceinline__ void row_stats(const float (&v)[NV][8], const int (&c
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float d = e < cnt[i] ? v[i][e] - mean : 0.0f;
+    for (int e = 0; e < E; ++e) {
+      const float d = counts(i, e) ? v[i][e] - mean : 0.0f;
       s[0] = fmaf(d, d, s[0]);
     }
   group_reduce<T, 1>(s, red, waves, par, OpSum());
   rstd = 1.0f / __builtin_sqrtf(s[0] * invN + eps);
-}
-
-template <bool kBf16, int NV, int T>
-__device__ __forceinline__ void load_row(const elem_t<kBf16>* row, int t, int N,
-                                         const int (&cnt)[NV], Vec<kBf16, 8> (&r)[NV]) {
-#pragma unroll
-  for (int i = 0; i < NV; ++i) r[i] = cnt[i] == 8 ? load_vec<kBf16, 8>(row + (t + i * T) * 8) : zero_vec<kBf16, 8>();
-  if (N % 8) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (cnt[i] > 0 && cnt[i] < 8) r[i] = load_part<kBf16, 8>(row + (t + i * T) * 8, cnt[i]);
-  }
 }
 
 struct NormFwd {
@@ -74,50 +128,37 @@ struct NormFwd {
   float* stats;
 };
 
-template <bool XB, bool YB, int T, int NV>
+template <bool XB, bool YB, int T, int N8, bool kShort>
 __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormFwd a) {
   constexpr int kThreads = T < 256 ? 256 : T;
   constexpr int kGroups = kThreads / T, kWaves = kThreads / 64;
+  constexpr int E = XB && YB ? 8 : 4, NV = N8 * 8 / E;
   __shared__ float red[2 * kWaves];
   const int t = threadIdx.x % T;
-  int cnt[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int left = a.N - (t + i * T) * 8;
-    cnt[i] = left < 0 ? 0 : left > 8 ? 8 : left;
-  }
-  float g[NV][8], b[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      g[i][e] = 1.0f;
-      b[i][e] = 0.0f;
-    }
-    if (a.gamma && cnt[i]) load_any_vec<8>(a.gamma, a.w_bf16, (t + i * T) * 8, cnt[i], g[i]);
-    if (a.beta && cnt[i]) load_any_vec<8>(a.beta, a.w_bf16, (t + i * T) * 8, cnt[i], b[i]);
-  }
+  const int64_t step = (int64_t)gridDim.x * kGroups;
+  int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T;
+  if (row >= a.M) return;  // of a group of one wave: there are no barriers then
+  const elem_t<XB>* x = static_cast<const elem_t<XB>*>(a.x);
+  const Place<T, NV, E> p(t, a.N);
+  Vec<XB, E> next[NV];
+  load_row<XB, kShort>(x + row * a.ldx, a.N, p, next);
+  float g[NV][E], b[NV][E];
+  load_affine<kShort>(a.gamma, a.w_bf16, a.N, p, 1.0f, g);
+  load_affine<kShort>(a.beta, a.w_bf16, a.N, p, 0.0f, b);
   const float invN = 1.0f / (float)a.N;
   int par = 0;
-  for (int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T; row < a.M;
-       row += (int64_t)gridDim.x * kGroups) {
-    Vec<XB, 8> raw[NV];
-    load_row<XB, NV, T>(static_cast<const elem_t<XB>*>(a.x) + row * a.ldx, t, a.N, cnt, raw);
-    float v[NV][8];
+  for (; row < a.M; row += step) {
+    float v[NV][E];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) to_float<XB, 8>(raw[i], v[i]);
+    for (int i = 0; i < NV; ++i) to_float<XB, E>(next[i], v[i]);
+    if (row + step < a.M) load_row<XB, kShort>(x + (row + step) * a.ldx, a.N, p, next);
     float mean, rstd;
-    row_stats<T, NV>(v, cnt, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
-    elem_t<YB>* out = static_cast<elem_t<YB>*>(a.y) + row * a.ldy;
+    row_stats<kShort>(v, p, a.N, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[i][e] = fmaf((v[i][e] - mean) * rstd, g[i][e], b[i][e]);
-      if (cnt[i] == 8)
-        store_vec<YB, 8>(out + (t + i * T) * 8, v[i]);
-      else if (cnt[i] > 0)
-        store_part<YB, 8>(out + (t + i * T) * 8, v[i], cnt[i]);
-    }
+      for (int e = 0; e < E; ++e) v[i][e] = fmaf((v[i][e] - mean) * rstd, g[i][e], b[i][e]);
+    store_row<YB, kShort>(static_cast<elem_t<YB>*>(a.y) + row * a.ldy, a.N, p, v);
     if (a.stats && t == 0) {
       a.stats[row] = mean;
       a.stats[a.M + row] = rstd;
@@ -146,113 +187,107 @@ constexpr int kBwdThreads = 1024;
 // Each workgroup walks rows and keeps its columns' sums for dgamma and dbeta
 // in registers; its row groups are added in LDS in order and leave one pair
 // of partial rows, which norm_grad_kernel adds in order.
-template <bool XB, bool YB, bool DB, int T, int NV>
+template <bool XB, bool YB, bool DB, int T, int N8, bool kShort>
 __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
   constexpr int kGroups = kBwdThreads / T, kWaves = kBwdThreads / 64;
+  constexpr int E = XB && YB && DB ? 8 : 4, NV = N8 * 8 / E;
   __shared__ float red[2 * 2 * kWaves];
-  __shared__ float join[kGroups > 1 ? 2 * T * 8 * NV : 1];
+  __shared__ float join[kGroups > 1 ? 2 * T * 8 * N8 : 1];
   const int t = threadIdx.x % T, group = threadIdx.x / T;
-  int cnt[NV];
-  float g[NV][8], ag[NV][8], ab[NV][8];
+  const elem_t<XB>* x = static_cast<const elem_t<XB>*>(a.x);
+  const elem_t<YB>* dY = static_cast<const elem_t<YB>*>(a.dY);
+  const Place<T, NV, E> p(t, a.N);
+  // A row past the end reads as zeros: the barriers are reached either way.
+  const int64_t step = (int64_t)gridDim.x * kGroups;
+  float g[NV][E], ag[NV][E], ab[NV][E];
+  load_affine<kShort>(a.gamma, a.w_bf16, a.N, p, 1.0f, g);
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int left = a.N - (t + i * T) * 8;
-    cnt[i] = left < 0 ? 0 : left > 8 ? 8 : left;
+  for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      g[i][e] = 1.0f;
-      ag[i][e] = ab[i][e] = 0.0f;
-    }
-    if (a.gamma && cnt[i]) load_any_vec<8>(a.gamma, a.w_bf16, (t + i * T) * 8, cnt[i], g[i]);
-  }
+    for (int e = 0; e < E; ++e) ag[i][e] = ab[i][e] = 0.0f;
   const float invN = 1.0f / (float)a.N;
   int par = 0;
-  for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.M;
-       row0 += (int64_t)gridDim.x * kGroups) {
+  for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.M; row0 += step) {
     const int64_t row = row0 + group;
-    const bool live = row < a.M;  // the barriers below are reached either way
-    Vec<XB, 8> rx[NV];
-    Vec<YB, 8> ry[NV];
     float mean = 0.0f, rstd = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      rx[i] = zero_vec<XB, 8>();
-      ry[i] = zero_vec<YB, 8>();
+    if (a.stats && row < a.M) {
+      if (a.center) mean = a.stats[row];
+      rstd = a.stats[a.M + row];
     }
-    if (live) {
-      load_row<XB, NV, T>(static_cast<const elem_t<XB>*>(a.x) + row * a.ldx, t, a.N, cnt, rx);
-      load_row<YB, NV, T>(static_cast<const elem_t<YB>*>(a.dY) + row * a.ldy, t, a.N, cnt, ry);
-      if (a.stats) {
-        mean = a.center ? a.stats[row] : 0.0f;
-        rstd = a.stats[a.M + row];
+    Vec<XB, E> rx[NV];
+    Vec<YB, E> ry[NV];
+    if (row < a.M) {
+      load_row<XB, kShort>(x + row * a.ldx, a.N, p, rx);
+      load_row<YB, kShort>(dY + row * a.ldy, a.N, p, ry);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        rx[i] = zero_vec<XB, E>();
+        ry[i] = zero_vec<YB, E>();
       }
     }
-    float x[NV][8], dy[NV][8];
+    float d[NV][E], dy[NV][E];  // x, from below x - mean
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      to_float<XB, 8>(rx[i], x[i]);
-      to_float<YB, 8>(ry[i], dy[i]);
+      to_float<XB, E>(rx[i], d[i]);
+      to_float<YB, E>(ry[i], dy[i]);
     }
-    if (!a.stats) row_stats<T, NV>(x, cnt, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
+    if (!a.stats)
+      row_stats<kShort>(d, p, a.N, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
+    if (row >= a.M) rstd = 0.0f;  // of zeros; with eps = 0 it was infinite
+    // With xh = d rstd: dX = rstd (g - c1 - d (rstd c2)), c2 = rstd (sum g d) / N.
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[i][e] = (x[i][e] - mean) * rstd;
-        if (live) {
-          // columns past N hold dY = 0 but x = -mean rstd: they add nothing
-          ag[i][e] = fmaf(dy[i][e], x[i][e], ag[i][e]);
-          ab[i][e] += dy[i][e];
-        }
+      for (int e = 0; e < E; ++e) {
+        // Where there is no element or no row, dY is 0 and d finite (unless
+        // the row's own mean is not): it adds nothing.
+        d[i][e] -= mean;
+        ag[i][e] = fmaf(dy[i][e] * rstd, d[i][e], ag[i][e]);
+        ab[i][e] += dy[i][e];
         dy[i][e] *= g[i][e];
-        s[0] += dy[i][e];
-        s[1] = fmaf(dy[i][e], x[i][e], s[1]);
+        const float once = e >= p.skip[i] ? dy[i][e] : 0.0f;
+        s[0] += once;
+        s[1] = fmaf(once, d[i][e], s[1]);
       }
     if (a.dX) {
       group_reduce<T, 2>(s, red, kWaves, par, OpSum());
-      const float c1 = a.center ? s[0] * invN : 0.0f, c2 = s[1] * invN;
-      if (live) {
-        elem_t<DB>* out = static_cast<elem_t<DB>*>(a.dX) + row * a.lddx;
+      const float c1 = a.center ? s[0] * invN : 0.0f, k2 = s[1] * invN * rstd * rstd;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
+      for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) dy[i][e] = (dy[i][e] - c1 - x[i][e] * c2) * rstd;
-          if (cnt[i] == 8)
-            store_vec<DB, 8>(out + (t + i * T) * 8, dy[i]);
-          else if (cnt[i] > 0)
-            store_part<DB, 8>(out + (t + i * T) * 8, dy[i], cnt[i]);
-        }
-      }
+        for (int e = 0; e < E; ++e) dy[i][e] = fmaf(-d[i][e], k2, dy[i][e] - c1) * rstd;
+      if (row < a.M)
+        store_row<DB, kShort>(static_cast<elem_t<DB>*>(a.dX) + row * a.lddx, a.N, p, dy);
     }
   }
   if (!a.part) return;
   float* out = a.part + (int64_t)blockIdx.x * 2 * a.ldp;
   if constexpr (kGroups > 1) {
+#pragma unroll 1
     for (int k = 0; k < kGroups; ++k) {
       if (group == k) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int at = (t + i * T) * 8 + e;
+          for (int e = 0; e < E; ++e) {
+            // a moved-back vector's first elements are the neighbour's to add
+            if (e < p.skip[i] || (kShort && e >= a.N)) continue;
+            const int at = p.at[i] + e;
             join[at] = k ? join[at] + ag[i][e] : ag[i][e];
-            join[T * 8 * NV + at] = k ? join[T * 8 * NV + at] + ab[i][e] : ab[i][e];
+            join[T * 8 * N8 + at] = k ? join[T * 8 * N8 + at] + ab[i][e] : ab[i][e];
           }
       }
       __syncthreads();
     }
     for (int c = threadIdx.x; c < a.N; c += kBwdThreads) {
       out[c] = join[c];
-      out[a.ldp + c] = join[T * 8 * NV + c];
+      out[a.ldp + c] = join[T * 8 * N8 + c];
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (cnt[i]) {  // ldp is a multiple of eight
-        store_vec<false, 8>(out + (t + i * T) * 8, ag[i]);
-        store_vec<false, 8>(out + a.ldp + (t + i * T) * 8, ab[i]);
-      }
+    store_row<false, kShort>(out, a.N, p, ag);
+    store_row<false, kShort>(out + a.ldp, a.N, p, ab);
   }
 }
 
@@ -291,17 +326,22 @@ __global__ __launch_bounds__(256) void norm_grad_kernel(const float* part, int r
   }
 }
 
-template <bool XB, bool YB, int T, int NV>
+template <bool XB, bool YB, int T, int N8, bool kShort = false>
 hipError_t fwd(const NormFwd& a, hipStream_t st) {
   constexpr int kThreads = T < 256 ? 256 : T;
   const int64_t blocks = (a.M + kThreads / T - 1) / (kThreads / T);
-  const unsigned grid = (unsigned)(blocks < 4096 ? blocks : 4096);
-  hipLaunchKernelGGL((norm_fwd_kernel<XB, YB, T, NV>), dim3(grid), dim3(kThreads), 0, st, a);
+  // As many workgroups as the GPU holds at once, six of 256 threads a CU or one
+  // of 1024, each with its share of rows (4096 x 4096 bf16: 11.3 us, one row a
+  // workgroup 13.3 us; 1500 x 12000: 16.5 us, 20 us with a row or two each).
+  const int64_t most = kThreads == 256 ? 1536 : 256;
+  const unsigned grid = (unsigned)(blocks < most ? blocks : most);
+  hipLaunchKernelGGL((norm_fwd_kernel<XB, YB, T, N8, kShort>), dim3(grid), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 
 template <bool XB, bool YB>
 hipError_t fwd_width(const NormFwd& a, hipStream_t st) {
+  if (a.N < (XB && YB ? 8 : 4)) return fwd<XB, YB, 64, 1, true>(a, st);
   if (a.N <= 512) return fwd<XB, YB, 64, 1>(a, st);
   if (a.N <= 1024) return fwd<XB, YB, 64, 2>(a, st);
   if (a.N <= 2048) return fwd<XB, YB, 256, 1>(a, st);
@@ -310,22 +350,22 @@ hipError_t fwd_width(const NormFwd& a, hipStream_t st) {
   return fwd<XB, YB, 1024, 2>(a, st);
 }
 
+template <bool XB, bool YB, bool DB, int T, int N8, bool kShort = false>
+hipError_t bwd(const NormBwd& a, unsigned grid, hipStream_t st) {
+  hipLaunchKernelGGL((norm_bwd_kernel<XB, YB, DB, T, N8, kShort>), dim3(grid), dim3(kBwdThreads), 0,
+                     st, a);
+  return hipGetLastError();
+}
+
 template <bool XB, bool YB, bool DB>
 hipError_t bwd_width(const NormBwd& a, unsigned grid, hipStream_t st) {
-  const dim3 g(grid), b(kBwdThreads);
-  if (a.N <= 512)
-    hipLaunchKernelGGL((norm_bwd_kernel<XB, YB, DB, 64, 1>), g, b, 0, st, a);
-  else if (a.N <= 1024)
-    hipLaunchKernelGGL((norm_bwd_kernel<XB, YB, DB, 128, 1>), g, b, 0, st, a);
-  else if (a.N <= 2048)
-    hipLaunchKernelGGL((norm_bwd_kernel<XB, YB, DB, 256, 1>), g, b, 0, st, a);
-  else if (a.N <= 4096)
-    hipLaunchKernelGGL((norm_bwd_kernel<XB, YB, DB, 512, 1>), g, b, 0, st, a);
-  else if (a.N <= 8192)
-    hipLaunchKernelGGL((norm_bwd_kernel<XB, YB, DB, 1024, 1>), g, b, 0, st, a);
-  else
-    hipLaunchKernelGGL((norm_bwd_kernel<XB, YB, DB, 1024, 2>), g, b, 0, st, a);
-  return hipGetLastError();
+  if (a.N < (XB && YB && DB ? 8 : 4)) return bwd<XB, YB, DB, 64, 1, true>(a, grid, st);
+  if (a.N <= 512) return bwd<XB, YB, DB, 64, 1>(a, grid, st);
+  if (a.N <= 1024) return bwd<XB, YB, DB, 128, 1>(a, grid, st);
+  if (a.N <= 2048) return bwd<XB, YB, DB, 256, 1>(a, grid, st);
+  if (a.N <= 4096) return bwd<XB, YB, DB, 512, 1>(a, grid, st);
+  if (a.N <= 8192) return bwd<XB, YB, DB, 1024, 1>(a, grid, st);
+  return bwd<XB, YB, DB, 1024, 2>(a, grid, st);
 }
 
 int bwd_groups(int64_t N) {

@@ -221,13 +221,18 @@ __device__ __forceinline__ void group_reduce(float (&v)[K], float* red, int wave
       for (int k = 0; k < K; ++k) half[k * waves + wave] = v[k];
     }
     __syncthreads();
-    const int first = wave & ~(T / 64 - 1);
+    // lane l takes the value of wave l % W of its group; the W lanes join
+    constexpr int W = T / 64;
+    static_assert(W == 2 || W == 4 || W == 8 || W == 16, "waves of a group");
+    const int from = (wave & ~(W - 1)) + (threadIdx.x & (W - 1));
+#pragma unroll
+    for (int k = 0; k < K; ++k) v[k] = half[k * waves + from];
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      float s = half[k * waves + first];
-#pragma unroll
-      for (int w = 1; w < T / 64; ++w) s = op(s, half[k * waves + first + w]);
-      v[k] = s;
+      v[k] = op(v[k], dpp<0xB1>(v[k]));
+      if constexpr (W >= 4) v[k] = op(v[k], dpp<0x4E>(v[k]));
+      if constexpr (W >= 8) v[k] = op(v[k], dpp<0x141>(v[k]));
+      if constexpr (W >= 16) v[k] = op(v[k], dpp<0x140>(v[k]));
     }
     par ^= 1;
   }

@@ -177,6 +177,18 @@ def test_norm_of_awkward_rows():
         assert torch.isnan(dg).any()
 
 
+def test_norm_with_no_eps():
+    """eps = 0: the workgroups' row groups that have no row add nothing."""
+    x, dY, gamma, _ = norm_inputs(3, 100, 6, F32, F32, F32)
+    for center in (True, False):
+        dX, dg, db = q.qlora_norm_bwd(dY.to(DEV), x.to(DEV), gamma.to(DEV), eps=0.0,
+                                      norm=q.NORM_LAYER if center else q.NORM_RMS)
+        (wX, eX), (wg, eg), (wb, eb) = rows.norm_bwd(host(dY), host(x), host(gamma), 0.0, center)
+        check(dX, wX, eX, "dX")
+        check(dg, wg, eg, "dgamma")
+        check(db, wb, eb, "dbeta")
+
+
 def test_norm_without_rows():
     dX, dg, db = q.qlora_norm_bwd(torch.empty(0, 70, device=DEV), torch.empty(0, 70, device=DEV),
                                   grad_dtype=BF16)
