@@ -15,7 +15,6 @@ allocate belongs to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import numpy as np
@@ -369,7 +368,22 @@ def qlora_adamw_step(param: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Ten
 _FLOATS = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
 _INDEXES = {torch.int32: _lib.DTYPE_I32, torch.int64: _lib.DTYPE_I64}
 _F32 = (torch.float32,)
-_HERE = contextlib.nullcontext()
+
+
+class _Here:
+    """The context of a call that stays where it is."""
+
+    __slots__ = ()
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *error):
+        return None
+
+
+_HERE = _Here()
+_device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _place(t, stream):
@@ -381,7 +395,7 @@ def _place(t, stream):
         if stream.device != dev:
             raise ValueError(f"stream on {stream.device}, tensors on {dev}")
         return torch.cuda.stream(stream)
-    return _HERE if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE if dev.index == _device_now() else torch.cuda.device(dev)
 
 
 def _at(t):
@@ -485,7 +499,8 @@ def qlora_embed_fwd(W: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
             ldo = _matrix(out, "out", (M, D), dev)
         st = _lib.load().qlora_embed_fwd(_at(W), ldw, _FLOATS[W.dtype], V, D, _at(ids), ids_dtype,
                                          M, scale, _at(out), ldo, _FLOATS[out.dtype], _here(dev))
-    _lib.check(st, "qlora_embed_fwd")
+    if st:
+        _lib.check(st, "qlora_embed_fwd")
     return out
 
 
@@ -510,7 +525,8 @@ def qlora_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 
         st = _lib.load().qlora_embed_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(ids), ids_dtype, M, V,
                                          D, scale, _at(dW), _FLOATS[dW.dtype], int(accumulate),
                                          _at(workspace), workspace.numel(), _here(dev))
-    _lib.check(st, "qlora_embed_bwd")
+    if st:
+        _lib.check(st, "qlora_embed_bwd")
     return dW
 
 
@@ -548,7 +564,8 @@ def qlora_norm_fwd(x: torch.Tensor, gamma: torch.Tensor | None = None,
         st = _lib.load().qlora_norm_fwd(_at(x), ldx, _FLOATS[x.dtype], M, N, norm, _at(gamma),
                                         _at(beta), w_dtype, eps, _at(y), ldy, _FLOATS[y.dtype],
                                         _at(stats_out), _here(dev))
-    _lib.check(st, "qlora_norm_fwd")
+    if st:
+        _lib.check(st, "qlora_norm_fwd")
     return y
 
 
@@ -582,7 +599,8 @@ def qlora_norm_bwd(dY: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None
                                         _at(stats), _at(dX), N, _FLOATS[dx_dtype], _at(dgamma),
                                         _at(dbeta), _FLOATS[grad_dtype], _at(workspace),
                                         0 if workspace is None else workspace.numel(), _here(dev))
-    _lib.check(st, "qlora_norm_bwd")
+    if st:
+        _lib.check(st, "qlora_norm_bwd")
     return dX, dgamma, dbeta
 
 
@@ -619,7 +637,8 @@ def qlora_distill_fwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: t
         st = _lib.load().qlora_distill_fwd(*heads, temperature, _at(loss), _at(stats_out),
                                            _at(workspace),
                                            0 if workspace is None else workspace.numel(), _here(dev))
-    _lib.check(st, "qlora_distill_fwd")
+    if st:
+        _lib.check(st, "qlora_distill_fwd")
     return loss
 
 
@@ -641,5 +660,6 @@ def qlora_distill_bwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: t
             ldg = _matrix(dlogits, "dlogits", (M, V), dev)
         st = _lib.load().qlora_distill_bwd(*heads, temperature, _at(stats), _at(dloss),
                                            _at(dlogits), ldg, _FLOATS[dlogits.dtype], _here(dev))
-    _lib.check(st, "qlora_distill_bwd")
+    if st:
+        _lib.check(st, "qlora_distill_bwd")
     return dlogits
