@@ -133,7 +133,7 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormFwd a) 
   constexpr int kThreads = T < 256 ? 256 : T;
   constexpr int kGroups = kThreads / T, kWaves = kThreads / 64;
   constexpr int E = XB && YB ? 8 : 4, NV = N8 * 8 / E;
-  __shared__ float red[2 * kWaves];
+  __shared__ float red[2 * kMostReduced * kWaves];
   const int t = threadIdx.x % T;
   const int64_t step = (int64_t)gridDim.x * kGroups;
   int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T;
@@ -191,7 +191,7 @@ template <bool XB, bool YB, bool DB, int T, int N8, bool kShort>
 __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
   constexpr int kGroups = kBwdThreads / T, kWaves = kBwdThreads / 64;
   constexpr int E = XB && YB && DB ? 8 : 4, NV = N8 * 8 / E;
-  __shared__ float red[2 * 2 * kWaves];
+  __shared__ float red[2 * kMostReduced * kWaves];
   __shared__ float join[kGroups > 1 ? 2 * T * 8 * N8 : 1];
   const int t = threadIdx.x % T, group = threadIdx.x / T;
   const elem_t<XB>* x = static_cast<const elem_t<XB>*>(a.x);

@@ -204,10 +204,13 @@ __device__ __forceinline__ float wave_reduce(float v, Op op) {
 }
 
 // K values reduced over the T threads of a group of a workgroup (T a multiple
-// of 64; `red` holds 2 * K * (waves of the workgroup) floats). The two halves
-// of `red` are used in turn (`par`), so one barrier a reduction is enough: a
+// of 64). `red` holds two halves of kMostReduced values for each wave of the
+// workgroup, used in turn (`par`), so one barrier a reduction is enough: a
 // wave writes a half again only after a barrier that every wave reaches once
-// it has read it. All threads of the workgroup call it.
+// it has read it. The halves lie at the same places whatever K is: reductions
+// of one and of two values follow each other. All threads of the workgroup
+// call it.
+constexpr int kMostReduced = 2;
 template <int T, int K, typename Op>
 __device__ __forceinline__ void group_reduce(float (&v)[K], float* red, int waves, int& par,
                                              Op op) {
@@ -215,7 +218,8 @@ __device__ __forceinline__ void group_reduce(float (&v)[K], float* red, int wave
   for (int k = 0; k < K; ++k) v[k] = wave_reduce(v[k], op);
   if constexpr (T > 64) {
     const int wave = threadIdx.x >> 6;
-    float* half = red + par * K * waves;
+    static_assert(K <= kMostReduced, "values of a reduction");
+    float* half = red + par * kMostReduced * waves;
     if ((threadIdx.x & 63) == 0) {
 #pragma unroll
       for (int k = 0; k < K; ++k) half[k * waves + wave] = v[k];

@@ -233,3 +233,25 @@ def test_python_argument_checks():
             c()
             pytest.fail(f"case {i} was accepted")
     assert f is torch.float32
+
+
+def test_reductions_in_turn_use_places_of_their_own():
+    """A workgroup's reductions of one and two values follow each other with a
+    barrier each. Replayed on the host: what a wave may write before the others
+    have passed the reduction's barrier is nothing that they may still read."""
+    import os
+    import re
+
+    root = os.path.dirname(os.path.dirname(os.path.abspath(q.__file__)))
+    src = open(os.path.join(root, "qlora_fine_tuning_blockwise_amd", "csrc", "rows.h")).read()
+    most = int(re.search(r"constexpr int kMostReduced = (\d+);", src).group(1))
+    expr = re.search(r"float\* half = red \+ par \* ([^;]+);", src).group(1)
+    for waves in (2, 4, 8, 16):
+        for sizes in ((1, 1, 2), (1, 2), (1, 1, 2, 1, 1, 2), (2, 1, 2, 1), (2, 2, 2)):
+            read, par = set(), 0
+            for k in sizes * 3:
+                base = par * eval(expr, {"kMostReduced": most, "waves": waves, "K": k})
+                place = set(range(base, base + k * waves))
+                assert not place & read, (waves, sizes)
+                assert max(place) < 2 * most * waves
+                read, par = place, par ^ 1
