@@ -121,6 +121,7 @@ extern "C" {
 
 /* Limits of the row operators (QLORA_ERR_SHAPE beyond them). */
 #define QLORA_MAX_ROWS (1 << 24)       /* rows or tokens of a call */
+#define QLORA_MAX_SORTED (1 << 20)     /* tokens of qlora_embed_bwd */
 #define QLORA_MAX_NORM_WIDTH 16384     /* elements of a normed row */
 #define QLORA_MAX_TOP 1024             /* teacher entries of a row */
 
@@ -428,7 +429,7 @@ int qlora_embed_fwd(const void* W, int64_t ldw, int w_dtype, int64_t V, int64_t 
                     int64_t ldo, int out_dtype, void* stream);
 
 /* Device workspace, in bytes, of qlora_embed_bwd. Host only; 0 on invalid
- * sizes. */
+ * sizes (M above QLORA_MAX_SORTED among them). */
 size_t qlora_embed_bwd_workspace_bytes(int64_t M, int64_t D);
 
 /* Gradient of the embedding's table, dense:
@@ -437,8 +438,9 @@ size_t qlora_embed_bwd_workspace_bytes(int64_t M, int64_t D);
  *   do not occur. accumulate != 0: the sums are added to dW instead (one
  *   rounding), and rows whose id does not occur are left as they were.
  * Tokens whose id lies outside of [0, V) add nothing, and their dY is not
- * read. Errors as qlora_embed_fwd; QLORA_ERR_WORKSPACE for a workspace
- * smaller than qlora_embed_bwd_workspace_bytes(M, D). */
+ * read. Errors as qlora_embed_fwd, with M <= QLORA_MAX_SORTED;
+ * QLORA_ERR_WORKSPACE for a workspace smaller than
+ * qlora_embed_bwd_workspace_bytes(M, D). */
 int qlora_embed_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* ids, int ids_dtype,
                     int64_t M, int64_t V, int64_t D, float scale, void* dW, int grad_dtype,
                     int accumulate, void* workspace, size_t workspace_bytes, void* stream);

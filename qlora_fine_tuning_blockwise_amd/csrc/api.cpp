@@ -682,7 +682,7 @@ int qlora_embed_fwd(const void* W, int64_t ldw, int w_dtype, int64_t V, int64_t 
 }
 
 size_t qlora_embed_bwd_workspace_bytes(int64_t M, int64_t D) {
-  if (M < 0 || M > QLORA_MAX_ROWS || D < 1 || D > kMaxEmbedWidth) return 0;
+  if (M < 0 || M > QLORA_MAX_SORTED || D < 1 || D > kMaxEmbedWidth) return 0;
   return embed_layout(M, D).total;
 }
 
@@ -690,7 +690,8 @@ int qlora_embed_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* ids, 
                     int64_t M, int64_t V, int64_t D, float scale, void* dW, int grad_dtype,
                     int accumulate, void* workspace, size_t workspace_bytes, void* stream) {
   if (M < 0 || !std::isfinite(scale)) return QLORA_ERR_INVALID_ARG;
-  if (!embed_shape_ok(V, D) || M > QLORA_MAX_ROWS || !stride_ok(M, D, ldy)) return QLORA_ERR_SHAPE;
+  if (!embed_shape_ok(V, D) || M > QLORA_MAX_SORTED || !stride_ok(M, D, ldy))
+    return QLORA_ERR_SHAPE;
   if (!float_type(dy_dtype) || !index_type(ids_dtype) || !float_type(grad_dtype))
     return QLORA_ERR_DTYPE;
   if (!dW || (M > 0 && (!dY || !ids))) return QLORA_ERR_INVALID_ARG;

@@ -368,6 +368,8 @@ hipError_t fwd(const EmbedFwd& a, hipStream_t st) {
   return hipGetLastError();
 }
 
+// At most 2^20 tokens (QLORA_MAX_SORTED): 2^15 tiles, within a grid's second
+// dimension.
 template <bool YB, bool GB>
 hipError_t sums(const EmbedBwd& a, hipStream_t st) {
   const unsigned tiles = (unsigned)((a.M + a.tile - 1) / a.tile);

@@ -421,6 +421,93 @@ def test_distill_gradient_by_differences():
     assert abs((host(dz) * d).sum() - want) <= tol
 
 
+# ------------------------------------------------------------ far addresses
+def test_offsets_past_32_bits():
+    """Rows that lie past 2^32 bytes and 2^31 elements in their buffers: a table
+    of 4.9 GB and its gradient, and views of two rows 2^31 + 24 elements apart."""
+    g = np.random.default_rng(12)
+    V, D = 600_000, 4096
+    say("far table")
+    table = torch.empty(V, D, dtype=BF16, device=DEV)
+    ids = torch.tensor([V - 1, 0, V - 2, V - 1, V], device=DEV)
+    W = randn(g, (2, D), BF16)
+    table[0], table[V - 2:] = W[0].to(DEV), W.to(DEV)
+    out = q.qlora_embed_fwd(table, ids)
+    assert torch.equal(out[0], W[1].to(DEV)) and torch.equal(out[1], W[0].to(DEV))
+    assert torch.equal(out[2], W[0].to(DEV)) and not out[4].any()
+    dY = randn(g, (5, D), BF16)
+    dW = q.qlora_embed_bwd(dY.to(DEV), ids, V, dW=table)
+    want, err = rows.embed_bwd(host(dY), np.array([2, 0, 1, 2, 3]), 3, 1.0)
+    check(dW[[0, V - 2, V - 1]], want, err, "dW")
+    assert not dW[1:V - 2].any()
+    del table, dW
+    say("far rows")
+    ld = (1 << 31) + 24
+    buf = torch.empty(ld + 4096, dtype=BF16, device=DEV)
+
+    def far(t):
+        v = buf.as_strided(t.shape, (ld, 1))
+        v.copy_(t)
+        return v
+    x, dy = randn(g, (2, 1000), BF16), randn(g, (2, 1000), BF16)
+    y = q.qlora_norm_fwd(far(x))
+    want, err, _, _ = rows.norm_fwd(host(x), None, None, 1e-5, True)
+    check(y, want, err, "y")
+    dX, _, _ = q.qlora_norm_bwd(dy.to(DEV), far(x))
+    (wX, eX), _, _ = rows.norm_bwd(host(dy), host(x), None, 1e-5, True)
+    check(dX, wX, eX, "dX")
+    top, t = torch.tensor([[3, 999], [0, 1]]), randn(g, (2, 2))
+    stats = torch.empty(2, 2, device=DEV)
+    loss = q.qlora_distill_fwd(far(x), top.to(DEV), t.to(DEV), stats_out=stats)
+    want, err, _, _ = rows.distill_fwd(host(x), host(top), host(t), 1.0)
+    check(loss, want, err, "loss")
+    got = q.qlora_distill_bwd(x.to(DEV), top.to(DEV), t.to(DEV), torch.ones(2, device=DEV), stats,
+                              dlogits=buf.as_strided((2, 1000), (ld, 1)))
+    want, err = rows.distill_bwd(host(x), host(top), host(t), np.ones(2), 1.0)
+    check(got, want, err, "dlogits")
+    dW = q.qlora_embed_bwd(far(dy), torch.tensor([1, 1], device=DEV), 2)
+    want, err = rows.embed_bwd(host(dy), np.array([1, 1]), 2, 1.0)
+    check(dW, want, err, "dW")
+
+
+def test_many_rows():
+    """More rows than a launch has workgroups: every kernel's loop over rows."""
+    M, g = 70001, np.random.default_rng(13)
+    say("many rows")
+    z, t = randn(g, (M, 24), BF16), randn(g, (M, 3))
+    ids = torch.from_numpy(g.integers(-1, 24, (M, 3)))
+    dl = torch.from_numpy(g.standard_normal(M).astype(np.float32))
+    stats = torch.empty(2, M, device=DEV)
+    args = (z.to(DEV), ids.to(DEV), t.to(DEV))
+    loss = q.qlora_distill_fwd(*args, stats_out=stats)
+    dz = q.qlora_distill_bwd(*args, dl.to(DEV), stats, grad_dtype=F32)
+    want, err, _, _ = rows.distill_fwd(host(z), host(ids), host(t), 1.0)
+    check(loss, want, err, "loss")
+    want, err = rows.distill_bwd(host(z), host(ids), host(t), host(dl), 1.0)
+    check(dz, want, err, "dlogits")
+    W = randn(g, (50, 24), BF16)
+    tok = torch.from_numpy(g.integers(-1, 51, M))
+    out = q.qlora_embed_fwd(W.to(DEV), tok.to(DEV), out_dtype=F32)
+    want, err = rows.embed_fwd(host(W), host(tok), 1.0)
+    check(out, want, err, "out")
+    dW = q.qlora_embed_bwd(z.to(DEV), tok.to(DEV), 50)
+    want, err = rows.embed_bwd(host(z), host(tok), 50, 1.0)
+    check(dW, want, err, "dW")
+    # rows cut into more pieces than a launch has workgroups
+    M, V = 9001, 70000
+    z = torch.randn(M, V, device=DEV, dtype=BF16)
+    ids, t = torch.randint(0, V, (M, 2), device=DEV), torch.randn(M, 2, device=DEV)
+    stats = torch.empty(2, M, device=DEV)
+    loss = q.qlora_distill_fwd(z, ids, t, stats_out=stats)
+    dz = q.qlora_distill_bwd(z, ids, t, torch.ones(M, device=DEV), stats)
+    for m in (0, 4500, 9000):
+        r = slice(m, m + 1)
+        want, err, _, _ = rows.distill_fwd(host(z[r]), host(ids[r]), host(t[r]), 1.0)
+        check(loss[r], want, err, "loss")
+        want, err = rows.distill_bwd(host(z[r]), host(ids[r]), host(t[r]), np.ones(1), 1.0)
+        check(dz[r], want, err, "dlogits")
+
+
 # ------------------------------------------------------------- a step of them
 class Step:
     """Embedding, norm, a quantized linear layer with its adapter, a second one

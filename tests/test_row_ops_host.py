@@ -133,6 +133,9 @@ def test_embed_bwd_validation(lib):
     assert q.qlora_embed_bwd_workspace_bytes(-1, 64) == 0
     assert q.qlora_embed_bwd_workspace_bytes(8, 0) == 0
     assert q.qlora_embed_bwd_workspace_bytes(0, 64) == 0
+    # more tokens than the second grid dimension has tiles for
+    assert call(5, (1 << 20) + 1) == 2 and q.qlora_embed_bwd_workspace_bytes((1 << 20) + 1, 64) == 0
+    assert q.qlora_embed_bwd_workspace_bytes(1 << 20, 64) > 0
 
 
 def test_norm_validation(lib):
