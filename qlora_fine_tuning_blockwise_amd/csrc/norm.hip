@@ -14,6 +14,11 @@
 //
 // T threads hold a row (NV vectors of E elements each, T vectors apart, so that
 // a wave's access is one run); a wave alone needs no barrier.
+//
+// Memory bounds the forward: 4096 x 4096 bf16 moves 67 MB in 11.3 us (5.9 TB/s;
+// a copy of that size reaches 5.7 to 6.0). One row alone takes 2.9 us, of which
+// a launch is 2. The squares of the deviations are summed in fp32, so a row's
+// values stay below 2^60.
 #include <type_traits>
 
 #include "rows.h"
@@ -115,6 +120,9 @@ __device__ __forceinline__ void row_stats(const float (&v)[NV][E], const Place<T
   rstd = 1.0f / __builtin_sqrtf(s[0] * invN + eps);
 }
 
+// A workgroup is one row's threads, or four waves with a row each.
+constexpr int fwd_threads(int T) { return T == 64 ? 256 : T; }
+
 struct NormFwd {
   const void* x;
   int64_t ldx, M;
@@ -129,15 +137,15 @@ struct NormFwd {
 };
 
 template <bool XB, bool YB, int T, int N8, bool kShort>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void norm_fwd_kernel(NormFwd a) {
-  constexpr int kThreads = T < 256 ? 256 : T;
+__global__ __launch_bounds__(fwd_threads(T)) void norm_fwd_kernel(NormFwd a) {
+  constexpr int kThreads = fwd_threads(T);
   constexpr int kGroups = kThreads / T, kWaves = kThreads / 64;
   constexpr int E = XB && YB ? 8 : 4, NV = N8 * 8 / E;
   __shared__ float red[2 * kMostReduced * kWaves];
   const int t = threadIdx.x % T;
   const int64_t step = (int64_t)gridDim.x * kGroups;
   int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / T;
-  if (row >= a.M) return;  // of a group of one wave: there are no barriers then
+  if (row >= a.M) return;  // of four waves with a row each: they have no barriers
   const elem_t<XB>* x = static_cast<const elem_t<XB>*>(a.x);
   const Place<T, NV, E> p(t, a.N);
   Vec<XB, E> next[NV];
@@ -184,9 +192,16 @@ struct NormBwd {
 
 constexpr int kBwdThreads = 1024;
 
-// Each workgroup walks rows and keeps its columns' sums for dgamma and dbeta
-// in registers; its row groups are added in LDS in order and leave one pair
-// of partial rows, which norm_grad_kernel adds in order.
+// Each workgroup, one a CU, walks rows and keeps its columns' sums for dgamma
+// and dbeta in registers; its row groups are added in LDS in order and leave
+// one pair of partial rows, which norm_grad_kernel adds in order.
+//
+// Memory bounds it: 2048 x 8192 bf16 moves 101 MB and 17 MB of partial rows in
+// 21 us (5.6 TB/s); norm_grad_kernel and the gap before it take 6 us more.
+// Loads of the next row in flight (16 more registers) changed nothing there,
+// nor did a quarter fewer vector instructions; two workgroups a CU double the
+// partial rows (37 us). Nontemporal stores of dX are 3 us faster alone and cost
+// the kernel that reads dX next 4.5 us, so the stores are plain.
 template <bool XB, bool YB, bool DB, int T, int N8, bool kShort>
 __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
   constexpr int kGroups = kBwdThreads / T, kWaves = kBwdThreads / 64;
@@ -197,7 +212,6 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
   const elem_t<XB>* x = static_cast<const elem_t<XB>*>(a.x);
   const elem_t<YB>* dY = static_cast<const elem_t<YB>*>(a.dY);
   const Place<T, NV, E> p(t, a.N);
-  // A row past the end reads as zeros: the barriers are reached either way.
   const int64_t step = (int64_t)gridDim.x * kGroups;
   float g[NV][E], ag[NV][E], ab[NV][E];
   load_affine<kShort>(a.gamma, a.w_bf16, a.N, p, 1.0f, g);
@@ -219,7 +233,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
     if (row < a.M) {
       load_row<XB, kShort>(x + row * a.ldx, a.N, p, rx);
       load_row<YB, kShort>(dY + row * a.ldy, a.N, p, ry);
-    } else {
+    } else {  // zeros: the barriers are reached either way
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         rx[i] = zero_vec<XB, E>();
@@ -328,26 +342,33 @@ __global__ __launch_bounds__(256) void norm_grad_kernel(const float* part, int r
 
 template <bool XB, bool YB, int T, int N8, bool kShort = false>
 hipError_t fwd(const NormFwd& a, hipStream_t st) {
-  constexpr int kThreads = T < 256 ? 256 : T;
+  constexpr int kThreads = fwd_threads(T);
   const int64_t blocks = (a.M + kThreads / T - 1) / (kThreads / T);
   // As many workgroups as the GPU holds at once, six of 256 threads a CU or one
-  // of 1024, each with its share of rows (4096 x 4096 bf16: 11.3 us, one row a
+  // of 512, each with its share of rows (4096 x 4096 bf16: 11.3 us, one row a
   // workgroup 13.3 us; 1500 x 12000: 16.5 us, 20 us with a row or two each).
-  const int64_t most = kThreads == 256 ? 1536 : 256;
+  const int64_t most = kThreads <= 256 ? 1536 * 256 / kThreads : 256;
   const unsigned grid = (unsigned)(blocks < most ? blocks : most);
   hipLaunchKernelGGL((norm_fwd_kernel<XB, YB, T, N8, kShort>), dim3(grid), dim3(kThreads), 0, st, a);
   return hipGetLastError();
 }
 
+// Threads of a row and elements of a thread (in eights): few threads with more
+// elements each, as long as the registers hold them, since a row's reductions
+// and barriers cost every wave the same. Measured on bf16 rows of 33.5 MB, us:
+//   N =   512:  64 x 1 13.3, 128 x 1 19.6       N =  4096: 256 x 2 12.9, 512 x 1 18.8
+//   N =  1024:  64 x 2 13.1, 128 x 1 14.4       N =  8192: 256 x 4 24.9, 512 x 2 25.1,
+//   N =  2048: 128 x 2 12.8, 256 x 1 14.3,                 1024 x 1 34.0 (67 MB)
+//               64 x 4 15.2                     N = 16384: 512 x 4 25.2, 1024 x 2 27.0 (67 MB)
 template <bool XB, bool YB>
 hipError_t fwd_width(const NormFwd& a, hipStream_t st) {
   if (a.N < (XB && YB ? 8 : 4)) return fwd<XB, YB, 64, 1, true>(a, st);
   if (a.N <= 512) return fwd<XB, YB, 64, 1>(a, st);
   if (a.N <= 1024) return fwd<XB, YB, 64, 2>(a, st);
-  if (a.N <= 2048) return fwd<XB, YB, 256, 1>(a, st);
+  if (a.N <= 2048) return fwd<XB, YB, 128, 2>(a, st);
   if (a.N <= 4096) return fwd<XB, YB, 256, 2>(a, st);
   if (a.N <= 8192) return fwd<XB, YB, 256, 4>(a, st);
-  return fwd<XB, YB, 1024, 2>(a, st);
+  return fwd<XB, YB, 512, 4>(a, st);
 }
 
 template <bool XB, bool YB, bool DB, int T, int N8, bool kShort = false>
@@ -357,6 +378,11 @@ hipError_t bwd(const NormBwd& a, unsigned grid, hipStream_t st) {
   return hipGetLastError();
 }
 
+// Threads of a row, eight elements each while 1024 threads hold the row; more
+// elements a thread leave too few registers. Measured, us: 32768 x 512 64 x 1
+// 31.9, 128 x 1 32.1, 256 x 1 46; 16384 x 1024 128 x 1 28.4, 64 x 2 50, 256 x 1
+// 31.0; 8192 x 2048 256 x 1 26.3, 128 x 2 41, 512 x 1 29.9; 4096 x 4096 512 x 1
+// 27.2, 256 x 2 40; 2048 x 8192 1024 x 1 27.6, 512 x 2 39.
 template <bool XB, bool YB, bool DB>
 hipError_t bwd_width(const NormBwd& a, unsigned grid, hipStream_t st) {
   if (a.N < (XB && YB && DB ? 8 : 4)) return bwd<XB, YB, DB, 64, 1, true>(a, grid, st);
