@@ -221,23 +221,51 @@ struct EmbedBwd {
   int ldp, tile;
 };
 
+// The columns of a lane: a whole vector, moved back where it would pass the
+// row's end. Its elements below `first` are then another lane's too and are
+// read, but only [first, n) are written (an accumulated element is written
+// once). n = 0: none; a row shorter than a vector is all of lane 0's.
+template <int E>
+struct Columns {
+  int at, first, n;
+  __device__ __forceinline__ Columns(int c, int D) {
+    at = c + E <= D || D < E ? c : D - E;
+    first = c - at < E ? c - at : E;
+    n = c >= D ? 0 : D < E ? D : E;
+  }
+  __device__ __forceinline__ bool whole() const { return first == 0 && n == E; }
+};
+
+template <bool kBf16, int E>
+__device__ __forceinline__ Vec<kBf16, E> load_columns(const elem_t<kBf16>* row, const Columns<E>& c,
+                                                      int D) {
+  if (c.n == 0) return zero_vec<kBf16, E>();
+  return D < E ? load_part<kBf16, E>(row + c.at, c.n) : load_vec<kBf16, E>(row + c.at);
+}
+
+template <bool kBf16, int E>
+__device__ __forceinline__ void store_columns(elem_t<kBf16>* row, const Columns<E>& c,
+                                              const float (&v)[E]) {
+  if (c.whole())
+    store_vec<kBf16, E>(row + c.at, v);
+  else
+    store_part<kBf16, E>(row + c.at, v, c.n, c.first);
+}
+
 template <bool GB, int E>
-__device__ __forceinline__ void write_row(const EmbedBwd& a, int32_t id, int c, int n,
+__device__ __forceinline__ void write_row(const EmbedBwd& a, int32_t id, const Columns<E>& c,
                                           const float (&acc)[E]) {
-  elem_t<GB>* p = static_cast<elem_t<GB>*>(a.dW) + (int64_t)id * a.D + c;
+  elem_t<GB>* p = static_cast<elem_t<GB>*>(a.dW) + (int64_t)id * a.D;
   float v[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) v[e] = acc[e] * a.scale;
   if (a.accumulate) {
     float old[E];
-    to_float<GB, E>(n >= E ? load_vec<GB, E>(p) : load_part<GB, E>(p, n), old);
+    to_float<GB, E>(load_columns<GB, E>(p, c, a.D), old);
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] += old[e];
   }
-  if (n >= E)
-    store_vec<GB, E>(p, v);
-  else
-    store_part<GB, E>(p, v, n);
+  store_columns<GB, E>(p, c, v);
 }
 
 // Wave (64 E columns, tile). The loads of kRows rows fly together.
@@ -260,9 +288,8 @@ __global__ __launch_bounds__(64) void embed_sum_kernel(EmbedBwd a) {
   // bit i: the sum that token i belongs to ends with it
   const uint64_t ends = __ballot(lane < n && (lane + 1 < size ? next : after) != key);
   bool open = __builtin_amdgcn_readfirstlane(key) == before;  // the sum began before the tile
-  const int c = ((int)blockIdx.x * 64 + lane) * E;
-  const int left = count_below<E>(c, a.D);
-  const elem_t<YB>* dY = static_cast<const elem_t<YB>*>(a.dY) + c;
+  const Columns<E> c(((int)blockIdx.x * 64 + lane) * E, a.D);
+  const elem_t<YB>* dY = static_cast<const elem_t<YB>*>(a.dY);
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
@@ -271,9 +298,7 @@ __global__ __launch_bounds__(64) void embed_sum_kernel(EmbedBwd a) {
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {  // behind the last token its row again
       const int i = i0 + u < n ? i0 + u : n - 1;
-      const elem_t<YB>* p = dY + (int64_t)__builtin_amdgcn_readlane(pos, i) * a.ldy;
-      r[u] = left == E ? load_vec<YB, E>(p) : zero_vec<YB, E>();
-      if (a.D % E && left > 0 && left < E) r[u] = load_part<YB, E>(p, left);
+      r[u] = load_columns<YB, E>(dY + (int64_t)__builtin_amdgcn_readlane(pos, i) * a.ldy, c, a.D);
     }
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
@@ -286,10 +311,10 @@ __global__ __launch_bounds__(64) void embed_sum_kernel(EmbedBwd a) {
       const bool end = ends >> i & 1;
       if (!end && i + 1 < size) continue;
       if (end && !open) {
-        if (left > 0) write_row<GB, E>(a, __builtin_amdgcn_readlane(key, i), c, left, acc);
+        if (c.n) write_row<GB, E>(a, __builtin_amdgcn_readlane(key, i), c, acc);
       } else {
         // a sum that covers the whole tile counts as one that began before it
-        if (left > 0) store_vec<false, E>(a.part + (tile * 2 + (open ? 0 : 1)) * a.ldp + c, acc);
+        if (c.n) store_columns<false, E>(a.part + (tile * 2 + (open ? 0 : 1)) * a.ldp, c, acc);
         if (!open && blockIdx.x == 0 && lane == 0)
           a.list[1 + atomicAdd(a.list, 1)] = (int32_t)tile;  // its order does not matter
       }
@@ -307,8 +332,8 @@ template <bool GB>
 __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedBwd a) {
   __shared__ float join[kJoinWaves][64 * 4];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int c = ((int)blockIdx.x * 64 + lane) * 4;
-  const int left = count_below<4>(c, a.D);
+  const int col = ((int)blockIdx.x * 64 + lane) * 4;  // the workspace's rows are whole vectors
+  const Columns<4> c(col, a.D);
   const int sums = a.list[0];
   for (int at = blockIdx.y; at < sums; at += gridDim.y) {
     const int64_t tile = a.list[1 + at];
@@ -325,8 +350,8 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedBwd a)
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     const int64_t per = (n + kJoinWaves - 1) / kJoinWaves;
     const int64_t stop = (wave + 1) * per < n ? (wave + 1) * per : n;
-    if (left > 0) {
-      const float* p = a.part + (tile + 1) * 2 * a.ldp + c;
+    if (c.n) {
+      const float* p = a.part + (tile + 1) * 2 * a.ldp + c.at;
       for (int64_t i0 = wave * per; i0 < stop; i0 += 8) {
         Vec<false, 4> r[8];
 #pragma unroll
@@ -344,13 +369,13 @@ __global__ __launch_bounds__(64 * kJoinWaves) void embed_join_kernel(EmbedBwd a)
 #pragma unroll
     for (int e = 0; e < 4; ++e) join[wave][lane * 4 + e] = acc[e];
     __syncthreads();
-    if (wave == 0 && left > 0) {
+    if (wave == 0 && c.n) {
       float v[4];
-      to_float<false, 4>(load_vec<false, 4>(a.part + (tile * 2 + 1) * a.ldp + c), v);
+      to_float<false, 4>(load_vec<false, 4>(a.part + (tile * 2 + 1) * a.ldp + c.at), v);
       for (int w = 0; w < kJoinWaves; ++w)
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] += join[w][lane * 4 + e];
-      write_row<GB, 4>(a, id, c, left, v);
+      write_row<GB, 4>(a, id, c, v);
     }
     __syncthreads();  // `join` is written anew for the next sum
   }
@@ -392,7 +417,8 @@ hipError_t sums(const EmbedBwd& a, hipStream_t st) {
 // one tile, so that nothing is left to join (20 tokens of 4096 columns: 14.3
 // against 16.8 us); above, shorter tiles give more waves and longer ones fewer
 // parts (tiles of 8, 16 and 32: 4096 x 256 24.8, 24.1 and 27.6 us, 16000 x 1024
-// 54, 46 and 44 us, 32768 x 2048 109, 98 and 96 us).
+// 54, 46 and 44 us, 32768 x 2048 109, 98 and 96 us; by the count of waves
+// instead, 16000 x 64 would take 36 us with tiles of 8 against 30 us).
 int embed_tile(int64_t M) { return M <= 32 ? 32 : M <= 4096 ? 16 : 32; }
 
 hipError_t launch_embed_fwd(const void* W, int64_t ldw, bool w_bf16, int64_t V, int64_t D,
