@@ -37,6 +37,13 @@ constexpr float kLog2e = 1.44269504088896340736f;
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
+// s exp(v): the hardware's exponential flushes results below 2^-126 to zero,
+// the square of the root keeps them.
+__device__ __forceinline__ float scaled_exp(float s, float v) {
+  const float h = exp2_fast(v * (0.5f * kLog2e));
+  return s * h * h;
+}
+
 struct Teacher {
   const void* ids;
   const void* t;
@@ -160,16 +167,17 @@ __device__ __forceinline__ void take(MaxSum& a, const Vec<ZB, E> (&q)[U], float 
 #pragma unroll
   for (int u = 0; u < U; ++u) s[u] = 0.0f;
   float fix = 1.0f;
-  if (__builtin_fabsf(base) <= 0x1p64f) {
+  const float bc = base * c;
+  if (__builtin_fabsf(bc) <= 0x1p20f) {
     // (v - base) c as one operation: v c - base c, whose second term is rounded
-    // alike for all of them; the rounding is taken out of the sum.
-    const float bc = base * c;
+    // alike for all of them, by 2^-4 at most; the rounding is taken out of the
+    // sum.
     fix = exp2_fast(-fmaf(base, c, -bc));
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int e = 0; e < E; ++e) s[u] += exp2_fast(fmaf(v[u][e], c, -bc));
-  } else {  // base c may not be finite
+  } else {  // base c is large against its rounding, or not finite
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -390,7 +398,7 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillBwd a) {
         float v[E];
         to_float<ZB, E>(q[u], v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = scale * exp2_fast(fmaf(v[e] - m, a.invT, -L) * kLog2e);
+        for (int e = 0; e < E; ++e) v[e] = scaled_exp(scale, fmaf(v[e] - m, a.invT, -L));
         store_vec<GB, E, true>(g + at + u * kThreads * E, v);
       }
     } else {
@@ -401,7 +409,7 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillBwd a) {
         float v[E];
         to_float<ZB, E>(q[u], v);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[e] = scale * exp2_fast(fmaf(v[e] - m, a.invT, -L) * kLog2e);
+        for (int e = 0; e < E; ++e) v[e] = scaled_exp(scale, fmaf(v[e] - m, a.invT, -L));
         if (first[u] == 0 && n[u] == E)
           store_vec<GB, E, true>(g + at + u * kThreads * E, v);
         else if (first[u] < n[u])
@@ -438,7 +446,7 @@ __global__ __launch_bounds__(kThreads) void distill_bwd_kernel(DistillBwd a) {
         again |= same && i < j;
       }
       if (again) continue;  // the first entry of an id writes it
-      const float e = exp2_fast(fmaf(load_any(z, ZB, v) - m, a.invT, -L) * kLog2e);
+      const float e = scaled_exp(1.0f, fmaf(load_any(z, ZB, v) - m, a.invT, -L));
       store1<GB>(g + v, scale * (e - sum));
     }
     wave_sync();  // the lists are written anew for the next item

@@ -387,6 +387,31 @@ def test_distill_of_masked_logits():
             check(dz, wz, ez, "dlogits")
 
 
+@pytest.mark.parametrize("size,T", [(30.0, 1.0), (1e5, 1.0), (1e5, 2.0 ** -20), (1e9, 0.01),
+                                    (1e20, 1.0), (1e30, 2.0 ** 20)])
+def test_distill_of_large_logits(size, T):
+    """Logits whose quotients by the temperature are far beyond the range of an
+    exponential, with their largest entries close together."""
+    g = np.random.default_rng(21)
+    M, V, k = 5, 3000, 6
+    z = randn(g, (M, V), F32, size)
+    top = z.max(dim=1, keepdim=True).values
+    for j in range(4):   # near the largest: steps of about T
+        z[:, 7 + j] = torch.nextafter(top[:, 0] - j * T, torch.tensor(0.0))
+    ids = torch.tensor([[7, 8, 9, 10, 0, 2999]] * M)
+    t = randn(g, (M, k), F32, T)
+    stats = torch.empty(2, M, device=DEV)
+    args = (z.to(DEV), ids.to(DEV), t.to(DEV))
+    loss = q.qlora_distill_fwd(*args, temperature=T, stats_out=stats)
+    dz = q.qlora_distill_bwd(*args, torch.ones(M, device=DEV), stats, temperature=T)
+    torch.cuda.synchronize()
+    want, err, wstats, e_stats = rows.distill_fwd(host(z), host(ids), host(t), T)
+    check(loss, want, err, "loss")
+    check(stats, wstats, e_stats, "stats")
+    wz, ez = rows.distill_bwd(host(z), host(ids), host(t), np.ones(M), T)
+    check(dz, wz, ez, "dlogits")
+
+
 def test_distill_spreads_nan_by_row():
     z, t = torch.zeros(4, 50), torch.zeros(4, 3)
     ids = torch.tensor([[0, 1, 2]] * 4)
