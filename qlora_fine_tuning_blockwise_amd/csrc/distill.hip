@@ -153,7 +153,8 @@ __device__ __forceinline__ MaxSum wave_join(MaxSum a, float c) {
 // U vectors of logits into the pair. -inf adds nothing: it fills the places
 // of a vector that lie outside of the row.
 template <bool ZB, int E, int U>
-__device__ __forceinline__ void take(MaxSum& a, const Vec<ZB, E> (&q)[U], float c) {
+__device__ __forceinline__ void take(MaxSum& a, const Vec<ZB, E> (&q)[U], float c,
+                                     float limit) {
   float v[U][E];
   float m = a.m;
 #pragma unroll
@@ -167,8 +168,8 @@ __device__ __forceinline__ void take(MaxSum& a, const Vec<ZB, E> (&q)[U], float 
 #pragma unroll
   for (int u = 0; u < U; ++u) s[u] = 0.0f;
   float fix = 1.0f;
-  const float bc = base * c;
-  if (__builtin_fabsf(bc) <= 0x1p20f) {
+  if (__builtin_fabsf(base) <= limit) {  // |base c| <= 2^20
+    const float bc = base * c;
     // (v - base) c as one operation: v c - base c, whose second term is rounded
     // alike for all of them, by 2^-4 at most; the rounding is taken out of the
     // sum.
@@ -228,6 +229,7 @@ struct DistillFwd {
   int64_t ldz, M, V;
   Teacher teacher;
   float T, invT;
+  float c, limit;  // log2(e) / T; 2^20 / c
   float* loss;
   float* stats;
   MaxSum* part;  // [M][splits][kWaves]
@@ -274,7 +276,7 @@ __global__ __launch_bounds__(kThreads) void distill_fwd_kernel(DistillFwd a) {
   int32_t* id = reinterpret_cast<int32_t*>(lds) + wave * 3 * a.teacher.k;
   float* t = reinterpret_cast<float*>(id) + a.teacher.k;
   float* logit = t + a.teacher.k;
-  const float c = a.invT * kLog2e;
+  const float c = a.c, limit = a.limit;
   for (int64_t item = blockIdx.x; item < a.M * a.splits; item += gridDim.x) {
     const int64_t row = item / a.splits;
     const int split = (int)(item - row * a.splits);
@@ -300,7 +302,7 @@ __global__ __launch_bounds__(kThreads) void distill_fwd_kernel(DistillFwd a) {
     Vec<ZB, E> q[U];
     for (int i = 0; i < a.rounds; ++i) {
       load(i, q);
-      take<ZB, E, U>(r, q, c);
+      take<ZB, E, U>(r, q, c, limit);
     }
     r = wave_join(r, c);
     if (a.splits > 1) {
@@ -325,7 +327,7 @@ __global__ __launch_bounds__(64) void distill_finish_kernel(DistillFwd a) {
   const int lane = threadIdx.x;
   int32_t* id = reinterpret_cast<int32_t*>(lds);
   float *t = lds + a.teacher.k, *logit = t + a.teacher.k;
-  const float c = a.invT * kLog2e;
+  const float c = a.c;
   const int parts = a.splits * kWaves;
   for (int64_t row = blockIdx.x; row < a.M; row += gridDim.x) {
     const elem_t<ZB>* z = static_cast<const elem_t<ZB>*>(a.z) + row * a.ldz;
@@ -486,8 +488,9 @@ hipError_t launch_distill_fwd(const void* z, int64_t ldz, bool z_bf16, int64_t M
                               float T, float* loss, float* stats, float* part, hipStream_t st) {
   const Pieces p = fwd_pieces(V);
   const int splits = p.count;
-  const DistillFwd a{z, ldz, M, V, {ids, t, ids64, t_bf16, k}, T, 1.0f / T, loss, stats,
-                     reinterpret_cast<MaxSum*>(part), splits, p.rounds};
+  const float c = 1.0f / T * kLog2e;
+  const DistillFwd a{z, ldz, M, V, {ids, t, ids64, t_bf16, k}, T, 1.0f / T, c, 0x1p20f / c, loss,
+                     stats, reinterpret_cast<MaxSum*>(part), splits, p.rounds};
   const int64_t items = M * splits;
   const dim3 grid((unsigned)(items < 65536 ? items : 65536)), rows((unsigned)(M < 65536 ? M : 65536));
   const size_t lds = (size_t)k * 12;
