@@ -15,14 +15,18 @@
 // the type's lowest values is a uniform distribution and not a NaN.
 //
 // The forward reads each logit once: a lane keeps a running maximum and the
-// sum of exponentials taken from it, and joins 32 (bf16) or 16 logits at a
-// time. The backward streams the row and then rewrites the few entries the
-// teacher names. Waves work alone (no barriers in the streams): each reads
-// the teacher's entries itself and, in the backward, rewrites those whose
-// logits it has written. The logits pass through once, so they are read and
-// their gradients written with the nontemporal hint.
-#include <type_traits>
-
+// sum of exponentials taken from it, and joins 32 logits at a time. The
+// backward streams the row and then rewrites the few entries the teacher
+// names. Waves work alone (no barriers in the streams): each reads the
+// teacher's entries itself and, in the backward, rewrites those whose logits it
+// has written. The logits pass through once, so they are read and their
+// gradients written with the nontemporal hint (a reader of the gradients that
+// follows gains too from 131 MB on: call and reader 93 against 101 us; at 42 MB
+// it loses, 36 against 33 us).
+//
+// Memory bounds both on long rows: the forward's pass over 2048 x 128000 bf16
+// runs at 6.7 TB/s (7.0 TB/s is what reading alone reaches here). On short rows
+// and few rows the chain of dependent loads does.
 #include "rows.h"
 
 namespace qlora {

@@ -18,8 +18,6 @@
 //      the tile; a sum that passes a tile's border goes to the workspace, and
 //      the tile in which it begins is noted in a list.
 //   4. Workgroups take the list's sums and collect their parts in tile order.
-#include <type_traits>
-
 #include "rows.h"
 
 namespace qlora {

@@ -19,8 +19,6 @@
 // a copy of that size reaches 5.7 to 6.0). One row alone takes 2.9 us, of which
 // a launch is 2. The squares of the deviations are summed in fp32, so a row's
 // values stay below 2^60.
-#include <type_traits>
-
 #include "rows.h"
 
 namespace qlora {

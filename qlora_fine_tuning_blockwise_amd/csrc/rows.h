@@ -3,6 +3,8 @@
 // over a wave or a workgroup.
 #pragma once
 
+#include <type_traits>
+
 #include "device.h"
 
 namespace qlora {
@@ -147,19 +149,7 @@ __device__ __forceinline__ int count_below(int64_t at, int64_t end) {
   return left >= E ? E : left < 0 ? 0 : (int)left;
 }
 
-// E elements (or the first n) of an array whose type is a run-time value.
-template <int E>
-__device__ __forceinline__ void load_any_vec(const void* p, bool bf16, int64_t at, int n,
-                                             float (&v)[E]) {
-  if (bf16) {
-    const uint16_t* q = static_cast<const uint16_t*>(p) + at;
-    to_float<true, E>(n >= E ? load_vec<true, E>(q) : load_part<true, E>(q, n), v);
-  } else {
-    const float* q = static_cast<const float*>(p) + at;
-    to_float<false, E>(n >= E ? load_vec<false, E>(q) : load_part<false, E>(q, n), v);
-  }
-}
-
+// An element of an array whose type is a run-time value.
 __device__ __forceinline__ float load_any(const void* p, bool bf16, int64_t at) {
   return bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[at] << 16)
               : static_cast<const float*>(p)[at];
