@@ -368,34 +368,24 @@ def qlora_adamw_step(param: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Ten
 _FLOATS = {torch.float32: _lib.DTYPE_F32, torch.bfloat16: _lib.DTYPE_BF16}
 _INDEXES = {torch.int32: _lib.DTYPE_I32, torch.int64: _lib.DTYPE_I64}
 _F32 = (torch.float32,)
-
-
-class _Here:
-    """The context of a call that stays where it is."""
-
-    __slots__ = ()
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *error):
-        return None
-
-
-_HERE = _Here()
 _device_now = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
-def _place(t, stream):
-    """Context in which a row operator on t's device allocates and launches."""
-    dev = t.device
+def _elsewhere(dev, stream):
+    """Whether a row operator has to change the current device or stream for
+    tensors on dev."""
+    return stream is not None or dev.type != "cuda" or dev.index != _device_now()
+
+
+def _place(dev, stream):
+    """Context in which a row operator on dev allocates and launches."""
     if dev.type != "cuda":
         raise ValueError(f"tensors must be on a ROCm device, got {dev}")
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream on {stream.device}, tensors on {dev}")
-        return torch.cuda.stream(stream)
-    return _HERE if dev.index == _device_now() else torch.cuda.device(dev)
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream on {stream.device}, tensors on {dev}")
+    return torch.cuda.stream(stream)
 
 
 def _at(t):
@@ -492,13 +482,15 @@ def qlora_embed_fwd(W: torch.Tensor, ids: torch.Tensor, scale: float = 1.0,
     M = ids.numel()
     ldw = _matrix(W, "W", (V, D), dev)
     ids_dtype = _indexes(ids, "ids", (M,), dev)
-    with _place(W, stream):
-        if out is None:
-            out, ldo = _new(W, M, D, out_dtype)
-        else:
-            ldo = _matrix(out, "out", (M, D), dev)
-        st = _lib.load().qlora_embed_fwd(_at(W), ldw, _FLOATS[W.dtype], V, D, _at(ids), ids_dtype,
-                                         M, scale, _at(out), ldo, _FLOATS[out.dtype], _here(dev))
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_embed_fwd(W, ids, scale, out, out_dtype)
+    if out is None:
+        out, ldo = _new(W, M, D, out_dtype)
+    else:
+        ldo = _matrix(out, "out", (M, D), dev)
+    st = _lib.load().qlora_embed_fwd(_at(W), ldw, _FLOATS[W.dtype], V, D, _at(ids), ids_dtype,
+                                     M, scale, _at(out), ldo, _FLOATS[out.dtype], _here(dev))
     if st:
         _lib.check(st, "qlora_embed_fwd")
     return out
@@ -518,13 +510,15 @@ def qlora_embed_bwd(dY: torch.Tensor, ids: torch.Tensor, V: int, scale: float = 
     if accumulate and dW is None:
         raise ValueError("qlora_embed_bwd: accumulate needs dW")
     _need(dW, "dW", (V, D), tuple(_FLOATS), dev)
-    with _place(dY, stream):
-        if dW is None:
-            dW, _ = _new(dY, V, D, grad_dtype)
-        workspace = _bytes(workspace, qlora_embed_bwd_workspace_bytes(M, D), dev)
-        st = _lib.load().qlora_embed_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(ids), ids_dtype, M, V,
-                                         D, scale, _at(dW), _FLOATS[dW.dtype], int(accumulate),
-                                         _at(workspace), workspace.numel(), _here(dev))
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_embed_bwd(dY, ids, V, scale, grad_dtype, dW, accumulate, workspace)
+    if dW is None:
+        dW, _ = _new(dY, V, D, grad_dtype)
+    workspace = _bytes(workspace, qlora_embed_bwd_workspace_bytes(M, D), dev)
+    st = _lib.load().qlora_embed_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(ids), ids_dtype, M, V,
+                                     D, scale, _at(dW), _FLOATS[dW.dtype], int(accumulate),
+                                     _at(workspace), workspace.numel(), _here(dev))
     if st:
         _lib.check(st, "qlora_embed_bwd")
     return dW
@@ -556,14 +550,16 @@ def qlora_norm_fwd(x: torch.Tensor, gamma: torch.Tensor | None = None,
     w_dtype = _norm_vectors(N, dev, (gamma, "gamma"), (beta, "beta"))
     if stats_out is not None:
         _vector(stats_out, "stats_out", (2, M), _F32, dev)
-    with _place(x, stream):
-        if y is None:
-            y, ldy = _new(x, M, N, y_dtype)
-        else:
-            ldy = _matrix(y, "y", (M, N), dev)
-        st = _lib.load().qlora_norm_fwd(_at(x), ldx, _FLOATS[x.dtype], M, N, norm, _at(gamma),
-                                        _at(beta), w_dtype, eps, _at(y), ldy, _FLOATS[y.dtype],
-                                        _at(stats_out), _here(dev))
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_norm_fwd(x, gamma, beta, eps, norm, y, y_dtype, stats_out)
+    if y is None:
+        y, ldy = _new(x, M, N, y_dtype)
+    else:
+        ldy = _matrix(y, "y", (M, N), dev)
+    st = _lib.load().qlora_norm_fwd(_at(x), ldx, _FLOATS[x.dtype], M, N, norm, _at(gamma),
+                                    _at(beta), w_dtype, eps, _at(y), ldy, _FLOATS[y.dtype],
+                                    _at(stats_out), _here(dev))
     if st:
         _lib.check(st, "qlora_norm_fwd")
     return y
@@ -587,18 +583,21 @@ def qlora_norm_bwd(dY: torch.Tensor, x: torch.Tensor, gamma: torch.Tensor | None
     dx_dtype = x.dtype if dx_dtype is None else dx_dtype
     if dx_dtype not in _FLOATS or grad_dtype not in _FLOATS:
         raise ValueError("qlora_norm_bwd: gradients are fp32 or bf16")
-    with _place(x, stream):
-        dX = torch.empty((M, N), dtype=dx_dtype, device=dev) if want_dx else None
-        dgamma = torch.empty(N, dtype=grad_dtype, device=dev) if want_dgamma else None
-        dbeta = torch.empty(N, dtype=grad_dtype, device=dev) if want_dbeta else None
-        need = qlora_norm_bwd_workspace_bytes(M, N) if want_dgamma or want_dbeta else 0
-        if need or workspace is not None:
-            workspace = _bytes(workspace, need, dev)
-        st = _lib.load().qlora_norm_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(x), ldx,
-                                        _FLOATS[x.dtype], M, N, norm, _at(gamma), w_dtype, eps,
-                                        _at(stats), _at(dX), N, _FLOATS[dx_dtype], _at(dgamma),
-                                        _at(dbeta), _FLOATS[grad_dtype], _at(workspace),
-                                        0 if workspace is None else workspace.numel(), _here(dev))
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_norm_bwd(dY, x, gamma, eps, norm, stats, want_dx, want_dgamma, want_dbeta,
+                                  dx_dtype, grad_dtype, workspace)
+    dX = torch.empty((M, N), dtype=dx_dtype, device=dev) if want_dx else None
+    dgamma = torch.empty(N, dtype=grad_dtype, device=dev) if want_dgamma else None
+    dbeta = torch.empty(N, dtype=grad_dtype, device=dev) if want_dbeta else None
+    need = qlora_norm_bwd_workspace_bytes(M, N) if want_dgamma or want_dbeta else 0
+    if need or workspace is not None:
+        workspace = _bytes(workspace, need, dev)
+    st = _lib.load().qlora_norm_bwd(_at(dY), ldy, _FLOATS[dY.dtype], _at(x), ldx,
+                                    _FLOATS[x.dtype], M, N, norm, _at(gamma), w_dtype, eps,
+                                    _at(stats), _at(dX), N, _FLOATS[dx_dtype], _at(dgamma),
+                                    _at(dbeta), _FLOATS[grad_dtype], _at(workspace),
+                                    0 if workspace is None else workspace.numel(), _here(dev))
     if st:
         _lib.check(st, "qlora_norm_bwd")
     return dX, dgamma, dbeta
@@ -628,15 +627,18 @@ def qlora_distill_fwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: t
     if stats_out is not None:
         _vector(stats_out, "stats_out", (2, M), _F32, dev)
     _need(loss, "loss", (M,), torch.float32, dev)
-    with _place(logits, stream):
-        if loss is None:
-            loss = torch.empty(M, dtype=torch.float32, device=dev)
-        need = qlora_distill_fwd_workspace_bytes(M, V)
-        if need or workspace is not None:
-            workspace = _bytes(workspace, need, dev)
-        st = _lib.load().qlora_distill_fwd(*heads, temperature, _at(loss), _at(stats_out),
-                                           _at(workspace),
-                                           0 if workspace is None else workspace.numel(), _here(dev))
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_distill_fwd(logits, top_ids, top_logits, temperature, loss, stats_out,
+                                     workspace)
+    if loss is None:
+        loss = torch.empty(M, dtype=torch.float32, device=dev)
+    need = qlora_distill_fwd_workspace_bytes(M, V)
+    if need or workspace is not None:
+        workspace = _bytes(workspace, need, dev)
+    st = _lib.load().qlora_distill_fwd(*heads, temperature, _at(loss), _at(stats_out),
+                                       _at(workspace),
+                                       0 if workspace is None else workspace.numel(), _here(dev))
     if st:
         _lib.check(st, "qlora_distill_fwd")
     return loss
@@ -653,13 +655,16 @@ def qlora_distill_bwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: t
     M, V, dev = heads[3], heads[4], logits.device
     _vector(stats, "stats", (2, M), _F32, dev)
     _vector(dloss, "dloss", (M,), _F32, dev)
-    with _place(logits, stream):
-        if dlogits is None:
-            dlogits, ldg = _new(logits, M, V, grad_dtype)
-        else:
-            ldg = _matrix(dlogits, "dlogits", (M, V), dev)
-        st = _lib.load().qlora_distill_bwd(*heads, temperature, _at(stats), _at(dloss),
-                                           _at(dlogits), ldg, _FLOATS[dlogits.dtype], _here(dev))
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_distill_bwd(logits, top_ids, top_logits, dloss, stats, temperature, dlogits,
+                                     grad_dtype)
+    if dlogits is None:
+        dlogits, ldg = _new(logits, M, V, grad_dtype)
+    else:
+        ldg = _matrix(dlogits, "dlogits", (M, V), dev)
+    st = _lib.load().qlora_distill_bwd(*heads, temperature, _at(stats), _at(dloss),
+                                       _at(dlogits), ldg, _FLOATS[dlogits.dtype], _here(dev))
     if st:
         _lib.check(st, "qlora_distill_bwd")
     return dlogits
