@@ -8,11 +8,12 @@
 // The gradient sorts the tokens by id (ties by position), so that each table
 // row is one sum in token order, whatever the launch: no floating-point
 // atomics, the same bits every time.
-//   1. The first launch fills dW with zeros, which is most of the call's
-//      traffic; beside the fill, small workgroups count for each token how many
-//      tokens of its run come before it, which is its place in the run.
+//   1. Small workgroups count for each token how many tokens of its run come
+//      before it, which is its place in the run. Beside them dW is filled with
+//      zeros, which is most of the call's traffic.
 //   2. With more than one run, a token's place among all is its place in its
 //      own run plus, by binary search, the count of smaller keys in the others.
+//      Most of the fill then runs beside this launch.
 //   3. The sorted tokens are cut into tiles. A wave adds one tile's rows over
 //      64 vectors of columns in fp32 and writes each id whose tokens all lie in
 //      the tile; a sum that passes a tile's border goes to the workspace, and
@@ -27,9 +28,9 @@ constexpr int32_t kDead = 0x7fffffff;  // key of an id outside of the table: sor
 
 // Tokens of a run. The count compares each token with its run, the search
 // walks through every other run: up to kMaxRun tokens are one run (the search
-// is a launch of 6 us). Measured with runs of 512, 1024, 2048 and 4096: 16000
-// tokens of 1024 columns 44.5, 41.9, 43.5 and 46.0 us, 32768 tokens 76, 64, 60
-// and 64 us.
+// is a launch of 6 us). Measured with runs of 512, 1024 and 2048 tokens: 16000
+// tokens of 1024 columns 43.2, 41.5 and 44.0 us; with 1024, 2048 and 4096: 30000
+// tokens of 500 columns 57.8, 54.9 and 61.4 us.
 constexpr int kMaxRun = 4096;
 int run_length(int64_t M) { return M <= kMaxRun ? kMaxRun : M <= 20000 ? 1024 : 2048; }
 
@@ -85,8 +86,7 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedFwd a) {
 // ---------------------------------------------------------------- the sort
 // The first workgroups order 16 tokens each (sixteen threads a token, each of
 // which compares it with every sixteenth group of four of its run's keys); the
-// others write zeros over dW (`halves` two-byte units, its base 16-byte
-// aligned). The fill is nontemporal: with plain stores it leaves the Infinity
+// others write zeros over dW or a part of it. The fill is nontemporal: with plain stores it leaves the Infinity
 // Cache full of lines that have yet to reach memory, and the sums that follow
 // wait for them (4096 tokens, 32000 x 4096 fp32: the sums take 23 against 13.7
 // us, the call 115 against 99 us). A workgroup writes 4 KB and ends: with a
@@ -112,16 +112,27 @@ __device__ __forceinline__ void stage_keys(const T* ids, int n, int64_t V, int32
   }
 }
 
+// Zeros over the sixteen-byte units [first, end) of dW and `tail` two-byte
+// units behind them, by `groups` workgroups of which this is number `at`.
+struct Fill {
+  u32x4_t* dW;
+  int64_t first, end;
+  int tail;
+};
+__device__ __forceinline__ void fill_zeros(const Fill& f, int64_t at, int64_t groups) {
+  for (int64_t i = f.first + at * kOrderThreads + threadIdx.x; i < f.end; i += groups * kOrderThreads)
+    __builtin_nontemporal_store(zero4(), f.dW + i);
+  if (at == 0 && (int)threadIdx.x < f.tail)
+    reinterpret_cast<uint16_t*>(f.dW + f.end)[threadIdx.x] = 0;
+}
+
 __global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
     const void* ids, bool i64, int64_t M, int64_t V, int run, int orders, int32_t* key, int32_t* pos,
-    int32_t* count, u32x4_t* dW, int64_t halves) {
+    int32_t* count, Fill fill) {
   __shared__ __align__(16) int32_t keys[kMaxRun];
   const int t = threadIdx.x;
   if ((int)blockIdx.x >= orders) {
-    const int64_t quads = halves / 8, stride = (int64_t)(gridDim.x - orders) * kOrderThreads;
-    const int64_t first = (int64_t)(blockIdx.x - orders) * kOrderThreads + t;
-    for (int64_t i = first; i < quads; i += stride) __builtin_nontemporal_store(zero4(), dW + i);
-    if (first < halves % 8) reinterpret_cast<uint16_t*>(dW)[quads * 8 + first] = 0;
+    fill_zeros(fill, (int)blockIdx.x - orders, gridDim.x - orders);
     return;
   }
   if (blockIdx.x == 0 && t == 0) *count = 0;  // the list of embed_sum_kernel is empty
@@ -155,14 +166,19 @@ __global__ __launch_bounds__(kOrderThreads) void embed_order_kernel(
 // The place of each token among all: its place in its run and, for every
 // other run, the count of keys before it by binary search. Sixteen lanes work
 // on a token, each on four runs at a time, so that the searches' loads fly
-// together.
+// together; they wait more than they move, and the workgroups behind the first
+// `ranks` fill dW meanwhile.
 constexpr int kRankLanes = 16;
 
 __global__ __launch_bounds__(256) void embed_rank_kernel(const int32_t* __restrict__ key,
                                                          const int32_t* __restrict__ pos,
-                                                         int64_t M, int run, int runs,
+                                                         int64_t M, int run, int runs, int ranks,
                                                          int32_t* __restrict__ key_out,
-                                                         int32_t* __restrict__ pos_out) {
+                                                         int32_t* __restrict__ pos_out, Fill fill) {
+  if ((int)blockIdx.x >= ranks) {
+    fill_zeros(fill, (int)blockIdx.x - ranks, gridDim.x - ranks);
+    return;
+  }
   const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kRankLanes;
   const int part = threadIdx.x % kRankLanes;
   const bool live = i < M;
@@ -434,20 +450,30 @@ hipError_t launch_embed_bwd(const void* dY, int64_t ldy, bool dy_bf16, const voi
   const int runs = (int)((M + run - 1) / run);
   const int64_t Mp = (M + 63) / 64 * 64;
   int32_t *key = sorted, *pos = sorted + Mp, *list = sorted + 4 * Mp;
-  const int64_t halves = accumulate ? 0 : V * D * (grad_bf16 ? 1 : 2);
-  const int64_t fills = (halves / 8 + kOrderThreads - 1) / kOrderThreads;
-  const int64_t fill = halves ? (fills < 1 ? 1 : fills > (1 << 20) ? (1 << 20) : fills) : 0;
+  const int64_t halves = accumulate ? 0 : V * D * (grad_bf16 ? 1 : 2), quads = halves / 8;
+  // With a search to come, the count takes a quarter of the fill and the search
+  // the rest: a quarter, half, three quarters and all beside the count take 41.5,
+  // 41.9, 43.7 and 45.3 us on 16000 tokens of 1024 columns (65 MB of bf16), 79.9,
+  // 79.9, 80.5 and 85.6 us on 16384 of 2048 (262 MB of fp32).
+  const int64_t split = runs > 1 ? quads / 4 : quads;
+  const Fill before{static_cast<u32x4_t*>(dW), 0, split, runs > 1 ? 0 : (int)(halves % 8)};
+  const Fill beside{static_cast<u32x4_t*>(dW), split, quads, (int)(halves % 8)};
+  const auto groups = [](const Fill& f) {
+    const int64_t n = (f.end - f.first + kOrderThreads - 1) / kOrderThreads;
+    return n < 1 ? (int64_t)(f.tail > 0) : n > (1 << 20) ? (int64_t)(1 << 20) : n;
+  };
   const int orders = (int)((M + kOrderTokens - 1) / kOrderTokens);
+  const int64_t fill = groups(before);
   if (orders + fill > 0) {
     hipLaunchKernelGGL(embed_order_kernel, dim3((unsigned)(orders + fill)), dim3(kOrderThreads), 0,
-                       st, ids, ids64, M, V, run, orders, key, pos, list, static_cast<u32x4_t*>(dW),
-                       halves);
+                       st, ids, ids64, M, V, run, orders, key, pos, list, before);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   if (M == 0) return hipSuccess;
   if (runs > 1) {
-    hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)((M * kRankLanes + 255) / 256)), dim3(256),
-                       0, st, key, pos, M, run, runs, sorted + 2 * Mp, sorted + 3 * Mp);
+    const int ranks = (int)((M * kRankLanes + 255) / 256);
+    hipLaunchKernelGGL(embed_rank_kernel, dim3((unsigned)(ranks + groups(beside))), dim3(256), 0, st,
+                       key, pos, M, run, runs, ranks, sorted + 2 * Mp, sorted + 3 * Mp, beside);
     if (const hipError_t e = hipGetLastError()) return e;
     key = sorted + 2 * Mp;
     pos = sorted + 3 * Mp;

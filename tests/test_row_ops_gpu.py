@@ -302,6 +302,24 @@ def test_embed_backward_without_tokens():
         assert dW.shape == (7, 33) and not dW.any()
 
 
+@pytest.mark.parametrize("M", [9, 4500])
+@pytest.mark.parametrize("V,D,dtype", [(1, 1, BF16), (7, 1, BF16), (8, 1, BF16), (3, 3, F32), (31, 1, BF16),
+                                       (33, 1, F32), (1023, 9, BF16), (1025, 4, F32), (2049, 513, BF16)])
+def test_embed_backward_fills_the_table(M, V, D, dtype):
+    """Rows without a token become zero to the last element whatever part of
+    the zeros each launch writes, and what lies behind the table stays."""
+    say("embed bwd fill", M, V, D, dtype)
+    ids = torch.full((M,), V - 1, dtype=torch.int64, device=DEV)
+    ids[1:] = -1
+    dY = torch.ones(M, D, device=DEV)
+    whole = torch.full((V * D + 64,), math.nan, dtype=dtype, device=DEV)
+    dW = whole[:V * D].view(V, D)
+    q.qlora_embed_bwd(dY, ids, V, scale=3.0, dW=dW)
+    torch.cuda.synchronize()
+    assert not dW[:-1].any() and bool((dW[-1] == 3.0).all())
+    assert bool(whole[V * D:].isnan().all())
+
+
 # --------------------------------------------------------------- distillation
 def distill_inputs(M, V, k, seed, z_dtype, t_dtype, ids_dtype):
     g = np.random.default_rng(seed)
