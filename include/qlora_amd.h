@@ -68,7 +68,8 @@ extern "C" {
 
 /* Status codes. */
 #define QLORA_OK 0
-#define QLORA_ERR_INVALID_ARG 1 /* NULL pointer, negative size, bad enum */
+#define QLORA_ERR_INVALID_ARG 1 /* NULL pointer, negative size, bad enum; a row
+                                   operator's output over an input */
 #define QLORA_ERR_SHAPE 2       /* K % 64 != 0, N or K < 1, or two of M, N, K
                                    whose product passes 2^40 elements; a row
                                    operator's size or stride out of its range */
@@ -413,6 +414,10 @@ int qlora_linear_fwd_noalloc(const qlora_nf4* w, const uint16_t* x, int64_t M,
  *   - Results do not depend on the launch or on earlier calls: no
  *     floating-point atomics, and sums are taken in a fixed order.
  *   - M == 0 is a successful no-op (gradients over the rows become zero).
+ *   - No output or workspace may share memory with an input or with another
+ *     output: QLORA_ERR_INVALID_ARG, but for the cases that qlora_norm_fwd and
+ *     qlora_norm_bwd name. (Matrices that take turns in each row of one wider
+ *     buffer share none.)
  *   - Like the other entry points they allocate nothing, do not synchronise
  *     and may be captured into a HIP graph. */
 
@@ -452,7 +457,7 @@ int qlora_embed_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* ids, 
  * QLORA_NORM_RMS: the same with mean = 0. The sums of squares are fp32: values
  * stay below 2^60 (a larger row gives rstd 0, not an error).
  *   x [M,N] (x_dtype); gamma, beta [N] (w_dtype), each may be NULL (1 and 0);
- *   y [M,N] (y_dtype).
+ *   y [M,N] (y_dtype); y may be x itself (the same address, type and stride).
  *   stats  fp32 [2,M] or NULL; when given it receives the means, then the
  *          rstd (for the backward).
  * QLORA_ERR_SHAPE unless 1 <= N <= QLORA_MAX_NORM_WIDTH, M <= QLORA_MAX_ROWS
@@ -472,7 +477,8 @@ size_t qlora_norm_bwd_workspace_bytes(int64_t M, int64_t N);
  *   dY [M,N] (dy_dtype), x, gamma, eps as in the forward; stats from the
  *   forward, or NULL to recompute them.
  *   dX [M,N] (dx_dtype), dgamma, dbeta [N] (grad_dtype) may each be NULL to
- *   skip that output.
+ *   skip that output; dX may be dY or x itself (the same address, type and
+ *   stride).
  * M == 0 writes zero dgamma and dbeta. Errors as qlora_norm_fwd;
  * QLORA_ERR_WORKSPACE for a workspace smaller than
  * qlora_norm_bwd_workspace_bytes(M, N) (not needed, and may be NULL, without

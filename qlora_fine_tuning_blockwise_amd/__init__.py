@@ -11,7 +11,9 @@ The row operators (qlora_embed_*, qlora_norm_*, qlora_distill_*) take
 matrices whose rows are contiguous, at any row stride (views of wider or
 longer tensors), and run on the device of their tensors whichever is current.
 Without `stream` they use that device's current stream; with it, what they
-allocate belongs to that stream.
+allocate belongs to that stream. A given output may not share memory with an
+input or another output (the library refuses the call); only qlora_norm_fwd's
+y may be x itself.
 """
 from __future__ import annotations
 

@@ -7,6 +7,7 @@
 
 #include "../../include/qlora_amd.h"
 #include "internal.h"
+#include "spans.h"
 
 namespace qlora {
 namespace {
@@ -214,12 +215,23 @@ constexpr int64_t kMaxEmbedWidth = (int64_t)1 << 24;
 
 bool float_type(int d) { return d == QLORA_DTYPE_F32 || d == QLORA_DTYPE_BF16; }
 bool index_type(int d) { return d == QLORA_DTYPE_I32 || d == QLORA_DTYPE_I64; }
+int64_t elem_bytes(int dtype) { return dtype == QLORA_DTYPE_BF16 ? 2 : dtype == QLORA_DTYPE_I64 ? 8 : 4; }
 
 // The alignment of an element of a QLORA_DTYPE_* type.
 bool aligned_elem(const void* p, int dtype) {
-  const uintptr_t size = dtype == QLORA_DTYPE_BF16 ? 2 : dtype == QLORA_DTYPE_I64 ? 8 : 4;
-  return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0;
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem_bytes(dtype) - 1)) == 0;
 }
+
+// What an argument occupies, for the check that no output lies on an input:
+// rows of a matrix, or a contiguous array.
+Span matrix(const void* p, int64_t rows, int64_t width, int64_t ld, int dtype) {
+  return span_of(p, rows, width, ld, elem_bytes(dtype));
+}
+Span array(const void* p, int64_t count, int dtype) { return span_of(p, count * elem_bytes(dtype)); }
+Span bytes(const void* p, size_t n) { return span_of(p, (int64_t)n); }
+// An output that may be the input `in` itself, at the same address and stride
+// in the same type: no span of its own then.
+Span unless_same(const Span& in, const Span& out) { return in.same(out) ? Span{} : in; }
 
 // Rows of `width` elements every `ld`: the last row's end stays countable.
 bool stride_ok(int64_t M, int64_t width, int64_t ld) {
@@ -285,7 +297,7 @@ extern "C" {
 const char* qlora_strerror(int status) {
   switch (status) {
     case QLORA_OK: return "ok";
-    case QLORA_ERR_INVALID_ARG: return "invalid argument (NULL pointer, negative size or bad enum)";
+    case QLORA_ERR_INVALID_ARG: return "invalid argument (NULL pointer, negative size, bad enum, or an output over an input)";
     case QLORA_ERR_SHAPE:
       return "unsupported shape or stride (a weight needs N >= 1, K >= 64, K % 64 == 0)";
     case QLORA_ERR_ALIGN:
@@ -675,6 +687,9 @@ int qlora_embed_fwd(const void* W, int64_t ldw, int w_dtype, int64_t V, int64_t 
   if (!W || !ids || !out) return QLORA_ERR_INVALID_ARG;
   if (!aligned_elem(W, w_dtype) || !aligned_elem(ids, ids_dtype) || !aligned_elem(out, out_dtype))
     return QLORA_ERR_ALIGN;
+  if (any_meet({matrix(out, M, D, ldo, out_dtype)},
+               {matrix(W, V, D, ldw, w_dtype), array(ids, M, ids_dtype)}))
+    return QLORA_ERR_INVALID_ARG;
   return launch_status(launch_embed_fwd(W, ldw, w_dtype == QLORA_DTYPE_BF16, V, D, ids,
                                         ids_dtype == QLORA_DTYPE_I64, M, scale, out, ldo,
                                         out_dtype == QLORA_DTYPE_BF16,
@@ -700,6 +715,9 @@ int qlora_embed_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* ids, 
     return QLORA_ERR_ALIGN;
   const EmbedLayout L = embed_layout(M, D);
   if (M > 0 && (!workspace || workspace_bytes < L.total)) return QLORA_ERR_WORKSPACE;
+  if (any_meet({array(dW, V * D, grad_dtype), bytes(workspace, L.total)},
+               {matrix(dY, M, D, ldy, dy_dtype), array(ids, M, ids_dtype)}))
+    return QLORA_ERR_INVALID_ARG;
   return launch_status(launch_embed_bwd(
       dY, ldy, dy_dtype == QLORA_DTYPE_BF16, ids, ids_dtype == QLORA_DTYPE_I64, M, V, D, scale, dW,
       grad_dtype == QLORA_DTYPE_BF16, accumulate != 0,
@@ -721,6 +739,11 @@ int qlora_norm_fwd(const void* x, int64_t ldx, int x_dtype, int64_t M, int64_t N
   if (!aligned_elem(x, x_dtype) || !aligned_elem(gamma, w_dtype) || !aligned_elem(beta, w_dtype) ||
       !aligned_elem(y, y_dtype) || !aligned_elem(stats, QLORA_DTYPE_F32))
     return QLORA_ERR_ALIGN;
+  const Span out = matrix(y, M, N, ldy, y_dtype), in = matrix(x, M, N, ldx, x_dtype);
+  const Span kept = array(stats, 2 * M, QLORA_DTYPE_F32);
+  if (any_meet({out, kept}, {unless_same(in, out), array(gamma, N, w_dtype), array(beta, N, w_dtype)}) ||
+      meet(kept, in))
+    return QLORA_ERR_INVALID_ARG;
   return launch_status(launch_norm_fwd(x, ldx, x_dtype == QLORA_DTYPE_BF16, M, N,
                                        norm == QLORA_NORM_LAYER, gamma, beta,
                                        w_dtype == QLORA_DTYPE_BF16, eps, y, ldy,
@@ -758,6 +781,15 @@ int qlora_norm_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* x, int
     return QLORA_ERR_WORKSPACE;
   if (!dX && !grads) return QLORA_OK;
   if (M == 0 && !grads) return QLORA_OK;
+  const Span dx = matrix(dX, M, N, lddx, dx_dtype);
+  const Span in = matrix(x, M, N, ldx, x_dtype), dy = matrix(dY, M, N, ldy, dy_dtype);
+  const Span dg = array(dgamma, N, grad_dtype), db = array(dbeta, N, grad_dtype);
+  const Span part = bytes(grads ? workspace : nullptr, norm_bwd_bytes(M, N));
+  if (any_meet({dx, dg, db, part},
+               {unless_same(in, dx), unless_same(dy, dx), array(gamma, N, w_dtype),
+                array(stats, 2 * M, QLORA_DTYPE_F32)}) ||
+      any_meet({dg, db, part}, {in, dy}))
+    return QLORA_ERR_INVALID_ARG;
   return launch_status(launch_norm_bwd(dY, ldy, dy_dtype == QLORA_DTYPE_BF16, x, ldx,
                                        x_dtype == QLORA_DTYPE_BF16, M, N, norm == QLORA_NORM_LAYER,
                                        gamma, w_dtype == QLORA_DTYPE_BF16, eps, stats, dX, lddx,
@@ -784,6 +816,11 @@ int qlora_distill_fwd(const void* logits, int64_t ldz, int z_dtype, int64_t M, i
     return QLORA_ERR_ALIGN;
   const size_t need = distill_fwd_bytes(M, V);
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (any_meet({array(loss, M, QLORA_DTYPE_F32), array(stats, 2 * M, QLORA_DTYPE_F32),
+                bytes(workspace, need)},
+               {matrix(logits, M, V, ldz, z_dtype), array(top_ids, M * k, ids_dtype),
+                array(top_logits, M * k, t_dtype)}))
+    return QLORA_ERR_INVALID_ARG;
   return launch_status(launch_distill_fwd(
       logits, ldz, z_dtype == QLORA_DTYPE_BF16, M, V, top_ids, ids_dtype == QLORA_DTYPE_I64,
       top_logits, t_dtype == QLORA_DTYPE_BF16, k, temperature, loss, stats,
@@ -805,6 +842,11 @@ int qlora_distill_bwd(const void* logits, int64_t ldz, int z_dtype, int64_t M, i
       !aligned_elem(top_logits, t_dtype) || !aligned_elem(stats, QLORA_DTYPE_F32) ||
       !aligned_elem(dloss, QLORA_DTYPE_F32) || !aligned_elem(dlogits, grad_dtype))
     return QLORA_ERR_ALIGN;
+  if (any_meet({matrix(dlogits, M, V, ldg, grad_dtype)},
+               {matrix(logits, M, V, ldz, z_dtype), array(top_ids, M * k, ids_dtype),
+                array(top_logits, M * k, t_dtype), array(stats, 2 * M, QLORA_DTYPE_F32),
+                array(dloss, M, QLORA_DTYPE_F32)}))
+    return QLORA_ERR_INVALID_ARG;
   return launch_status(launch_distill_bwd(
       logits, ldz, z_dtype == QLORA_DTYPE_BF16, M, V, top_ids, ids_dtype == QLORA_DTYPE_I64,
       top_logits, t_dtype == QLORA_DTYPE_BF16, k, temperature, stats, dloss, dlogits, ldg,
