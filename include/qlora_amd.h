@@ -455,7 +455,8 @@ int qlora_embed_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* ids, 
  *   y = (x - mean) * rstd * gamma + beta,
  *   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps);
  * QLORA_NORM_RMS: the same with mean = 0. The sums of squares are fp32: values
- * stay below 2^60 (a larger row gives rstd 0, not an error).
+ * stay below 2^60 (a row beyond 2^63 may give rstd 0, not an error), and with
+ * eps = 0 the root of sum (x - mean)^2 / N stays above 2^-50.
  *   x [M,N] (x_dtype); gamma, beta [N] (w_dtype), each may be NULL (1 and 0);
  *   y [M,N] (y_dtype); y may be x itself (the same address, type and stride).
  *   stats  fp32 [2,M] or NULL; when given it receives the means, then the

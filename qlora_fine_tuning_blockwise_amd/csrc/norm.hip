@@ -17,8 +17,14 @@
 //
 // Memory bounds the forward: 4096 x 4096 bf16 moves 67 MB in 11.3 us (5.9 TB/s;
 // a copy of that size reaches 5.7 to 6.0). One row alone takes 2.9 us, of which
-// a launch is 2. The squares of the deviations are summed in fp32, so a row's
-// values stay below 2^60.
+// a launch is 2.
+//
+// The deviations are squared at 2^-k of their size, 4^k >= N: the sum of N
+// squares then leaves fp32 no sooner than one square does, and a row's values
+// may come near 2^64 (unscaled, rows of 2^60 gave rstd = 0 from about 256
+// columns on). Powers of two change no rounding, and the scaled difference is
+// one fused operation, so it costs nothing; the smallest square that keeps its
+// bits is of a deviation of 2^(k - 63), which counts only without eps.
 #include "rows.h"
 
 namespace qlora {
@@ -90,11 +96,12 @@ __device__ __forceinline__ void load_affine(const void* w, bool bf16, int N,
   }
 }
 
-// The statistics of the row in v.
+// The statistics of the row in v; `scale` is the 2^-k of the squares.
 template <bool kShort, int T, int NV, int E>
 __device__ __forceinline__ void row_stats(const float (&v)[NV][E], const Place<T, NV, E>& p, int N,
-                                          float invN, bool center, float eps, float* red, int waves,
-                                          int& par, float& mean, float& rstd) {
+                                          float invN, float scale, bool center, float eps,
+                                          float* red, int waves, int& par, float& mean,
+                                          float& rstd) {
   const auto counts = [&](int i, int e) { return e >= p.skip[i] && (!kShort || e < N); };
   mean = 0.0f;
   if (center) {
@@ -106,16 +113,17 @@ __device__ __forceinline__ void row_stats(const float (&v)[NV][E], const Place<T
     group_reduce<T, 1>(s, red, waves, par, OpSum());
     mean = s[0] * invN;
   }
+  const float shift = -mean * scale;
   float s[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float d = counts(i, e) ? v[i][e] - mean : 0.0f;
+      const float d = counts(i, e) ? fmaf(v[i][e], scale, shift) : 0.0f;
       s[0] = fmaf(d, d, s[0]);
     }
   group_reduce<T, 1>(s, red, waves, par, OpSum());
-  rstd = 1.0f / __builtin_sqrtf(s[0] * invN + eps);
+  rstd = 1.0f / __builtin_sqrtf(s[0] * (invN / (scale * scale)) + eps);
 }
 
 // A workgroup is one row's threads, or four waves with a row each.
@@ -128,7 +136,7 @@ struct NormFwd {
   bool center, w_bf16;
   const void* gamma;
   const void* beta;
-  float eps;
+  float eps, scale;
   void* y;
   int64_t ldy;
   float* stats;
@@ -159,7 +167,7 @@ __global__ __launch_bounds__(fwd_threads(T)) void norm_fwd_kernel(NormFwd a) {
     for (int i = 0; i < NV; ++i) to_float<XB, E>(next[i], v[i]);
     if (row + step < a.M) load_row<XB, kShort>(x + (row + step) * a.ldx, a.N, p, next);
     float mean, rstd;
-    row_stats<kShort>(v, p, a.N, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
+    row_stats<kShort>(v, p, a.N, invN, a.scale, a.center, a.eps, red, kWaves, par, mean, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -180,7 +188,7 @@ struct NormBwd {
   int N;
   bool center, w_bf16;
   const void* gamma;
-  float eps;
+  float eps, scale;
   const float* stats;
   void* dX;
   int64_t lddx;
@@ -245,7 +253,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
       to_float<YB, E>(ry[i], dy[i]);
     }
     if (!a.stats)
-      row_stats<kShort>(d, p, a.N, invN, a.center, a.eps, red, kWaves, par, mean, rstd);
+      row_stats<kShort>(d, p, a.N, invN, a.scale, a.center, a.eps, red, kWaves, par, mean, rstd);
     if (row >= a.M) rstd = 0.0f;  // of zeros; with eps = 0 it was infinite
     // With xh = d rstd: dX = rstd (g - c1 - d (rstd c2)), c2 = rstd (sum g d) / N.
     float s[2] = {0.0f, 0.0f};
@@ -392,6 +400,13 @@ hipError_t bwd_width(const NormBwd& a, unsigned grid, hipStream_t st) {
   return bwd<XB, YB, DB, 1024, 2>(a, grid, st);
 }
 
+// 2^-k with the least k that has 4^k >= N.
+float square_scale(int64_t N) {
+  float s = 1.0f;
+  for (int64_t n = 1; n < N; n *= 4) s *= 0.5f;
+  return s;
+}
+
 int bwd_groups(int64_t N) {
   return N <= 512 ? 16 : N <= 1024 ? 8 : N <= 2048 ? 4 : N <= 4096 ? 2 : 1;
 }
@@ -408,7 +423,7 @@ hipError_t launch_norm_fwd(const void* x, int64_t ldx, bool x_bf16, int64_t M, i
                            bool center, const void* gamma, const void* beta, bool w_bf16,
                            float eps, void* y, int64_t ldy, bool y_bf16, float* stats,
                            hipStream_t st) {
-  const NormFwd a{x, ldx, M, (int)N, center, w_bf16, gamma, beta, eps, y, ldy, stats};
+  const NormFwd a{x, ldx, M, (int)N, center, w_bf16, gamma, beta, eps, square_scale(N), y, ldy, stats};
   if (x_bf16) return y_bf16 ? fwd_width<true, true>(a, st) : fwd_width<true, false>(a, st);
   return y_bf16 ? fwd_width<false, true>(a, st) : fwd_width<false, false>(a, st);
 }
@@ -420,8 +435,8 @@ hipError_t launch_norm_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void
                            hipStream_t st) {
   const int ldp = (int)((N + 7) / 8 * 8);
   const bool grads = dgamma || dbeta;
-  const NormBwd a{dY, ldy, x, ldx, M, (int)N, center, w_bf16, gamma, eps, stats, dX, lddx,
-                  grads ? part : nullptr, ldp};
+  const NormBwd a{dY, ldy, x, ldx, M, (int)N, center, w_bf16, gamma, eps, square_scale(N), stats, dX,
+                  lddx, grads ? part : nullptr, ldp};
   const unsigned grid = (unsigned)norm_bwd_parts(M, N);
   hipError_t e = hipSuccess;
   if (M == 0) {
