@@ -26,8 +26,9 @@ def embed_fwd(W, ids, scale):
     return out, U * np.abs(out)
 
 
-def embed_bwd(dY, ids, V, scale, dW=None):
-    """dW given: the gradient is added to it."""
+def embed_bwd(dY, ids, V, scale, dW=None, h=None):
+    """dW given: the gradient is added to it. h: additions between a token's
+    row and its sum (default: as many as the id has tokens)."""
     ids = np.asarray(ids, np.int64)
     live = (ids >= 0) & (ids < V)
     out = np.zeros((V, dY.shape[1]))
@@ -36,7 +37,7 @@ def embed_bwd(dY, ids, V, scale, dW=None):
     np.add.at(out, ids[live], scale * rows)
     np.add.at(size, ids[live], np.abs(scale * rows))
     count = np.bincount(ids[live], minlength=V)[:, None]
-    err = U * (count + 1) * size
+    err = U * ((count if h is None else np.minimum(count, h)) + 1) * size
     if dW is not None:
         out = out + dW
         err = err + U * np.where(count > 0, np.abs(out), 0.0)
@@ -77,10 +78,11 @@ def norm_fwd(x, gamma, beta, eps, center, h=None):
     return y, err, stats, e_stats
 
 
-def norm_bwd(dY, x, gamma, eps, center, h=None):
-    """(dX, err), (dgamma, err), (dbeta, err)."""
+def norm_bwd(dY, x, gamma, eps, center, h=None, hm=None):
+    """(dX, err), (dgamma, err), (dbeta, err). hm: additions between a row and
+    the sums over the rows (default: as many as there are rows)."""
     h = x.shape[1] if h is None else h
-    M = x.shape[0]
+    M = x.shape[0] if hm is None else min(hm, x.shape[0])
     dY = dY.astype(np.float64)
     _, rstd, xh, _, e_rstd, e_xh = _stats(x, eps, center, h)
     g = dY if gamma is None else dY * gamma.astype(np.float64)
