@@ -96,12 +96,17 @@ __device__ __forceinline__ void load_affine(const void* w, bool bf16, int N,
   }
 }
 
-// The statistics of the row in v; `scale` is the 2^-k of the squares.
+// 1 / N, the 2^-k at which deviations are squared, and what the squares' sum is
+// multiplied by, 4^k / N.
+struct Width {
+  float inv, scale, inv_squares;
+};
+
+// The statistics of the row in v.
 template <bool kShort, int T, int NV, int E>
 __device__ __forceinline__ void row_stats(const float (&v)[NV][E], const Place<T, NV, E>& p, int N,
-                                          float invN, float scale, bool center, float eps,
-                                          float* red, int waves, int& par, float& mean,
-                                          float& rstd) {
+                                          const Width& w, bool center, float eps, float* red,
+                                          int waves, int& par, float& mean, float& rstd) {
   const auto counts = [&](int i, int e) { return e >= p.skip[i] && (!kShort || e < N); };
   mean = 0.0f;
   if (center) {
@@ -111,19 +116,19 @@ __device__ __forceinline__ void row_stats(const float (&v)[NV][E], const Place<T
 #pragma unroll
       for (int e = 0; e < E; ++e) s[0] += counts(i, e) ? v[i][e] : 0.0f;
     group_reduce<T, 1>(s, red, waves, par, OpSum());
-    mean = s[0] * invN;
+    mean = s[0] * w.inv;
   }
-  const float shift = -mean * scale;
+  const float shift = -mean * w.scale;
   float s[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      const float d = counts(i, e) ? fmaf(v[i][e], scale, shift) : 0.0f;
+      const float d = counts(i, e) ? fmaf(v[i][e], w.scale, shift) : 0.0f;
       s[0] = fmaf(d, d, s[0]);
     }
   group_reduce<T, 1>(s, red, waves, par, OpSum());
-  rstd = 1.0f / __builtin_sqrtf(s[0] * (invN / (scale * scale)) + eps);
+  rstd = 1.0f / __builtin_sqrtf(s[0] * w.inv_squares + eps);
 }
 
 // A workgroup is one row's threads, or four waves with a row each.
@@ -136,7 +141,8 @@ struct NormFwd {
   bool center, w_bf16;
   const void* gamma;
   const void* beta;
-  float eps, scale;
+  float eps;
+  Width width;
   void* y;
   int64_t ldy;
   float* stats;
@@ -159,7 +165,6 @@ __global__ __launch_bounds__(fwd_threads(T)) void norm_fwd_kernel(NormFwd a) {
   float g[NV][E], b[NV][E];
   load_affine<kShort>(a.gamma, a.w_bf16, a.N, p, 1.0f, g);
   load_affine<kShort>(a.beta, a.w_bf16, a.N, p, 0.0f, b);
-  const float invN = 1.0f / (float)a.N;
   int par = 0;
   for (; row < a.M; row += step) {
     float v[NV][E];
@@ -167,7 +172,7 @@ __global__ __launch_bounds__(fwd_threads(T)) void norm_fwd_kernel(NormFwd a) {
     for (int i = 0; i < NV; ++i) to_float<XB, E>(next[i], v[i]);
     if (row + step < a.M) load_row<XB, kShort>(x + (row + step) * a.ldx, a.N, p, next);
     float mean, rstd;
-    row_stats<kShort>(v, p, a.N, invN, a.scale, a.center, a.eps, red, kWaves, par, mean, rstd);
+    row_stats<kShort>(v, p, a.N, a.width, a.center, a.eps, red, kWaves, par, mean, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -188,7 +193,8 @@ struct NormBwd {
   int N;
   bool center, w_bf16;
   const void* gamma;
-  float eps, scale;
+  float eps;
+  Width width;
   const float* stats;
   void* dX;
   int64_t lddx;
@@ -225,7 +231,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < E; ++e) ag[i][e] = ab[i][e] = 0.0f;
-  const float invN = 1.0f / (float)a.N;
+  const float invN = a.width.inv;
   int par = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * kGroups; row0 < a.M; row0 += step) {
     const int64_t row = row0 + group;
@@ -253,7 +259,7 @@ __global__ __launch_bounds__(kBwdThreads) void norm_bwd_kernel(NormBwd a) {
       to_float<YB, E>(ry[i], dy[i]);
     }
     if (!a.stats)
-      row_stats<kShort>(d, p, a.N, invN, a.scale, a.center, a.eps, red, kWaves, par, mean, rstd);
+      row_stats<kShort>(d, p, a.N, a.width, a.center, a.eps, red, kWaves, par, mean, rstd);
     if (row >= a.M) rstd = 0.0f;  // of zeros; with eps = 0 it was infinite
     // With xh = d rstd: dX = rstd (g - c1 - d (rstd c2)), c2 = rstd (sum g d) / N.
     float s[2] = {0.0f, 0.0f};
@@ -400,11 +406,14 @@ hipError_t bwd_width(const NormBwd& a, unsigned grid, hipStream_t st) {
   return bwd<XB, YB, DB, 1024, 2>(a, grid, st);
 }
 
-// 2^-k with the least k that has 4^k >= N.
-float square_scale(int64_t N) {
-  float s = 1.0f;
-  for (int64_t n = 1; n < N; n *= 4) s *= 0.5f;
-  return s;
+// k is the least that has 4^k >= N.
+Width width_of(int64_t N) {
+  Width w{1.0f / (float)N, 1.0f, 1.0f / (float)N};
+  for (int64_t n = 1; n < N; n *= 4) {
+    w.scale *= 0.5f;
+    w.inv_squares *= 4.0f;
+  }
+  return w;
 }
 
 int bwd_groups(int64_t N) {
@@ -423,7 +432,7 @@ hipError_t launch_norm_fwd(const void* x, int64_t ldx, bool x_bf16, int64_t M, i
                            bool center, const void* gamma, const void* beta, bool w_bf16,
                            float eps, void* y, int64_t ldy, bool y_bf16, float* stats,
                            hipStream_t st) {
-  const NormFwd a{x, ldx, M, (int)N, center, w_bf16, gamma, beta, eps, square_scale(N), y, ldy, stats};
+  const NormFwd a{x, ldx, M, (int)N, center, w_bf16, gamma, beta, eps, width_of(N), y, ldy, stats};
   if (x_bf16) return y_bf16 ? fwd_width<true, true>(a, st) : fwd_width<true, false>(a, st);
   return y_bf16 ? fwd_width<false, true>(a, st) : fwd_width<false, false>(a, st);
 }
@@ -435,7 +444,7 @@ hipError_t launch_norm_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void
                            hipStream_t st) {
   const int ldp = (int)((N + 7) / 8 * 8);
   const bool grads = dgamma || dbeta;
-  const NormBwd a{dY, ldy, x, ldx, M, (int)N, center, w_bf16, gamma, eps, square_scale(N), stats, dX,
+  const NormBwd a{dY, ldy, x, ldx, M, (int)N, center, w_bf16, gamma, eps, width_of(N), stats, dX,
                   lddx, grads ? part : nullptr, ldp};
   const unsigned grid = (unsigned)norm_bwd_parts(M, N);
   hipError_t e = hipSuccess;
