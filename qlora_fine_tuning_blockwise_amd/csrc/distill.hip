@@ -26,7 +26,11 @@
 //
 // Memory bounds both on long rows: the forward's pass over 2048 x 128000 bf16
 // runs at 6.7 TB/s (7.0 TB/s is what reading alone reaches here). On short rows
-// and few rows the chain of dependent loads does.
+// and few rows the chain of dependent loads does. Since every wave of every
+// piece loads all of a row's entries, many of them cost time: with k = 64, 256
+// and 1024 entries 512 x 32000 bf16 takes 10.4, 13.0 and 27.8 us forward and
+// 16.8, 21.6 and 60 us backward, 2048 x 128000 89, 98 and 226 us and 175, 189 and
+// 414 us.
 #include "rows.h"
 
 namespace qlora {

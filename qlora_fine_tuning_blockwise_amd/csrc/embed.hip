@@ -30,7 +30,10 @@ constexpr int32_t kDead = 0x7fffffff;  // key of an id outside of the table: sor
 // walks through every other run: up to kMaxRun tokens are one run (the search
 // is a launch of 6 us). Measured with runs of 512, 1024 and 2048 tokens: 16000
 // tokens of 1024 columns 43.2, 41.5 and 44.0 us; with 1024, 2048 and 4096: 30000
-// tokens of 500 columns 57.8, 54.9 and 61.4 us.
+// tokens of 500 columns 57.8, 54.9 and 61.4 us. Every token searches every other
+// run, so the search grows with the square of the tokens and is most of the call
+// from 65536 on: bf16 rows into 32000 x 1024 fp32, 32768, 65536, 131072, 262144
+// and 2^20 tokens: 70, 132, 297, 837 and 9980 us.
 constexpr int kMaxRun = 4096;
 int run_length(int64_t M) { return M <= kMaxRun ? kMaxRun : M <= 20000 ? 1024 : 2048; }
 
@@ -86,12 +89,12 @@ __global__ __launch_bounds__(256) void embed_fwd_kernel(EmbedFwd a) {
 // ---------------------------------------------------------------- the sort
 // The first workgroups order 16 tokens each (sixteen threads a token, each of
 // which compares it with every sixteenth group of four of its run's keys); the
-// others write zeros over dW or a part of it. The fill is nontemporal: with plain stores it leaves the Infinity
-// Cache full of lines that have yet to reach memory, and the sums that follow
-// wait for them (4096 tokens, 32000 x 4096 fp32: the sums take 23 against 13.7
-// us, the call 115 against 99 us). A workgroup writes 4 KB and ends: with a
-// quarter as many, four stores a thread, the call takes 101 us, with 8192 and
-// sixteen stores 130 us.
+// others write zeros over dW or a part of it. The fill is nontemporal: with
+// plain stores it leaves the Infinity Cache full of lines that have yet to reach
+// memory, and the sums that follow wait for them (4096 tokens, 32000 x 4096
+// fp32: the sums take 23 against 13.7 us, the call 115 against 99 us). A
+// workgroup writes 4 KB and ends: with a quarter as many, four stores a thread,
+// the call takes 101 us, with 8192 and sixteen stores 130 us.
 constexpr int kOrderTokens = 16, kOrderThreads = 256;
 
 // The keys of a run's n tokens into LDS, up to the next multiple of four, with
@@ -427,7 +430,7 @@ hipError_t sums(const EmbedBwd& a, hipStream_t st) {
 
 }  // namespace
 
-// Tokens of a tile (at most 62, which a wave's lanes hold). Up to 32 tokens are
+// Tokens of a tile (a wave's lanes hold at most 64). Up to 32 tokens are
 // one tile, so that nothing is left to join (20 tokens of 4096 columns: 14.3
 // against 16.8 us); above, shorter tiles give more waves and longer ones fewer
 // parts (tiles of 8, 16 and 32: 4096 x 256 24.8, 24.1 and 27.6 us, 16000 x 1024

@@ -394,7 +394,10 @@ hipError_t bwd(const NormBwd& a, unsigned grid, hipStream_t st) {
 // elements a thread leave too few registers. Measured, us: 32768 x 512 64 x 1
 // 31.9, 128 x 1 32.1, 256 x 1 46; 16384 x 1024 128 x 1 28.4, 64 x 2 50, 256 x 1
 // 31.0; 8192 x 2048 256 x 1 26.3, 128 x 2 41, 512 x 1 29.9; 4096 x 4096 512 x 1
-// 27.2, 256 x 2 40; 2048 x 8192 1024 x 1 27.6, 512 x 2 39.
+// 27.2, 256 x 2 40; 2048 x 8192 1024 x 1 27.6, 512 x 2 39. Rows past 8192 need 16
+// elements a thread all the same: those builds sit at the limit of 128 registers
+// and, but for the one that is bf16 throughout, keep 4 to 28 more in scratch
+// (2048 x 16384 bf16 48 us for 201 MB, fp32 95 us for 403 MB).
 template <bool XB, bool YB, bool DB>
 hipError_t bwd_width(const NormBwd& a, unsigned grid, hipStream_t st) {
   if (a.N < (XB && YB && DB ? 8 : 4)) return bwd<XB, YB, DB, 64, 1, true>(a, grid, st);
