@@ -27,38 +27,38 @@ PROJECTIONS = [(1, 1), (1, 1), (1, 1), (1, 1), (1, 2.6875), (1, 2.6875), (2.6875
 def listed():
     return [
         # A decoded token joins the residual stream: latency is all there is.
-        dict(name="add norm fwd, one token", op="add_norm_fwd", M=1, N=4096, center=False, bias=False,
+        dict(name="add norm fwd one token", op="add_norm_fwd", M=1, N=4096, center=False, bias=False,
              x="bf16", h="bf16", y="bf16", w="bf16"),
         # A training batch of 4 x 1024 tokens; the normed rows are kept in 8 bits.
-        dict(name="add norm fwd, batch, 8 bits", op="add_norm_fwd", M=4096, N=4096, center=False, bias=False,
+        dict(name="add norm fwd batch 8 bits", op="add_norm_fwd", M=4096, N=4096, center=False, bias=False,
              x="bf16", h="bf16", y="e4m3", w="bf16"),
         # An fp32 residual stream of odd width behind bf16 layers.
-        dict(name="add norm bwd, odd width", op="add_norm_bwd", M=1001, N=5003, center=True, bias=True,
+        dict(name="add norm bwd odd width", op="add_norm_bwd", M=1001, N=5003, center=True, bias=True,
              x="bf16", h="f32", y="bf16", w="f32"),
         # The backward pass of the residual stream of 2048 tokens.
-        dict(name="add norm bwd, batch", op="add_norm_bwd", M=2048, N=8192, center=False, bias=False,
+        dict(name="add norm bwd batch", op="add_norm_bwd", M=2048, N=8192, center=False, bias=False,
              x="bf16", h="bf16", y="bf16", w="bf16"),
         # One answer token scored against the whole vocabulary.
-        dict(name="head loss fwd, one token", op="head_fwd", M=1, V=32000, K=4096, empty=0.0, ids="int64"),
+        dict(name="head loss fwd one token", op="head_fwd", M=1, V=32000, K=4096, empty=0.0, ids="int64"),
         # A training batch over a large vocabulary; prompt tokens carry no loss.
-        dict(name="head loss fwd, batch", op="head_fwd", M=2048, V=128000, K=4096, empty=0.25, ids="int64"),
+        dict(name="head loss fwd batch", op="head_fwd", M=2048, V=128000, K=4096, empty=0.25, ids="int64"),
         # A vocabulary with added tokens, an odd hidden size, a ragged batch.
-        dict(name="head loss fwd, odd sizes", op="head_fwd", M=1001, V=32003, K=1027, empty=0.1, ids="int32"),
+        dict(name="head loss fwd odd sizes", op="head_fwd", M=1001, V=32003, K=1027, empty=0.1, ids="int32"),
         # The gradient for a few answer tokens through a frozen head.
-        dict(name="head loss bwd, few rows", op="head_bwd", M=8, V=32000, K=4096, empty=0.0, ids="int64",
+        dict(name="head loss bwd few rows", op="head_bwd", M=8, V=32000, K=4096, empty=0.0, ids="int64",
              dw=False, g="bf16"),
         # The gradient of a training batch through a frozen head, the largest
         # of the cases.
-        dict(name="head loss bwd, batch", op="head_bwd", M=2048, V=128000, K=4096, empty=0.25, ids="int64",
+        dict(name="head loss bwd batch", op="head_bwd", M=2048, V=128000, K=4096, empty=0.25, ids="int64",
              dw=False, g="bf16"),
         # A trained head with added tokens: both gradients.
-        dict(name="head loss bwd, trained head", op="head_bwd", M=1500, V=32003, K=2048, empty=0.0, ids="int32",
+        dict(name="head loss bwd trained head", op="head_bwd", M=1500, V=32003, K=2048, empty=0.0, ids="int32",
              dw=True, g="bf16"),
         # The adapters of 32 layers, each projection's two matrices a tensor of
         # its own.
-        dict(name="clip, adapters of 32 layers", op="clip", layers=32, hidden=4096, r=16, odd=False, g="bf16"),
+        dict(name="clip adapters of 32 layers", op="clip", layers=32, hidden=4096, r=16, odd=False, g="bf16"),
         # One flat buffer of all adapters' gradients, in fp32.
-        dict(name="clip, flat buffer", op="clip", layers=0, hidden=1 << 25, r=1, odd=False, g="f32"),
+        dict(name="clip flat buffer", op="clip", layers=0, hidden=1 << 25, r=1, odd=False, g="f32"),
     ]
 
 
