@@ -92,6 +92,8 @@ extern "C" {
 /* Index types (token ids of the row operators). */
 #define QLORA_DTYPE_I32 2
 #define QLORA_DTYPE_I64 3
+/* FP8 E4M3 (OCP E4M3FN) with one fp32 scale a row: an output of qlora_add_norm_fwd. */
+#define QLORA_DTYPE_E4M3 4
 
 /* Second-level formats of absmax_q (see STORAGE FORMAT). */
 #define QLORA_DQ_INT8 0
@@ -125,6 +127,7 @@ extern "C" {
 #define QLORA_MAX_SORTED (1 << 20)     /* tokens of qlora_embed_bwd */
 #define QLORA_MAX_NORM_WIDTH 16384     /* elements of a normed row */
 #define QLORA_MAX_TOP 1024             /* teacher entries of a row */
+#define QLORA_MAX_TENSORS (1 << 20)    /* tensors of a gradient's norm */
 
 /* Format version of the storage layout above. */
 #define QLORA_FORMAT_VERSION 1u
@@ -535,6 +538,93 @@ int qlora_distill_bwd(const void* logits, int64_t ldz, int z_dtype, int64_t M, i
                       const void* top_ids, int ids_dtype, const void* top_logits, int t_dtype,
                       int k, float temperature, const float* stats, const float* dloss,
                       void* dlogits, int64_t ldg, int grad_dtype, void* stream);
+
+/* THE CLOSE OF A STEP: the norm behind a residual addition, the loss of the
+ * vocabulary head, and the clipping of the gradients' global norm. What is said
+ * of the row operators holds for these too: strides, alignment, sums in fp32 or
+ * more, one rounding an output, the same bits on every run, no shared memory
+ * between outputs and inputs but where it is named, M == 0 a successful no-op,
+ * nothing allocated on the device, no synchronisation, capture into a HIP
+ * graph. */
+
+/* Norm behind a residual addition (the residual stream of the layers around
+ * [P3] "How it works"):
+ *   h = x + residual, rounded to r_dtype;  y = the norm of h (qlora_norm_fwd)
+ *   x [M,N] (x_dtype), residual and h [M,N] (r_dtype); h may be x (of the same
+ *   type and stride) or residual itself. residual and h both NULL: the norm of
+ *   x, r_dtype is ignored.
+ *   y [M,N]: fp32, bf16, or QLORA_DTYPE_E4M3, bytes with one scale a row in
+ *   scales (fp32 [M]; NULL for the other types):
+ *     scale = max |y| / 448 (0 for a row of zeros),  code = e4m3(y * (448 / max |y|)),
+ *   rounded to nearest even; a row with a NaN has the scale NaN and codes NaN.
+ *   stats  fp32 [2,M] or NULL, as of qlora_norm_fwd, of h.
+ * Limits and errors as qlora_norm_fwd; QLORA_ERR_INVALID_ARG for one of
+ * residual and h without the other, or scales without (or missing for) E4M3. */
+int qlora_add_norm_fwd(const void* x, int64_t ldx, int x_dtype, const void* residual, int64_t ldr,
+                       int r_dtype, int64_t M, int64_t N, int norm, const void* gamma,
+                       const void* beta, int w_dtype, float eps, void* h, int64_t ldh, void* y,
+                       int64_t ldy, int y_dtype, float* scales, float* stats, void* stream);
+
+/* Its gradients: dX = qlora_norm_bwd's dX of (dY, h) + dH, the gradient of x
+ * and of the residual alike; dgamma and dbeta as there.
+ *   dH [M,N] (dx_dtype), the gradient that reaches h by itself, or NULL (0);
+ *   h [M,N] (h_dtype) and stats from the forward; dX may be dY, dH or h itself
+ *   (the same address, type and stride).
+ * The other arguments, the workspace (qlora_norm_bwd_workspace_bytes) and the
+ * errors as qlora_norm_bwd. */
+int qlora_add_norm_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* dH, int64_t lddh,
+                       const void* h, int64_t ldh, int h_dtype, int64_t M, int64_t N, int norm,
+                       const void* gamma, int w_dtype, float eps, const float* stats, void* dX,
+                       int64_t lddx, int dx_dtype, void* dgamma, void* dbeta, int grad_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* One of many tensors: n contiguous elements, aligned to their type. */
+typedef struct qlora_tensor {
+  void* data;       /* device; may be NULL where n == 0 */
+  int64_t n;        /* elements */
+  int32_t dtype;    /* QLORA_DTYPE_F32 or QLORA_DTYPE_BF16 */
+  int32_t reserved; /* 0 */
+} qlora_tensor;
+
+/* Device workspace, in bytes, of qlora_grad_norm for these tensors (their sizes
+ * alone count). Host only; 0 for invalid ones and for no elements. */
+size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* grads, int64_t count);
+
+/* Global norm of many tensors ([P2] s3: only the adapters have gradients, two
+ * tensors a projection) and the factor that clips it:
+ *   result[0] = norm = sqrt(sum over all elements of g^2)
+ *   result[1] = max_norm / norm where norm > max_norm, else 1
+ *   grads   host array of count descriptors, read during the call only;
+ *   result  fp32 [2], device;  max_norm >= 0 (infinity: the factor is 1).
+ * Squares and sums are in 64 bits, so values of every size have their norm. A
+ * norm that is infinite gives the factor 0, a NaN gives NaN: a caller that skips
+ * such steps looks at the norm. A tensor that is listed twice counts twice. No
+ * elements: norm 0, factor 1. QLORA_ERR_INVALID_ARG for count < 0, n < 0,
+ * reserved != 0, a NULL array, max_norm < 0 or NaN; QLORA_ERR_SHAPE past
+ * QLORA_MAX_TENSORS tensors or 2^40 elements; QLORA_ERR_DTYPE, QLORA_ERR_ALIGN
+ * and QLORA_ERR_WORKSPACE as elsewhere. */
+int qlora_grad_norm(const qlora_tensor* grads, int64_t count, float max_norm, float* result,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* out[i] = RN(grads[i] * factor) for every tensor, in its own type.
+ *   out     host array of count descriptors with the sizes and types of grads
+ *           (QLORA_ERR_SHAPE, QLORA_ERR_DTYPE otherwise), or NULL: in place. An
+ *           out[i] may be grads[i]; a factor of 1 then leaves it untouched.
+ *   factor  fp32, device: for instance result + 1 of qlora_grad_norm.
+ * QLORA_ERR_INVALID_ARG where an output shares memory with another output (a
+ * tensor listed twice, in place), another input or the factor. Other errors as
+ * qlora_grad_norm; QLORA_ERR_INTERNAL if the host has no memory for that check. */
+int qlora_grad_scale(const qlora_tensor* grads, const qlora_tensor* out, int64_t count,
+                     const float* factor, void* stream);
+
+/* qlora_adamw_step on the gradient grad * factor, each product rounded to fp32
+ * before the step's first operation; factor is fp32 on the device (NULL:
+ * QLORA_ERR_INVALID_ARG): clipping without a pass over the gradients. Everything
+ * else as qlora_adamw_step. */
+int qlora_adamw_step_scaled(float* param, const void* grad, int grad_dtype, const float* factor,
+                            float* exp_avg, float* exp_avg_sq, uint16_t* param_bf16, int64_t n,
+                            double lr, double beta1, double beta2, double eps, double weight_decay,
+                            int64_t step, void* stream);
 
 #ifdef __cplusplus
 }

@@ -7,13 +7,15 @@ The functions below carry the names of the C entry points
 memory and the current stream, and every step of the computation runs in
 libqlora_amd.so. Tensors must be contiguous and on a ROCm device.
 
-The row operators (qlora_embed_*, qlora_norm_*, qlora_distill_*) take
-matrices whose rows are contiguous, at any row stride (views of wider or
+The row operators (qlora_embed_*, qlora_norm_*, qlora_distill_*,
+qlora_add_norm_*) take matrices whose rows are contiguous, at any row stride (views of wider or
 longer tensors), and run on the device of their tensors whichever is current.
 Without `stream` they use that device's current stream; with it, what they
 allocate belongs to that stream. A given output may not share memory with an
 input or another output (the library refuses the call); only qlora_norm_fwd's
-y may be x itself.
+y may be x itself, and qlora_add_norm_fwd's h x or the residual. The clipping of
+the gradients (qlora_grad_norm, qlora_grad_scale) takes contiguous tensors, one
+by one or as a list that the program keeps (qlora_tensor_list).
 """
 from __future__ import annotations
 
@@ -32,7 +34,9 @@ __all__ = [
     "qlora_embed_fwd", "qlora_embed_bwd", "qlora_embed_bwd_workspace_bytes",
     "qlora_norm_fwd", "qlora_norm_bwd", "qlora_norm_bwd_workspace_bytes",
     "qlora_distill_fwd", "qlora_distill_bwd", "qlora_distill_fwd_workspace_bytes",
-    "NORM_LAYER", "NORM_RMS",
+    "qlora_add_norm_fwd", "qlora_add_norm_bwd",
+    "qlora_tensor_list", "qlora_grad_norm", "qlora_grad_norm_workspace_bytes", "qlora_grad_scale",
+    "TensorList", "NORM_LAYER", "NORM_RMS",
     "NF4Weight", "DQ_INT8", "DQ_UINT8", "DQ_E4M3", "LAYOUT_ROWS", "LAYOUT_KSLAB32",
 ]
 
@@ -343,14 +347,21 @@ def qlora_merge_lora(A: torch.Tensor, B: torch.Tensor, alpha: float, w: NF4Weigh
     return out
 
 
+def _one_factor(t, name):
+    if t.numel() != 1 or t.dtype != torch.float32 or t.device.type != "cuda":
+        raise ValueError(f"{name}: one fp32 value on the device")
+
 
 def qlora_adamw_step(param: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Tensor,
                      exp_avg_sq: torch.Tensor, step: int, lr: float, beta1: float = 0.9,
                      beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
-                     param_bf16: torch.Tensor | None = None, stream=None) -> None:
+                     param_bf16: torch.Tensor | None = None, stream=None,
+                     grad_factor: torch.Tensor | None = None) -> None:
     """One AdamW step in place on flat fp32 master values, moments and an
     optional bf16 copy; grad is bf16 or fp32. The arrays may be device tensors
-    or pinned host tensors (the paged state); the step runs on the GPU."""
+    or pinned host tensors (the paged state); the step runs on the GPU.
+    grad_factor: one fp32 value on the device that the gradient is multiplied
+    by, such as the second of qlora_grad_norm's result."""
     n = param.numel()
     for name, t, dt in (("param", param, torch.float32), ("exp_avg", exp_avg, torch.float32),
                         ("exp_avg_sq", exp_avg_sq, torch.float32),
@@ -359,6 +370,14 @@ def qlora_adamw_step(param: torch.Tensor, grad: torch.Tensor, exp_avg: torch.Ten
             raise ValueError(f"qlora_adamw_step: {name} must be {dt} with {n} elements")
     if grad.numel() != n:
         raise ValueError("qlora_adamw_step: grad must have as many elements as param")
+    if grad_factor is not None:
+        _one_factor(grad_factor, "grad_factor")
+        st = _lib.load().qlora_adamw_step_scaled(
+            _ptr(param), _ptr(grad), _dtype_code(grad.dtype), _ptr(grad_factor), _ptr(exp_avg),
+            _ptr(exp_avg_sq), _ptr(param_bf16), n, float(lr), float(beta1), float(beta2), float(eps),
+            float(weight_decay), int(step), _stream(stream))
+        _lib.check(st, "qlora_adamw_step_scaled")
+        return
     st = _lib.load().qlora_adamw_step(_ptr(param), _ptr(grad), _dtype_code(grad.dtype),
                                       _ptr(exp_avg), _ptr(exp_avg_sq), _ptr(param_bf16), n,
                                       float(lr), float(beta1), float(beta2), float(eps),
@@ -406,12 +425,12 @@ def _here(dev):
     return torch.cuda.current_stream(dev).cuda_stream
 
 
-def _matrix(t, name, shape, device) -> int:
-    """Row stride of a [rows, width] fp32 or bf16 matrix whose rows are
-    contiguous; shape and device checked."""
+def _matrix(t, name, shape, device, codes=False) -> int:
+    """Row stride of a [rows, width] fp32 or bf16 matrix (or one of 8-bit codes)
+    whose rows are contiguous; shape and device checked."""
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype not in _FLOATS:
+    if t.dtype not in _FLOATS and not codes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected fp32 or bf16")
     if t.device != device:
         raise ValueError(f"{name}: on {t.device}, expected {device}")
@@ -670,3 +689,198 @@ def qlora_distill_bwd(logits: torch.Tensor, top_ids: torch.Tensor, top_logits: t
     if st:
         _lib.check(st, "qlora_distill_bwd")
     return dlogits
+
+
+# ------------------------------------------------------- the close of a step
+def qlora_add_norm_fwd(x: torch.Tensor, residual: torch.Tensor | None = None,
+                       gamma: torch.Tensor | None = None, beta: torch.Tensor | None = None,
+                       eps: float = 1e-5, norm: int = NORM_LAYER, h: torch.Tensor | None = None,
+                       y: torch.Tensor | None = None, y_dtype=None,
+                       scales_out: torch.Tensor | None = None,
+                       stats_out: torch.Tensor | None = None, stream=None):
+    """h = x + residual in the residual's dtype, and y = the norm of h (as
+    qlora_norm_fwd; in x's dtype by default). y_dtype torch.float8_e4m3fn: codes
+    of 8 bits with one scale a row, written to scales_out (fp32 [M], needed then).
+    h may be given, also as x or residual itself. stats_out: fp32 [2,M]. Without a
+    residual h is x. Returns (y, h)."""
+    M, N = _two_dims(x, "x")
+    dev = x.device
+    ldx = _matrix(x, "x", (M, N), dev)
+    ldr = ldh = max(N, 1)
+    if residual is not None:
+        ldr = _matrix(residual, "residual", (M, N), dev)
+    elif h is not None:
+        raise ValueError("qlora_add_norm_fwd: h needs a residual")
+    w_dtype = _norm_vectors(N, dev, (gamma, "gamma"), (beta, "beta"))
+    if stats_out is not None:
+        _vector(stats_out, "stats_out", (2, M), _F32, dev)
+    if y is not None:
+        y_dtype = y.dtype
+    elif y_dtype is None:
+        y_dtype = x.dtype
+    codes = y_dtype == torch.float8_e4m3fn
+    if not codes and y_dtype not in _FLOATS:
+        raise ValueError(f"qlora_add_norm_fwd: y of {y_dtype}, expected fp32, bf16 or float8_e4m3fn")
+    if codes != (scales_out is not None):
+        raise ValueError("qlora_add_norm_fwd: scales_out goes with y of float8_e4m3fn")
+    if codes:
+        _vector(scales_out, "scales_out", (M,), _F32, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_add_norm_fwd(x, residual, gamma, beta, eps, norm, h, y, y_dtype, scales_out,
+                                      stats_out)
+    if residual is not None:
+        if h is None:
+            h, ldh = _new(residual, M, N, None)
+        else:
+            ldh = _matrix(h, "h", (M, N), dev)
+            if h.dtype != residual.dtype:
+                raise ValueError(f"h: dtype {h.dtype}, the residual's is {residual.dtype}")
+    if y is None:
+        y, ldy = x.new_empty((M, N), dtype=y_dtype), max(N, 1)
+    else:
+        ldy = _matrix(y, "y", (M, N), dev, codes)
+    st = _lib.load().qlora_add_norm_fwd(
+        _at(x), ldx, _FLOATS[x.dtype], _at(residual), ldr,
+        0 if residual is None else _FLOATS[residual.dtype], M, N, norm, _at(gamma), _at(beta),
+        w_dtype, eps, _at(h), ldh, _at(y), ldy, _lib.DTYPE_E4M3 if codes else _FLOATS[y_dtype],
+        _at(scales_out), _at(stats_out), _here(dev))
+    if st:
+        _lib.check(st, "qlora_add_norm_fwd")
+    return y, x if residual is None else h
+
+
+def qlora_add_norm_bwd(dY: torch.Tensor, h: torch.Tensor, dH: torch.Tensor | None = None,
+                       gamma: torch.Tensor | None = None, eps: float = 1e-5,
+                       norm: int = NORM_LAYER, stats: torch.Tensor | None = None,
+                       want_dx: bool = True, want_dgamma: bool = True, want_dbeta: bool = True,
+                       dx_dtype=None, grad_dtype=torch.float32, dX: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """Returns (dX or None, dgamma or None, dbeta or None) of the norm behind a
+    residual addition: dX, the gradient of x and of the residual, is the norm's
+    plus dH, the gradient that reaches h by itself. dX has dH's dtype (h's without
+    dH) unless dx_dtype or dX says another, which dH must then have too."""
+    M, N = _two_dims(h, "h")
+    dev = h.device
+    ldh = _matrix(h, "h", (M, N), dev)
+    ldy = _matrix(dY, "dY", (M, N), dev)
+    lddh = lddx = max(N, 1)
+    if dX is not None:
+        lddx = _matrix(dX, "dX", (M, N), dev)
+        dx_dtype = dX.dtype
+    if dx_dtype is None:
+        dx_dtype = h.dtype if dH is None else dH.dtype
+    if dH is not None:
+        lddh = _matrix(dH, "dH", (M, N), dev)
+        if dH.dtype != dx_dtype:
+            raise ValueError(f"dH: dtype {dH.dtype}, dX has {dx_dtype}")
+    w_dtype = _norm_vectors(N, dev, (gamma, "gamma"))
+    if stats is not None:
+        _vector(stats, "stats", (2, M), _F32, dev)
+    if dx_dtype not in _FLOATS or grad_dtype not in _FLOATS:
+        raise ValueError("qlora_add_norm_bwd: gradients are fp32 or bf16")
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_add_norm_bwd(dY, h, dH, gamma, eps, norm, stats, want_dx, want_dgamma,
+                                      want_dbeta, dx_dtype, grad_dtype, dX, workspace)
+    if dX is None and want_dx:
+        dX = torch.empty((M, N), dtype=dx_dtype, device=dev)
+    dgamma = torch.empty(N, dtype=grad_dtype, device=dev) if want_dgamma else None
+    dbeta = torch.empty(N, dtype=grad_dtype, device=dev) if want_dbeta else None
+    need = qlora_norm_bwd_workspace_bytes(M, N) if want_dgamma or want_dbeta else 0
+    if need or workspace is not None:
+        workspace = _bytes(workspace, need, dev)
+    st = _lib.load().qlora_add_norm_bwd(
+        _at(dY), ldy, _FLOATS[dY.dtype], _at(dH), lddh, _at(h), ldh, _FLOATS[h.dtype], M, N, norm,
+        _at(gamma), w_dtype, eps, _at(stats), _at(dX) if want_dx else None, lddx, _FLOATS[dx_dtype],
+        _at(dgamma), _at(dbeta), _FLOATS[grad_dtype], _at(workspace),
+        0 if workspace is None else workspace.numel(), _here(dev))
+    if st:
+        _lib.check(st, "qlora_add_norm_bwd")
+    return dX if want_dx else None, dgamma, dbeta
+
+
+class TensorList:
+    """Tensors as qlora_grad_norm and qlora_grad_scale take them: contiguous,
+    fp32 or bf16, on one device. A program whose gradients stay where they are
+    makes the list once; it holds the tensors, which must keep their storage."""
+
+    def __init__(self, tensors):
+        self.tensors = tuple(tensors)
+        self.device = self.tensors[0].device if self.tensors else None
+        self.array = (_lib.Tensor * max(1, len(self.tensors)))()
+        for d, t in zip(self.array, self.tensors):
+            if t.dtype not in _FLOATS:
+                raise ValueError(f"tensors: dtype {t.dtype}, expected fp32 or bf16")
+            if not t.is_contiguous():
+                raise ValueError("tensors: must be contiguous")
+            if t.device != self.device:
+                raise ValueError(f"tensors: on {t.device} and on {self.device}")
+            d.data, d.n, d.dtype, d.reserved = t.data_ptr(), t.numel(), _FLOATS[t.dtype], 0
+        self.address = ctypes.addressof(self.array)
+        self.workspace_bytes = int(_lib.load().qlora_grad_norm_workspace_bytes(
+            self.address, len(self.tensors)))
+
+    def __len__(self):
+        return len(self.tensors)
+
+
+def qlora_tensor_list(tensors) -> TensorList:
+    """The tensors as a list that a program keeps (see TensorList)."""
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+
+
+def qlora_grad_norm_workspace_bytes(grads) -> int:
+    return qlora_tensor_list(grads).workspace_bytes
+
+
+def qlora_grad_norm(grads, max_norm: float = float("inf"), result: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """fp32 [2] on the device: the global norm of all gradients (a TensorList or
+    tensors), and the factor that clips it to max_norm (1 where the norm is not
+    above it)."""
+    grads = qlora_tensor_list(grads)
+    dev = grads.device
+    if dev is None:
+        if result is None:
+            raise ValueError("qlora_grad_norm: no tensors, and no result to say on which device")
+        dev = result.device
+    if result is not None:
+        _vector(result, "result", (2,), _F32, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_grad_norm(grads, max_norm, result, workspace)
+    if result is None:
+        result = torch.empty(2, dtype=torch.float32, device=dev)
+    if grads.workspace_bytes or workspace is not None:
+        workspace = _bytes(workspace, grads.workspace_bytes, dev)
+    st = _lib.load().qlora_grad_norm(grads.address, len(grads), max_norm, _at(result),
+                                     _at(workspace), 0 if workspace is None else workspace.numel(),
+                                     _here(dev))
+    if st:
+        _lib.check(st, "qlora_grad_norm")
+    return result
+
+
+def qlora_grad_scale(grads, factor: torch.Tensor, out=None, stream=None) -> None:
+    """Every gradient times factor (one fp32 value on the device, such as
+    qlora_grad_norm's result[1:]), in place or into out (a TensorList or tensors
+    of the same sizes and dtypes)."""
+    grads = qlora_tensor_list(grads)
+    dev = grads.device
+    _one_factor(factor, "factor")
+    if dev is None:
+        return
+    if factor.device != dev:
+        raise ValueError(f"factor: on {factor.device}, expected {dev}")
+    if out is not None:
+        out = qlora_tensor_list(out)
+        if len(out) != len(grads) or out.device != dev:
+            raise ValueError("qlora_grad_scale: out needs as many tensors, on the same device")
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_grad_scale(grads, factor, out)
+    st = _lib.load().qlora_grad_scale(grads.address, None if out is None else out.address,
+                                      len(grads), _at(factor), _here(dev))
+    if st:
+        _lib.check(st, "qlora_grad_scale")

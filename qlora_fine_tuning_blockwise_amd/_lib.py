@@ -18,6 +18,7 @@ DTYPE_F32 = 0
 DTYPE_BF16 = 1
 DTYPE_I32 = 2
 DTYPE_I64 = 3
+DTYPE_E4M3 = 4
 NORM_LAYER = 0
 NORM_RMS = 1
 LAYOUT_ROWS = 0
@@ -44,6 +45,11 @@ class NF4Desc(ctypes.Structure):
     _fields_ = [("N", I64), ("K", I64), ("codes", P), ("absmax_q", P), ("absmax_scale", P),
                 ("dq_format", ctypes.c_int32), ("format_version", ctypes.c_uint32),
                 ("setup_id", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
+class Tensor(ctypes.Structure):
+    """struct qlora_tensor of include/qlora_amd.h."""
+    _fields_ = [("data", P), ("n", I64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 DESC = ctypes.POINTER(NF4Desc)
@@ -77,6 +83,14 @@ SIGNATURES = {
     "qlora_distill_fwd": (INT, [P, I64, INT, I64, I64, P, INT, P, INT, INT, FLT, P, P, P, SZ, P]),
     "qlora_distill_bwd": (INT, [P, I64, INT, I64, I64, P, INT, P, INT, INT, FLT, P, P, P, I64, INT,
                                 P]),
+    "qlora_add_norm_fwd": (INT, [P, I64, INT, P, I64, INT, I64, I64, INT, P, P, INT, FLT, P, I64, P,
+                                 I64, INT, P, P, P]),
+    "qlora_add_norm_bwd": (INT, [P, I64, INT, P, I64, P, I64, INT, I64, I64, INT, P, INT, FLT, P, P,
+                                 I64, INT, P, P, INT, P, SZ, P]),
+    "qlora_grad_norm_workspace_bytes": (SZ, [P, I64]),
+    "qlora_grad_norm": (INT, [P, I64, FLT, P, P, SZ, P]),
+    "qlora_grad_scale": (INT, [P, P, I64, P, P]),
+    "qlora_adamw_step_scaled": (INT, [P, P, INT, P, P, P, P, I64, DBL, DBL, DBL, DBL, DBL, I64, P]),
 }
 
 _lib = None

@@ -48,12 +48,16 @@ __device__ __forceinline__ void adam_elem(float& p, float& m, float& v, float g,
 
 __device__ __forceinline__ uint16_t bf16_bits(float x) { return (uint16_t)pack_bf16x2(x, 0.0f); }
 
-template <bool kGradBf16>
+// kScaled: the gradient is first multiplied by *factor (one more rounding), the
+// clipping factor that qlora_grad_norm left on the device; a pass over the
+// gradients less than scaling them in memory.
+template <bool kGradBf16, bool kScaled>
 __global__ __launch_bounds__(256) void adamw_kernel(float* __restrict__ p,
                                                     const void* __restrict__ g,
                                                     float* __restrict__ m, float* __restrict__ v,
                                                     uint16_t* __restrict__ pb, int64_t n,
-                                                    AdamScalars s) {
+                                                    AdamScalars s, const float* factor) {
+  const float f = kScaled ? *factor : 1.0f;
   const int64_t e0 = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 8;
   if (e0 >= n) return;
   if (e0 + 8 <= n) {
@@ -91,7 +95,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(float* __restrict__ p,
       ve[4 * h] = vv[h].x; ve[4 * h + 1] = vv[h].y; ve[4 * h + 2] = vv[h].z; ve[4 * h + 3] = vv[h].w;
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) adam_elem(pe[i], me[i], ve[i], gv[i], s);
+    for (int i = 0; i < 8; ++i) adam_elem(pe[i], me[i], ve[i], kScaled ? gv[i] * f : gv[i], s);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       *reinterpret_cast<f32x4_t*>(p + e0 + 4 * h) =
@@ -110,7 +114,7 @@ __global__ __launch_bounds__(256) void adamw_kernel(float* __restrict__ p,
       const float ge = kGradBf16 ? bf16_lo(static_cast<const uint16_t*>(g)[e])
                                  : static_cast<const float*>(g)[e];
       float pe = p[e], me = m[e], ve = v[e];
-      adam_elem(pe, me, ve, ge, s);
+      adam_elem(pe, me, ve, kScaled ? ge * f : ge, s);
       p[e] = pe;
       m[e] = me;
       v[e] = ve;
@@ -119,18 +123,32 @@ __global__ __launch_bounds__(256) void adamw_kernel(float* __restrict__ p,
   }
 }
 
-}  // namespace
-
-hipError_t launch_adamw(float* p, const void* g, bool g_bf16, float* m, float* v, uint16_t* pb,
-                        int64_t n, const AdamScalars& s, hipStream_t st) {
+template <bool kScaled>
+hipError_t launch(float* p, const void* g, bool g_bf16, float* m, float* v, uint16_t* pb, int64_t n,
+                  const AdamScalars& s, const float* factor, hipStream_t st) {
   if (n <= 0) return hipSuccess;
   const int64_t threads = (n + 7) / 8;
   const dim3 grid((unsigned)((threads + 255) / 256));
   if (g_bf16)
-    hipLaunchKernelGGL(adamw_kernel<true>, grid, dim3(256), 0, st, p, g, m, v, pb, n, s);
+    hipLaunchKernelGGL((adamw_kernel<true, kScaled>), grid, dim3(256), 0, st, p, g, m, v, pb, n, s,
+                       factor);
   else
-    hipLaunchKernelGGL(adamw_kernel<false>, grid, dim3(256), 0, st, p, g, m, v, pb, n, s);
+    hipLaunchKernelGGL((adamw_kernel<false, kScaled>), grid, dim3(256), 0, st, p, g, m, v, pb, n, s,
+                       factor);
   return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_adamw(float* p, const void* g, bool g_bf16, float* m, float* v, uint16_t* pb,
+                        int64_t n, const AdamScalars& s, hipStream_t st) {
+  return launch<false>(p, g, g_bf16, m, v, pb, n, s, nullptr, st);
+}
+
+hipError_t launch_adamw_scaled(float* p, const void* g, bool g_bf16, float* m, float* v,
+                               uint16_t* pb, int64_t n, const AdamScalars& s, const float* factor,
+                               hipStream_t st) {
+  return launch<true>(p, g, g_bf16, m, v, pb, n, s, factor, st);
 }
 
 }  // namespace qlora

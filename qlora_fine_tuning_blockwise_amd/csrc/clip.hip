@@ -1,0 +1,187 @@
+// The global norm of many gradients and its clipping on gfx950:
+//   norm   = sqrt(sum over all tensors of g^2)
+//   factor = max_norm / norm where norm > max_norm, else 1
+//   out    = g * factor
+//
+// The squares are formed and summed in 64 bits: the square of an fp32 value is
+// exact there, nothing overflows (gradients of 2^100 have a norm), and the
+// order of the additions is beyond what the fp32 result shows. It costs no
+// time, memory bounds the pass: a CU sees 4 bf16 elements a cycle at 5 TB/s and
+// has 64 fused operations of 64 bits a cycle.
+//
+// The tensors travel in the launch's own arguments (kSpans a launch), so a
+// launch needs no table on the device and a captured graph keeps its own copy.
+// A launch's work is cut into chunks of one size, a workgroup each; the
+// workgroup finds its tensor by a ballot over the chunks' ends.
+#include "rows.h"
+#include "spans_table.h"
+
+namespace qlora {
+namespace {
+
+constexpr int kThreads = 256;
+
+// The tensor that chunk `c` of a launch belongs to: the number of tensors that
+// end at or before it.
+__device__ __forceinline__ int span_of_chunk(const SpanTable& t, uint32_t c) {
+  const int lane = threadIdx.x & 63;
+  int s = 0;
+#pragma unroll
+  for (int k = 0; k < kSpans; k += 64)
+    s += __popcll(__ballot(k + lane < t.count && t.end[k + lane] <= c));
+  return __builtin_amdgcn_readfirstlane(s);
+}
+
+// The elements [first, last) of the chunk in tensor s.
+__device__ __forceinline__ void chunk_range(const SpanTable& t, uint32_t c, int s, int64_t& first,
+                                            int64_t& last) {
+  const uint32_t at = c - (s ? t.end[s - 1] : 0u);
+  first = (int64_t)at * t.chunk;
+  last = first + t.chunk < t.n[s] ? first + t.chunk : t.n[s];
+}
+
+__device__ __forceinline__ double wave_sum(double v) {
+#pragma unroll
+  for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
+  return v;
+}
+
+// Sum over a workgroup; thread 0 has it.
+template <int kWaves>
+__device__ __forceinline__ double block_sum(double v, double* red) {
+  v = wave_sum(v);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double s = red[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) s += red[w];
+  return s;
+}
+
+constexpr int kDepth = 4;  // vectors of a thread whose loads are in flight together
+
+template <bool kBf16>
+__device__ __forceinline__ double squares(const elem_t<kBf16>* p, int64_t first, int64_t last) {
+  constexpr int E = kBf16 ? 8 : 4;
+  double s[2] = {0.0, 0.0};
+  int64_t at = first + (int64_t)threadIdx.x * E;
+  for (; at + (int64_t)(kDepth - 1) * kThreads * E + E <= last; at += (int64_t)kDepth * kThreads * E) {
+    Vec<kBf16, E> r[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) r[d] = load_vec<kBf16, E>(p + at + (int64_t)d * kThreads * E);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      float v[E];
+      to_float<kBf16, E>(r[d], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) s[e & 1] = fma((double)v[e], (double)v[e], s[e & 1]);
+    }
+  }
+  for (; at < last; at += (int64_t)kThreads * E) {
+    const int n = count_below<E>(at, last);
+    const Vec<kBf16, E> r = n == E ? load_vec<kBf16, E>(p + at) : load_part<kBf16, E>(p + at, n);
+    float v[E];
+    to_float<kBf16, E>(r, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) s[e & 1] = fma((double)v[e], (double)v[e], s[e & 1]);
+  }
+  return s[0] + s[1];
+}
+
+__global__ __launch_bounds__(kThreads) void grad_norm_kernel(SpanTable t, double* part) {
+  __shared__ double red[kThreads / 64];
+  const int s = span_of_chunk(t, blockIdx.x);
+  int64_t first, last;
+  chunk_range(t, blockIdx.x, s, first, last);
+  const double v = t.bf16(s) ? squares<true>(static_cast<const uint16_t*>(t.in[s]), first, last)
+                             : squares<false>(static_cast<const float*>(t.in[s]), first, last);
+  const double all = block_sum<kThreads / 64>(v, red);
+  if (threadIdx.x == 0) part[blockIdx.x] = all;
+}
+
+constexpr int kJoin = 1024;
+
+// result = (norm, factor) from the chunks' sums, thread by thread in order.
+__global__ __launch_bounds__(kJoin) void grad_norm_join_kernel(const double* part, int64_t parts,
+                                                               float max_norm, float* result) {
+  __shared__ double red[kJoin / 64];
+  double s = 0.0;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < parts; i += kJoin) s += part[i];
+  const double all = block_sum<kJoin / 64>(s, red);
+  if (threadIdx.x == 0) {
+    const double norm = __builtin_sqrt(all);
+    result[0] = (float)norm;
+    // a NaN stays one; an infinite norm has the factor 0
+    result[1] = norm > (double)max_norm ? (float)((double)max_norm / norm)
+                                        : norm == norm ? 1.0f : (float)norm;
+  }
+}
+
+template <bool kBf16>
+__device__ __forceinline__ void scale(const elem_t<kBf16>* p, elem_t<kBf16>* out, int64_t first,
+                                      int64_t last, float f) {
+  constexpr int E = kBf16 ? 8 : 4;
+  int64_t at = first + (int64_t)threadIdx.x * E;
+  for (; at + (int64_t)(kDepth - 1) * kThreads * E + E <= last; at += (int64_t)kDepth * kThreads * E) {
+    Vec<kBf16, E> r[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) r[d] = load_vec<kBf16, E>(p + at + (int64_t)d * kThreads * E);
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      float v[E];
+      to_float<kBf16, E>(r[d], v);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] *= f;
+      store_vec<kBf16, E>(out + at + (int64_t)d * kThreads * E, v);
+    }
+  }
+  for (; at < last; at += (int64_t)kThreads * E) {
+    const int n = count_below<E>(at, last);
+    const Vec<kBf16, E> r = n == E ? load_vec<kBf16, E>(p + at) : load_part<kBf16, E>(p + at, n);
+    float v[E];
+    to_float<kBf16, E>(r, v);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] *= f;
+    if (n == E)
+      store_vec<kBf16, E>(out + at, v);
+    else
+      store_part<kBf16, E>(out + at, v, n);
+  }
+}
+
+// In place a factor of 1 changes nothing, and nothing is read or written.
+__global__ __launch_bounds__(kThreads) void grad_scale_kernel(SpanTable t, const float* factor) {
+  const float f = *factor;
+  const int s = span_of_chunk(t, blockIdx.x);
+  if (f == 1.0f && t.in[s] == t.out[s]) return;
+  int64_t first, last;
+  chunk_range(t, blockIdx.x, s, first, last);
+  if (t.bf16(s))
+    scale<true>(static_cast<const uint16_t*>(t.in[s]), static_cast<uint16_t*>(t.out[s]), first,
+                last, f);
+  else
+    scale<false>(static_cast<const float*>(t.in[s]), static_cast<float*>(t.out[s]), first, last, f);
+}
+
+}  // namespace
+
+hipError_t launch_grad_norm(const SpanTable& t, uint32_t chunks, double* part, hipStream_t st) {
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(chunks), dim3(kThreads), 0, st, t, part);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_norm_join(const double* part, int64_t parts, float max_norm, float* result,
+                                 hipStream_t st) {
+  hipLaunchKernelGGL(grad_norm_join_kernel, dim3(1), dim3(kJoin), 0, st, part, parts, max_norm,
+                     result);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_scale(const SpanTable& t, uint32_t chunks, const float* factor,
+                             hipStream_t st) {
+  hipLaunchKernelGGL(grad_scale_kernel, dim3(chunks), dim3(kThreads), 0, st, t, factor);
+  return hipGetLastError();
+}
+
+}  // namespace qlora

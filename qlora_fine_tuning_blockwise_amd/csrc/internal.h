@@ -178,6 +178,10 @@ struct AdamScalars {
 // copy of p, may be NULL). Pointers may be device or mapped host memory.
 hipError_t launch_adamw(float* p, const void* g, bool g_bf16, float* m, float* v, uint16_t* pb,
                         int64_t n, const AdamScalars& s, hipStream_t st);
+// The same on gradients times *factor (device memory).
+hipError_t launch_adamw_scaled(float* p, const void* g, bool g_bf16, float* m, float* v,
+                               uint16_t* pb, int64_t n, const AdamScalars& s, const float* factor,
+                               hipStream_t st);
 
 // Adapter gradients: part[split][c][j] = sum_{m in split} X[m][c] * P[m][j]
 // (X [M,C] bf16; P given as the transposed two-term bf16 split PT [2r, Mp]
@@ -237,6 +241,22 @@ hipError_t launch_norm_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void
                            bool w_bf16, float eps, const float* stats, void* dX, int64_t lddx,
                            bool dx_bf16, void* dgamma, void* dbeta, bool grad_bf16, float* part,
                            hipStream_t st);
+
+// The norm behind a residual addition. h = x + r in r's type (r NULL: h is x and
+// is not written, r_bf16 = x_bf16); y in y_kind (0 fp32, 1 bf16, 2 E4M3 with one
+// scale a row in `scales`). gamma, beta, stats may be NULL.
+hipError_t launch_add_norm_fwd(const void* x, int64_t ldx, bool x_bf16, const void* r, int64_t ldr,
+                               bool r_bf16, int64_t M, int64_t N, bool center, const void* gamma,
+                               const void* beta, bool w_bf16, float eps, void* h, int64_t ldh,
+                               void* y, int64_t ldy, int y_kind, float* scales, float* stats,
+                               hipStream_t st);
+// launch_norm_bwd with dH, in dX's type, added to dX (dX is given).
+hipError_t launch_add_norm_bwd(const void* dY, int64_t ldy, bool dy_bf16, const void* dH,
+                               int64_t lddh, const void* h, int64_t ldh, bool h_bf16, int64_t M,
+                               int64_t N, bool center, const void* gamma, bool w_bf16, float eps,
+                               const float* stats, void* dX, int64_t lddx, bool dx_bf16,
+                               void* dgamma, void* dbeta, bool grad_bf16, float* part,
+                               hipStream_t st);
 
 // part: M * distill_parts(V) * 2 floats (none where that is 0). stats of
 // the forward may be NULL.

@@ -6,38 +6,13 @@
 
 #include "host.h"
 #include "internal.h"
-#include "spans.h"
+#include "row_args.h"
 
 namespace qlora {
 namespace {
 
 constexpr int64_t kMaxIds = ((int64_t)1 << 31) - 2;  // ids are held in 32 bits, one value is taken
 constexpr int64_t kMaxEmbedWidth = (int64_t)1 << 24;
-
-bool float_type(int d) { return d == QLORA_DTYPE_F32 || d == QLORA_DTYPE_BF16; }
-bool index_type(int d) { return d == QLORA_DTYPE_I32 || d == QLORA_DTYPE_I64; }
-int64_t elem_bytes(int dtype) { return dtype == QLORA_DTYPE_BF16 ? 2 : dtype == QLORA_DTYPE_I64 ? 8 : 4; }
-
-// The alignment of an element of a QLORA_DTYPE_* type.
-bool aligned_elem(const void* p, int dtype) {
-  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem_bytes(dtype) - 1)) == 0;
-}
-
-// What an argument occupies, for the check that no output lies on an input:
-// rows of a matrix, or a contiguous array.
-Span matrix(const void* p, int64_t rows, int64_t width, int64_t ld, int dtype) {
-  return span_of(p, rows, width, ld, elem_bytes(dtype));
-}
-Span array(const void* p, int64_t count, int dtype) { return span_of(p, count * elem_bytes(dtype)); }
-Span bytes(const void* p, size_t n) { return span_of(p, (int64_t)n); }
-// An output that may be the input `in` itself, at the same address and stride
-// in the same type: no span of its own then.
-Span unless_same(const Span& in, const Span& out) { return in.same(out) ? Span{} : in; }
-
-// Rows of `width` elements every `ld`: the last row's end stays countable.
-bool stride_ok(int64_t M, int64_t width, int64_t ld) {
-  return ld >= width && ld <= kMaxElems / (M > 0 ? M : 1);
-}
 
 bool embed_shape_ok(int64_t V, int64_t D) {
   return V >= 1 && V <= kMaxIds && D >= 1 && D <= kMaxEmbedWidth && V <= kMaxElems / D;
@@ -56,10 +31,6 @@ EmbedLayout embed_layout(int64_t M, int64_t D) {
   L.part = c.take(tiles * 2 * (size_t)((D + 7) / 8 * 8) * 4);
   L.total = c.off;
   return L;
-}
-
-bool norm_shape_ok(int64_t M, int64_t N) {
-  return M >= 0 && M <= QLORA_MAX_ROWS && N >= 1 && N <= QLORA_MAX_NORM_WIDTH;
 }
 
 size_t norm_bwd_bytes(int64_t M, int64_t N) {

@@ -1,0 +1,351 @@
+"""GPU tests of the norm behind a residual addition and of the gradients'
+clipping against their 64-bit forms: |got - want| <= err + half a step of the
+output's type, where err is the bound that oracle/close.py derives for the
+values at hand."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import qlora_fine_tuning_blockwise_amd as q
+from oracle import close
+from test_row_ops_gpu import BF16, DEV, F32, NORM_SHAPES, check, host, randn, say, strided
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+U = 2.0 ** -24
+
+
+def dev(t):
+    return None if t is None else t.to(DEV)
+
+
+def add_norm_inputs(M, N, seed, x_dtype, h_dtype, w_dtype):
+    g = np.random.default_rng(seed)
+    r = randn(g, (M, N), scale=1.5, shift=0.4) * torch.from_numpy(
+        np.exp(0.5 * g.standard_normal((M, 1))).astype(np.float32))
+    return (randn(g, (M, N), x_dtype, 0.7), r.to(h_dtype), randn(g, N, w_dtype, 0.3, 1.0),
+            randn(g, N, w_dtype, 0.2))
+
+
+def check_codes(y, scales, want, err, w_scales, e_scales, name):
+    check(scales, w_scales, e_scales, name + " scales")
+    got = y.float().cpu().double().numpy() * scales.cpu().double().numpy()[:, None]
+    off = np.abs(got - want) - close.codes_err(want, err, w_scales, e_scales)
+    assert (off <= 0).all(), f"{name}: {int((off > 0).sum())} codes beyond the bound, by {off.max():.3e}"
+
+
+# ------------------------------------------------- norm behind an addition
+@pytest.mark.parametrize("i,shape", list(enumerate(NORM_SHAPES)))
+@pytest.mark.parametrize("center", [True, False])
+@pytest.mark.parametrize("out", [BF16, F32, E4M3], ids=["bf16", "f32", "e4m3"])
+def test_add_norm_forward(i, shape, center, out):
+    M, N = shape
+    x_dtype, h_dtype, w_dtype = [(BF16, BF16, BF16), (F32, BF16, F32), (BF16, F32, F32),
+                                 (F32, F32, BF16)][(i + center + (out == E4M3)) % 4]
+    say("add norm fwd", M, N, center, x_dtype, h_dtype, out)
+    x, r, gamma, beta = add_norm_inputs(M, N, 10 + i, x_dtype, h_dtype, w_dtype)
+    gamma = None if i % 5 == 4 else gamma
+    beta = None if i % 3 == 2 else beta
+    xv, _ = strided(x, i % 4, lead=i % 3)
+    rv, rbuf = strided(r, (i + 2) % 3, lead=i % 2)
+    place = i % 3  # h in memory of its own, over the residual, over x
+    if place == 2 and x_dtype == h_dtype:
+        hv, hbuf = xv, None
+    elif place == 1:
+        hv, hbuf = rv, rbuf
+    else:
+        hv, hbuf = strided(torch.zeros(M, N, dtype=h_dtype), (i + 1) % 4, lead=i % 3)
+    codes = out == E4M3
+    if codes:
+        raw = torch.full((M * (N + i % 3) + 1,), 0x55, dtype=torch.uint8, device=DEV)
+        yv = raw[1:].view(M, N + i % 3)[:, :N].view(E4M3) if N + i % 3 else None
+    else:
+        yv, ybuf = strided(torch.zeros(M, N, dtype=out), (i + 1) % 3, lead=i % 2)
+    stats = torch.empty(2, M, device=DEV)
+    scales = torch.empty(M, device=DEV) if codes else None
+    y, h = q.qlora_add_norm_fwd(xv, rv, dev(gamma), dev(beta), eps=1e-5,
+                                norm=q.NORM_LAYER if center else q.NORM_RMS, h=hv, y=yv,
+                                scales_out=scales, stats_out=stats)
+    torch.cuda.synchronize()
+    assert h is hv and y is yv
+    kept = (x.float() + r.float()).to(h_dtype)
+    assert torch.equal(hv.cpu(), kept)
+    if hbuf is not None:
+        assert int(torch.isnan(hbuf).sum()) == hbuf.numel() - M * N
+    want, err, wstats, e_stats, w_sc, e_sc = close.add_norm_fwd(
+        host(kept), None if gamma is None else host(gamma), None if beta is None else host(beta),
+        1e-5, center)
+    check(stats, wstats, e_stats, "stats")
+    if codes:
+        check_codes(yv, scales, want, err, w_sc, e_sc, "y")
+        rest = raw[1:].view(M, N + i % 3)[:, N:]
+        assert int((rest != 0x55).sum()) == 0 and int(raw[0]) == 0x55  # nothing else was written
+    else:
+        check(yv, want, err, "y")
+        assert int(torch.isnan(ybuf).sum()) == ybuf.numel() - M * N
+
+
+@pytest.mark.parametrize("out", [BF16, E4M3], ids=["bf16", "e4m3"])
+def test_add_norm_without_a_residual(out):
+    g = np.random.default_rng(5)
+    x, gamma = randn(g, (7, 300), BF16), randn(g, 300, BF16, 0.2, 1.0)
+    scales = torch.empty(7, device=DEV) if out == E4M3 else None
+    y, h = q.qlora_add_norm_fwd(dev(x), None, dev(gamma), y_dtype=out, scales_out=scales)
+    want, err, _, _, w_sc, e_sc = close.add_norm_fwd(host(x), host(gamma), None, 1e-5, True)
+    assert torch.equal(h.cpu(), x)
+    if out == E4M3:
+        check_codes(y, scales, want, err, w_sc, e_sc, "y")
+    else:
+        check(y, want, err, "y")
+        assert torch.equal(y, q.qlora_norm_fwd(dev(x), dev(gamma)))
+
+
+def test_add_norm_codes_of_awkward_rows():
+    """Rows of zeros, of one large value, with a NaN, with infinities, and rows
+    whose largest magnitude leaves 448 / max outside of fp32."""
+    N = 130
+    x = torch.zeros(6, N)
+    x[1, 5] = 1e4
+    x[2, 7] = math.nan
+    x[3, 9] = math.inf
+    x[4] = torch.linspace(-1, 1, N)
+    x[5] = torch.linspace(-1, 1, N)
+    gamma = torch.ones(N)
+    scales = torch.empty(6, device=DEV)
+    y, _ = q.qlora_add_norm_fwd(dev(x), None, dev(gamma), norm=q.NORM_RMS, y_dtype=E4M3, scales_out=scales)
+    y, s = y.float().cpu(), scales.cpu()
+    assert float(s[0]) == 0 and not y[0].any()
+    assert float(y[1, 5]) == 448 and int((y[1] != 0).sum()) == 1
+    assert math.isnan(s[2]) and bool(torch.isnan(y[2]).all())
+    assert math.isnan(s[3]) and bool(torch.isnan(y[3]).all())  # inf / inf in the norm itself
+    for size in (2.0 ** -90, 2.0 ** -110, 2.0 ** -120):
+        y, _ = q.qlora_add_norm_fwd(dev(x[4:]), None, dev(gamma * size), norm=q.NORM_RMS, y_dtype=E4M3,
+                                    scales_out=scales[:2])
+        want, err, _, _, w_sc, e_sc = close.add_norm_fwd(host(x[4:]), host(gamma * size), None, 1e-5, False)
+        # below 2^-126 a scale keeps 2^-149
+        check_codes(y, scales[:2], want, err + 448 * 2.0 ** -149, w_sc, e_sc + 2.0 ** -149, str(size))
+    gamma[3] = math.inf  # an infinite entry: its code is NaN, finite ones are 0
+    y, _ = q.qlora_add_norm_fwd(dev(x[4:]), None, dev(gamma), norm=q.NORM_RMS, y_dtype=E4M3, scales_out=scales[:2])
+    y = y.float().cpu()
+    assert bool(torch.isnan(y[:, 3]).all()) and bool((y[:, 4:] == 0).all())
+    assert bool(torch.isinf(scales[:2]).all())
+
+
+@pytest.mark.parametrize("i,shape", list(enumerate(NORM_SHAPES)))
+@pytest.mark.parametrize("center", [True, False])
+def test_add_norm_backward(i, shape, center):
+    M, N = shape
+    types = [(BF16, BF16, BF16), (F32, BF16, F32), (BF16, F32, F32), (F32, F32, BF16), (BF16, BF16, F32)]
+    h_dtype, y_dtype, d_dtype = types[(i + center) % 5]
+    say("add norm bwd", M, N, center, h_dtype, y_dtype, d_dtype)
+    g = np.random.default_rng(90 + i)
+    h, dY = randn(g, (M, N), h_dtype, 1.5, 0.4), randn(g, (M, N), y_dtype)
+    dH, gamma = randn(g, (M, N), d_dtype, 0.5), None if i % 5 == 4 else randn(g, N, BF16, 0.3, 1.0)
+    hv, _ = strided(h, i % 3, lead=i % 2)
+    dv, _ = strided(dY, (i + 1) % 4, lead=i % 3)
+    dHv, buf = strided(dH, (i + 2) % 3, lead=i % 2)
+    stats = None
+    if i % 2:
+        stats = torch.empty(2, M, device=DEV)
+        q.qlora_norm_fwd(hv, norm=q.NORM_LAYER if center else q.NORM_RMS, stats_out=stats)
+    out = dHv if i % 2 else None  # over dH itself
+    dX, dg, db = q.qlora_add_norm_bwd(dv, hv, dHv, dev(gamma), norm=q.NORM_LAYER if center else q.NORM_RMS,
+                                      stats=stats, dX=out)
+    torch.cuda.synchronize()
+    (wX, eX), (wg, eg), (wb, eb) = close.add_norm_bwd(host(dY), host(dH), host(h),
+                                                      None if gamma is None else host(gamma), 1e-5, center)
+    assert dX.dtype == d_dtype
+    check(dX, wX, eX, "dX")
+    check(dg, wg, eg, "dgamma")
+    check(db, wb, eb, "dbeta")
+    assert int(torch.isnan(buf).sum()) == buf.numel() - M * N
+
+
+def test_add_norm_backward_without_dH_is_the_norms():
+    g = np.random.default_rng(6)
+    h, dY, gamma = dev(randn(g, (9, 515), BF16)), dev(randn(g, (9, 515), BF16)), dev(randn(g, 515, BF16))
+    for a, b in zip(q.qlora_add_norm_bwd(dY, h, None, gamma), q.qlora_norm_bwd(dY, h, gamma)):
+        assert torch.equal(a, b)
+    dX, dg, db = q.qlora_add_norm_bwd(dY, h, dY, gamma, want_dx=False, want_dbeta=False)
+    assert dX is None and db is None and torch.equal(dg, q.qlora_norm_bwd(dY, h, gamma)[1])
+
+
+def test_add_norm_gradient_by_differences():
+    """Central differences of the fp32 forward along random directions. With a
+    step of 2^-6 the difference's own error is of the third derivative (2^-12
+    of terms of the derivative's size) and 2^-24 |f| / 2^-6 from the forward's
+    roundings, both below 1e-3 of the values here."""
+    g = np.random.default_rng(8)
+    M, N = 6, 200
+    x, r, dY, dH = (dev(randn(g, (M, N))) for _ in range(4))
+    gamma = dev(randn(g, N, F32, 0.2, 1.0))
+    dX, _, _ = q.qlora_add_norm_bwd(dY, x + r, dH, gamma)
+
+    def f(x_, r_):
+        y, h = q.qlora_add_norm_fwd(x_, r_, gamma)
+        return float((y.double() * dY).sum() + (h.double() * dH).sum())
+    for which in range(2):
+        d = dev(randn(g, (M, N)))
+        step = 2.0 ** -6
+        a = (x + step * d, r) if which == 0 else (x, r + step * d)
+        b = (x - step * d, r) if which == 0 else (x, r - step * d)
+        want = (f(*a) - f(*b)) / (2 * step)
+        size = float((dX.double() * d).abs().sum())
+        assert abs(float((dX.double() * d).sum()) - want) <= 1e-3 * size
+
+
+def test_add_norm_many_rows_and_none():
+    g = np.random.default_rng(9)
+    x, r = dev(randn(g, (9001, 96), BF16)), dev(randn(g, (9001, 96), BF16))
+    y, h = q.qlora_add_norm_fwd(x, r)
+    assert torch.equal(h, (x.float() + r.float()).to(BF16)) and torch.equal(y, q.qlora_norm_fwd(h))
+    x, r = dev(randn(g, (1200, 4096), BF16)), dev(randn(g, (1200, 4096), F32))
+    y, h = q.qlora_add_norm_fwd(x, r, y_dtype=F32)
+    assert torch.equal(h, x.float() + r) and torch.equal(y, q.qlora_norm_fwd(h))
+    e = torch.empty(0, 96, dtype=BF16, device=DEV)
+    y, h = q.qlora_add_norm_fwd(e, e, y_dtype=E4M3, scales_out=torch.empty(0, device=DEV))
+    assert y.shape == h.shape == (0, 96)
+    dX, dg, db = q.qlora_add_norm_bwd(e, e, e)
+    assert dX.shape == (0, 96) and not dg.any() and not db.any()
+
+
+# ----------------------------------------------------- clipping of gradients
+SIZES = [[1], [7], [8, 9, 1], [0, 5, 0], [16384], [16385, 16383, 3], [40000, 1, 100003],
+         [3 * k + 1 for k in range(300)], [1 << 21]]
+
+
+def grads_of(sizes, kinds, seed, lead):
+    g = np.random.default_rng(seed)
+    out = []
+    for i, n in enumerate(sizes):
+        t = randn(g, n, kinds[i % len(kinds)], 10.0 ** g.uniform(-3, 1))
+        buf = torch.full((n + 24,), math.nan, dtype=t.dtype, device=DEV)
+        at = (i + lead) % 9
+        buf[at:at + n] = t.to(DEV)
+        out.append((t, buf, buf[at:at + n]))
+    return out
+
+
+@pytest.mark.parametrize("i,sizes", list(enumerate(SIZES)))
+@pytest.mark.parametrize("kinds", [[BF16], [F32], [BF16, F32, F32]], ids=["bf16", "f32", "mixed"])
+def test_grad_norm_and_scale(i, sizes, kinds):
+    say("clip", len(sizes), sum(sizes), kinds)
+    made = grads_of(sizes, kinds, 70 + i, i)
+    views = [v for _, _, v in made]
+    norm, _ = close.grad_norm([host(t) for t, _, _ in made], math.inf)
+    for max_norm in (0.25 * norm, 4 * norm, math.inf):
+        w_norm, w_factor = close.grad_norm([host(t) for t, _, _ in made], float(np.float32(max_norm)))
+        lists = views if i % 2 else q.qlora_tensor_list(views)
+        result = q.qlora_grad_norm(lists, max_norm)
+        torch.cuda.synchronize()
+        r = result.cpu().double().numpy()
+        assert abs(r[0] - w_norm) <= 1.01 * U * w_norm and abs(r[1] - w_factor) <= 1.01 * U * w_factor
+        # elsewhere, then in place
+        other = grads_of(sizes, kinds, 1, i + 4)
+        q.qlora_grad_scale(lists, result[1:], out=[v for _, _, v in other])
+        want = [(t.float() * result[1].cpu()).to(t.dtype) for t, _, _ in made]
+        for (_, buf, v), w in zip(other, want):
+            assert torch.equal(v.cpu(), w) and int(torch.isnan(buf).sum()) == buf.numel() - w.numel()
+    small = q.qlora_grad_norm(views, 0.25 * norm)
+    want = [(t.float() * small[1].cpu()).to(t.dtype) for t, _, _ in made]
+    q.qlora_grad_scale(views, small[1:])
+    for (_, buf, v), w in zip(made, want):
+        assert torch.equal(v.cpu(), w) and int(torch.isnan(buf).sum()) == buf.numel() - w.numel()
+    again = [v.clone() for v in views]
+    q.qlora_grad_scale(views, torch.ones(1, device=DEV))
+    assert all(torch.equal(a, b) for a, b in zip(again, views))
+
+
+@pytest.mark.parametrize("place", [0, 1, 255 * 8, 16383, 16384, 32768, 100002])
+def test_grad_norm_counts_every_element_once(place):
+    """One element is as large as all others together."""
+    t = torch.ones(100003, device=DEV)
+    t[place] = math.sqrt(100002)
+    r = q.qlora_grad_norm([t, t.bfloat16()[:17]]).cpu().double()
+    want = math.sqrt(100002 + float(t[place].double()) ** 2 + float((t.bfloat16()[:17].double() ** 2).sum()))
+    assert abs(float(r[0]) - want) <= 1.01 * U * want
+
+
+def test_grad_norm_of_every_size():
+    """Squares that leave fp32 on either side, and values that are not finite."""
+    for size in (2.0 ** 120, 2.0 ** -120, 2.0 ** -149):
+        t = torch.full((3000,), size, device=DEV)
+        r = q.qlora_grad_norm([t], size).cpu().double()
+        norm = math.sqrt(3000) * size
+        assert abs(float(r[0]) - norm) <= max(1.01 * U * norm, 2.0 ** -150)
+        assert abs(float(r[1]) - 1 / math.sqrt(3000)) <= 1.01 * U / math.sqrt(3000)
+    t = torch.full((3000,), 2.0 ** 127, device=DEV)  # the norm itself leaves fp32; its factor does not
+    r = q.qlora_grad_norm([t], 2.0 ** 127).cpu().double()
+    assert math.isinf(r[0]) and abs(float(r[1]) - 1 / math.sqrt(3000)) <= 1.01 * U / math.sqrt(3000)
+    t[7] = math.inf
+    assert q.qlora_grad_norm([t], 1.0).tolist() == [math.inf, 0.0]
+    t[8] = math.nan
+    assert all(math.isnan(v) for v in q.qlora_grad_norm([t], 1.0).tolist())
+    assert all(math.isnan(v) for v in q.qlora_grad_norm([t]).tolist())
+    z = torch.zeros(10, device=DEV)
+    assert q.qlora_grad_norm([z], 0.0).tolist() == [0.0, 1.0]
+    assert q.qlora_grad_norm([z[:0]], 1.0).tolist() == [0.0, 1.0]
+    assert q.qlora_grad_norm([], 1.0, result=torch.empty(2, device=DEV)).tolist() == [0.0, 1.0]
+    # sqrt(2) 2^127 is below fp32's largest value, 2^128 (1 - 2^-24)
+    assert abs(float(q.qlora_grad_norm([t[:1], t[:1]])[0]) / 2.0 ** 127.5 - 1) <= 1.01 * U
+    ones = torch.ones(8, device=DEV)
+    assert abs(float(q.qlora_grad_norm([ones, ones])[0]) - 4.0) <= 4 * U  # listed twice: counted twice
+    assert q.qlora_grad_norm([ones], 0.0).tolist()[1] == 0.0
+
+
+def test_grad_norm_past_32_bits():
+    n = (1 << 32) + 100003
+    t = torch.zeros(n, dtype=BF16, device=DEV)
+    t[-1] = 3.0
+    t[(1 << 31) + 5] = 4.0
+    r = q.qlora_grad_norm([t], 2.5)
+    assert r.tolist() == [5.0, 0.5]
+    q.qlora_grad_scale([t], r[1:])
+    assert float(t[-1]) == 1.5 and float(t[(1 << 31) + 5]) == 2.0 and float(t.max()) == 2.0
+
+
+@pytest.mark.parametrize("n", [1, 9, 4096, 100001])
+@pytest.mark.parametrize("kind", [BF16, F32])
+def test_adamw_takes_the_factor(n, kind):
+    """The bits of a step on gradients that were multiplied before it."""
+    g = np.random.default_rng(n)
+    grad, factor = dev(randn(g, n, kind)), torch.full((1,), 0.37, device=DEV)
+    p = dev(randn(g, n))
+    state = [p, dev(randn(g, n, F32, 0.1)), dev(randn(g, n, F32, 0.1)) ** 2]
+    a, b = [t.clone() for t in state], [t.clone() for t in state]
+    pa, pb = torch.empty(n, dtype=BF16, device=DEV), torch.empty(n, dtype=BF16, device=DEV)
+    q.qlora_adamw_step(a[0], grad, a[1], a[2], 3, 1e-2, weight_decay=0.01, param_bf16=pa, grad_factor=factor)
+    q.qlora_adamw_step(b[0], grad.float() * factor, b[1], b[2], 3, 1e-2, weight_decay=0.01, param_bf16=pb)
+    assert all(torch.equal(x, y) for x, y in zip(a + [pa], b + [pb]))
+    assert not torch.equal(a[0], p)
+
+
+def test_adamw_takes_the_factor_on_paged_state():
+    g = np.random.default_rng(2)
+    n = 5000
+    host_state = [randn(g, n).pin_memory(), randn(g, n).pin_memory(), (randn(g, n) ** 2).pin_memory()]
+    dev_state = [t.to(DEV) for t in host_state]
+    grad, factor = dev(randn(g, n, BF16)), torch.full((1,), 0.2, device=DEV)
+    for s in (host_state, dev_state):
+        q.qlora_adamw_step(s[0], grad, s[1], s[2], 1, 1e-2, grad_factor=factor)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b.cpu()) for a, b in zip(host_state, dev_state))
+
+
+def test_refused_on_the_device_as_on_the_host():
+    x = torch.zeros(4, 64, device=DEV)
+    with pytest.raises(RuntimeError):
+        q.qlora_add_norm_fwd(x, x + 1, y=x)
+    with pytest.raises(RuntimeError):
+        q.qlora_grad_scale([x, x], torch.ones(1, device=DEV))
+    with pytest.raises(RuntimeError):
+        q.qlora_grad_scale([x], x.view(-1)[:1])
+    with pytest.raises(RuntimeError):
+        q.qlora_grad_norm([x], result=x.view(-1)[:2])
+    with pytest.raises(RuntimeError):
+        q.qlora_grad_norm([x], workspace=torch.empty(4, dtype=torch.uint8, device=DEV))
+    with pytest.raises(ValueError):
+        q.qlora_add_norm_fwd(x, x + 1, y_dtype=E4M3)
