@@ -128,6 +128,7 @@ extern "C" {
 #define QLORA_MAX_NORM_WIDTH 16384     /* elements of a normed row */
 #define QLORA_MAX_TOP 1024             /* teacher entries of a row */
 #define QLORA_MAX_TENSORS (1 << 20)    /* tensors of a gradient's norm */
+#define QLORA_MAX_HEAD_WIDTH 65536     /* in-features of a vocabulary head */
 
 /* Format version of the storage layout above. */
 #define QLORA_FORMAT_VERSION 1u
@@ -577,6 +578,60 @@ int qlora_add_norm_bwd(const void* dY, int64_t ldy, int dy_dtype, const void* dH
                        const void* gamma, int w_dtype, float eps, const float* stats, void* dX,
                        int64_t lddx, int dx_dtype, void* dgamma, void* dbeta, int grad_dtype,
                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device workspace, in bytes, of qlora_head_loss_fwd. w_copy: not 0 where W is
+ * not read in place, that is where K % 32 != 0, ldw % 8 != 0, ldw > 2^20 or W is
+ * not 16-byte aligned (the call then copies it, a part at a time). Host only; 0
+ * on invalid sizes. */
+size_t qlora_head_loss_fwd_workspace_bytes(int64_t M, int64_t V, int64_t K, int w_copy);
+
+/* Loss of the vocabulary head, softmax cross entropy, without keeping the logits
+ * ([P3] "How it works" keeps the output layer in 16-bit):
+ *   z = scale * x W^T,  loss[m] = log sum_v exp(z_mv - max z_m) + (max z_m - z_m,label)
+ *   x [M,K], W [V,K] bf16 with row strides; labels [M] QLORA_DTYPE_I32 or
+ *   QLORA_DTYPE_I64;
+ *   loss   fp32 [M];
+ *   stats  fp32 [2,M] or NULL; when given it receives the rows' largest logits,
+ *          then log sum_v exp(z_v - largest) (for the backward).
+ * A row whose label lies outside of [0, V) has loss 0 and stats 0; its x takes
+ * part in nothing, and a batch costs what its other rows do. Products are exact
+ * and sums fp32. NaN and infinities in x stay in their row; one in W reaches
+ * every row. QLORA_ERR_SHAPE unless 1 <= V < 2^31 - 1, 1 <= K <=
+ * QLORA_MAX_HEAD_WIDTH, V*K <= 2^40, M <= QLORA_MAX_SORTED and the strides hold
+ * their rows; QLORA_ERR_INVALID_ARG for M < 0, a NULL array or a scale that is
+ * not finite; QLORA_ERR_WORKSPACE for a workspace smaller than
+ * qlora_head_loss_fwd_workspace_bytes. */
+int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64_t ldw, int64_t M,
+                        int64_t V, int64_t K, const void* labels, int ids_dtype, float scale,
+                        float* loss, float* stats, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* Device workspace, in bytes, of qlora_head_loss_bwd for these outputs (dx_dtype,
+ * grad_dtype: their types, negative for one that is not wanted): the
+ * probabilities of one piece of the vocabulary, 128 MB of them at most up to
+ * 32768 rows, and its products' operands. */
+size_t qlora_head_loss_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K, int w_copy,
+                                           int dx_dtype, int grad_dtype);
+
+/* Gradients of the losses, with p_m = softmax(z_m) formed again from x, W and stats:
+ *   dX[m] = dloss[m] * scale * (sum_v p_mv W_v - W_label)
+ *   dW[v] = sum over m of dloss[m] * scale * (p_mv - [v = label]) x[m]
+ *   dloss  fp32 [M], the gradient of each row's loss; a row with dloss 0 or
+ *          without a label gets zeros, whatever its x holds, and adds nothing;
+ *   stats  fp32 [2,M] from qlora_head_loss_fwd with the same x, W and scale;
+ *   dX     [M,K] (dx_dtype), row stride lddx; dW [V,K] contiguous, 16-byte
+ *          aligned (grad_dtype); either may be NULL to skip that output.
+ *          accumulate != 0: dW's sums are added to what it holds (one rounding).
+ * The products take probabilities (for dX) and logit gradients (for dW) in bf16,
+ * one rounding each, for bf16 outputs, and as the sum of two bf16 numbers for fp32
+ * ones, which cost those products twice. A probability below 2^-126 counts as 0.
+ * M == 0 writes zero dW (unless it
+ * accumulates). The other arguments and errors as in the forward. */
+int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64_t ldw, int64_t M,
+                        int64_t V, int64_t K, const void* labels, int ids_dtype, float scale,
+                        const float* stats, const float* dloss, void* dX, int64_t lddx,
+                        int dx_dtype, void* dW, int grad_dtype, int accumulate, void* workspace,
+                        size_t workspace_bytes, void* stream);
 
 /* One of many tensors: n contiguous elements, aligned to their type. */
 typedef struct qlora_tensor {

@@ -119,7 +119,9 @@ def head_loss_bwd(x, W, labels, dloss, scale=1.0, terms=1):
     m, L, p, e_m, e_L, rel = _softmax(z, e)
     f = np.where(live, dloss.astype(np.float64) * scale, 0.0)[:, None]
     lost = BF16 ** terms
-    e_p = p * (rel + e_L + 4 * U)
+    # The hardware's exponential, its product with exp(-L), and a bf16 part of
+    # it are zero below 2^-126: at most 2^-126 is lost of each.
+    e_p = p * (rel + e_L + 4 * U) + 3 * 2.0 ** -126
     hot = np.zeros_like(p)
     hot[np.arange(M), ids] = 1.0
     # sums of fp32 products in the matrix units, as the logits', and over pieces

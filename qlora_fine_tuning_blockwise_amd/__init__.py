@@ -8,8 +8,9 @@ memory and the current stream, and every step of the computation runs in
 libqlora_amd.so. Tensors must be contiguous and on a ROCm device.
 
 The row operators (qlora_embed_*, qlora_norm_*, qlora_distill_*,
-qlora_add_norm_*) take matrices whose rows are contiguous, at any row stride (views of wider or
-longer tensors), and run on the device of their tensors whichever is current.
+qlora_add_norm_*, qlora_head_loss_*) take matrices whose rows are contiguous, at
+any row stride (views of wider or longer tensors), and run on the device of
+their tensors whichever is current.
 Without `stream` they use that device's current stream; with it, what they
 allocate belongs to that stream. A given output may not share memory with an
 input or another output (the library refuses the call); only qlora_norm_fwd's
@@ -35,6 +36,8 @@ __all__ = [
     "qlora_norm_fwd", "qlora_norm_bwd", "qlora_norm_bwd_workspace_bytes",
     "qlora_distill_fwd", "qlora_distill_bwd", "qlora_distill_fwd_workspace_bytes",
     "qlora_add_norm_fwd", "qlora_add_norm_bwd",
+    "qlora_head_loss_fwd", "qlora_head_loss_bwd", "qlora_head_loss_fwd_workspace_bytes",
+    "qlora_head_loss_bwd_workspace_bytes",
     "qlora_tensor_list", "qlora_grad_norm", "qlora_grad_norm_workspace_bytes", "qlora_grad_scale",
     "TensorList", "NORM_LAYER", "NORM_RMS",
     "NF4Weight", "DQ_INT8", "DQ_UINT8", "DQ_E4M3", "LAYOUT_ROWS", "LAYOUT_KSLAB32",
@@ -798,6 +801,107 @@ def qlora_add_norm_bwd(dY: torch.Tensor, h: torch.Tensor, dH: torch.Tensor | Non
     if st:
         _lib.check(st, "qlora_add_norm_bwd")
     return dX if want_dx else None, dgamma, dbeta
+
+
+def qlora_head_loss_fwd_workspace_bytes(M: int, V: int, K: int, w_copy: bool = False) -> int:
+    return int(_lib.load().qlora_head_loss_fwd_workspace_bytes(M, V, K, int(w_copy)))
+
+
+def qlora_head_loss_bwd_workspace_bytes(M: int, V: int, K: int, w_copy: bool = False,
+                                        dx_dtype=torch.bfloat16, grad_dtype=None) -> int:
+    """For dX of dx_dtype and dW of grad_dtype (None: not wanted)."""
+    code = lambda dt: -1 if dt is None else _dtype_code(dt)  # noqa: E731
+    return int(_lib.load().qlora_head_loss_bwd_workspace_bytes(M, V, K, int(w_copy), code(dx_dtype),
+                                                               code(grad_dtype)))
+
+
+def _head(x, W, labels):
+    """The shared arguments of both directions, and whether W is copied (not read
+    in place)."""
+    M, K = _two_dims(x, "x")
+    V = _two_dims(W, "W")[0]
+    dev = x.device
+    ldx, ldw = _matrix(x, "x", (M, K), dev), _matrix(W, "W", (V, K), dev)
+    for t, name in ((x, "x"), (W, "W")):
+        if t.dtype != torch.bfloat16:
+            raise ValueError(f"{name}: dtype {t.dtype}, expected bf16")
+    ids_dtype = _indexes(labels, "labels", (M,), dev)
+    at = W.data_ptr()
+    copy = K % 32 != 0 or ldw % 8 != 0 or ldw > 1 << 20 or at % 16 != 0
+    return (_at(x), ldx, at, ldw, M, V, K, _at(labels), ids_dtype), copy
+
+
+def qlora_head_loss_fwd(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor, scale: float = 1.0,
+                        loss: torch.Tensor | None = None, stats_out: torch.Tensor | None = None,
+                        workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Softmax cross entropy of each row (fp32 [M]) with the logits scale * x W^T,
+    which are not kept: x [M,K], W [V,K] bf16, labels [M] int32 or int64 (outside
+    of [0, V): no loss, and no work). stats_out: fp32 [2,M] for the backward."""
+    head, copy = _head(x, W, labels)
+    M, V, K, dev = head[4], head[5], head[6], x.device
+    if stats_out is not None:
+        _vector(stats_out, "stats_out", (2, M), _F32, dev)
+    _need(loss, "loss", (M,), torch.float32, dev)
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_head_loss_fwd(x, W, labels, scale, loss, stats_out, workspace)
+    if loss is None:
+        loss = torch.empty(M, dtype=torch.float32, device=dev)
+    workspace = _bytes(workspace, qlora_head_loss_fwd_workspace_bytes(M, V, K, copy), dev)
+    st = _lib.load().qlora_head_loss_fwd(*head, scale, _at(loss), _at(stats_out), _at(workspace),
+                                         workspace.numel(), _here(dev))
+    if st:
+        _lib.check(st, "qlora_head_loss_fwd")
+    return loss
+
+
+def qlora_head_loss_bwd(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
+                        dloss: torch.Tensor, stats: torch.Tensor, scale: float = 1.0,
+                        want_dx: bool = True, want_dw: bool = True, dx_dtype=torch.bfloat16,
+                        grad_dtype=torch.bfloat16, dX: torch.Tensor | None = None,
+                        dW: torch.Tensor | None = None, accumulate: bool = False,
+                        workspace: torch.Tensor | None = None, stream=None):
+    """Returns (dX or None, dW or None) of the rows' losses for their gradients
+    dloss (fp32 [M]) and the forward's stats_out: dX [M,K] in dx_dtype, dW [V,K]
+    in grad_dtype (or as they are given); with accumulate the sums are added to
+    the given dW."""
+    head, copy = _head(x, W, labels)
+    M, V, K, dev = head[4], head[5], head[6], x.device
+    _vector(stats, "stats", (2, M), _F32, dev)
+    _vector(dloss, "dloss", (M,), _F32, dev)
+    lddx = K
+    if dX is not None:
+        lddx, dx_dtype = _matrix(dX, "dX", (M, K), dev), dX.dtype
+    if accumulate and want_dw and dW is None:
+        raise ValueError("qlora_head_loss_bwd: accumulate needs dW")
+    if dW is not None:
+        _vector(dW, "dW", (V, K), tuple(_FLOATS), dev)
+        grad_dtype = dW.dtype
+    if dx_dtype not in _FLOATS or grad_dtype not in _FLOATS:
+        raise ValueError("qlora_head_loss_bwd: gradients are fp32 or bf16")
+    if _elsewhere(dev, stream):
+        with _place(dev, stream):
+            return qlora_head_loss_bwd(x, W, labels, dloss, stats, scale, want_dx, want_dw, dx_dtype,
+                                       grad_dtype, dX, dW, accumulate, workspace)
+    if not want_dx:
+        dX = None
+    elif dX is None:
+        dX = torch.empty((M, K), dtype=dx_dtype, device=dev)
+    if not want_dw:
+        dW = None
+    elif dW is None:
+        dW = torch.empty((V, K), dtype=grad_dtype, device=dev)
+    if want_dx or want_dw:
+        need = qlora_head_loss_bwd_workspace_bytes(M, V, K, copy, dx_dtype if want_dx else None,
+                                                   grad_dtype if want_dw else None)
+        workspace = _bytes(workspace, need, dev)
+    st = _lib.load().qlora_head_loss_bwd(
+        *head, scale, _at(stats), _at(dloss), _at(dX), lddx, _FLOATS[dx_dtype], _at(dW),
+        _FLOATS[grad_dtype], int(accumulate), _at(workspace),
+        0 if workspace is None else workspace.numel(), _here(dev))
+    if st:
+        _lib.check(st, "qlora_head_loss_bwd")
+    return dX, dW
 
 
 class TensorList:

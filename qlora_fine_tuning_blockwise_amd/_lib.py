@@ -87,6 +87,11 @@ SIGNATURES = {
                                  I64, INT, P, P, P]),
     "qlora_add_norm_bwd": (INT, [P, I64, INT, P, I64, P, I64, INT, I64, I64, INT, P, INT, FLT, P, P,
                                  I64, INT, P, P, INT, P, SZ, P]),
+    "qlora_head_loss_fwd_workspace_bytes": (SZ, [I64, I64, I64, INT]),
+    "qlora_head_loss_fwd": (INT, [P, I64, P, I64, I64, I64, I64, P, INT, FLT, P, P, P, SZ, P]),
+    "qlora_head_loss_bwd_workspace_bytes": (SZ, [I64, I64, I64, INT, INT, INT]),
+    "qlora_head_loss_bwd": (INT, [P, I64, P, I64, I64, I64, I64, P, INT, FLT, P, P, P, I64, INT, P,
+                                  INT, INT, P, SZ, P]),
     "qlora_grad_norm_workspace_bytes": (SZ, [P, I64]),
     "qlora_grad_norm": (INT, [P, I64, FLT, P, P, SZ, P]),
     "qlora_grad_scale": (INT, [P, P, I64, P, P]),

@@ -1,0 +1,119 @@
+// Internal declarations of the vocabulary head's loss: what its entry points
+// lay out and launch.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace qlora {
+
+constexpr int kTile = 256;  // rows and columns of a product's tile
+constexpr int kStep = 32;   // reduction elements of a step
+
+// A live row as the tile kernels see it: its largest logit, exp(-log of its
+// sum), the factor of its gradient, its label. Behind the live rows, up to a
+// whole tile: zeros and no label.
+struct HeadColumn {
+  float most, over, factor;
+  int32_t label;
+};
+
+// The rows that carry loss, in order: map[j] is the row of live row j, inv[m]
+// the live row of row m or -1, *count how many there are.
+struct HeadRows {
+  const void* labels;
+  bool ids64;
+  const float* dloss;  // rows with 0 carry nothing either; NULL in the forward
+  const float* stats;  // [2, M]; NULL in the forward
+  float scale;
+  int64_t M, V;
+  int32_t* map;
+  int32_t* inv;
+  int32_t* count;
+  HeadColumn* cols;
+};
+hipError_t launch_head_rows(const HeadRows& a, hipStream_t st);
+
+// b operands lie in tiles of 256 of their rows, a tile's steps one behind
+// another, 16 KB each: [tile][step][256][32].
+// out = rows map[j] of src (rows j themselves without a map), j < *count (or
+// `rows` without), reduction over the K columns; zero up to a whole tile of rows
+// and a whole step.
+hipError_t launch_head_pack_rows(const uint16_t* src, int64_t ld, const int32_t* map,
+                                 const int32_t* count, int64_t rows, int64_t K, uint16_t* out,
+                                 hipStream_t st);
+// The transpose: rows are the K columns of src, the reduction runs over its rows,
+// zero up to two whole steps. `steps`: those that a tile has room for.
+hipError_t launch_head_pack_cols(const uint16_t* src, int64_t ld, const int32_t* map,
+                                 const int32_t* count, int64_t rows, int64_t K, int64_t steps,
+                                 uint16_t* out, hipStream_t st);
+// out[rows][Kp] = src with zeros behind its K columns.
+hipError_t launch_head_pad(const uint16_t* src, int64_t ld, int64_t rows, int64_t K, int64_t Kp,
+                           uint16_t* out, hipStream_t st);
+
+// A product's tiles: rows of a [rows, red] (row stride lda elements, a multiple
+// of 8, 16-byte aligned) against columns of b, fp32 sums.
+struct HeadTiles {
+  const uint16_t* a;
+  int64_t lda;
+  const uint16_t* b;
+  int64_t b_steps;  // steps that a tile of b has room for
+  const int32_t* count;
+  int64_t v0, vocab;  // the piece's first entry of the vocabulary, its entries
+  int64_t rows_most;  // the most live rows there can be
+  int64_t K;          // the hidden size
+  int64_t steps;      // of the logits' reduction
+  float scale;
+  // logits: partial statistics [tile of the vocabulary][rows_pad][2]
+  const HeadColumn* cols;
+  float2* part;
+  int64_t rows_pad;
+  float* at_label;
+  // probabilities: live rows by vocabulary, and their gradients transposed
+  uint16_t* P;
+  int64_t ldp;
+  int p_terms;
+  uint16_t* Q;
+  int64_t ldq;
+  int q_terms;
+  // gradients
+  float* acc;  // [splits][live rows up to a whole tile][K]
+  bool add;    // to what acc holds
+  void* dW;
+  bool dw_bf16, accumulate;
+};
+// Partial statistics and the labels' logits; probabilities; the gradient of the
+// live rows; the gradient of the piece's rows of W.
+hipError_t launch_head_stats(const HeadTiles& a, hipStream_t st);
+hipError_t launch_head_probs(const HeadTiles& a, hipStream_t st);
+hipError_t launch_head_dx(const HeadTiles& a, hipStream_t st);
+hipError_t launch_head_dw(const HeadTiles& a, hipStream_t st);
+// Floats of acc: the rows' sums, or the splits' where rows are few (they have
+// 256 tiles at most).
+inline int64_t head_acc_floats(int64_t rows_pad, int64_t K) {
+  const int64_t few = (int64_t)256 * kTile * kTile;
+  return rows_pad * K > few ? rows_pad * K : few;
+}
+
+// loss and stats (may be NULL) of all M rows from the partial statistics.
+hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
+                            const float* at_label, const int32_t* inv, int64_t M, float* loss,
+                            float* stats, hipStream_t st);
+// dX of all M rows: factor (sum of the splits - the label's row of W), or 0.
+// steps: of the reduction of the first piece's product, which has the most
+// splits.
+struct HeadDx {
+  const float* acc;
+  int steps;
+  const int32_t* inv;
+  const int32_t* count;
+  const HeadColumn* cols;
+  const uint16_t* W;
+  int64_t ldw, M, K;
+  void* dX;
+  int64_t lddx;
+};
+hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st);
+
+}  // namespace qlora

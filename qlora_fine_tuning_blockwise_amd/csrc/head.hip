@@ -1,0 +1,708 @@
+// The loss of the vocabulary head on gfx950, without keeping the logits.
+//
+// For a row x[K], a head W[V, K], a label and a scale s:
+//   z_v  = s sum_k x_k W_vk,  m = max z,  L = log sum_v exp(z_v - m)
+//   loss = L + (m - z_label)
+//   p_v  = exp(z_v - m) exp(-L)
+//   dX   = dloss s (sum_v p_v W_v - W_label)
+//   dW_v = sum over the rows of dloss s (p_v - [v = label]) x
+// A row whose label lies outside of the vocabulary carries no loss.
+//
+// The rows that carry loss are gathered first (in a padded or masked batch a
+// half of the rows and more carry none), so that the products run over live
+// rows only; how many there are is known on the device alone, and every kernel
+// reads it there.
+//
+// Forward: one product of the matrix units. A tile of 256 entries of the
+// vocabulary by 256 rows keeps its logits in registers and leaves each row's
+// largest one and the sum of exponentials taken from it, 8 bytes for 256 logits.
+// Backward, in pieces of the vocabulary: the logits are formed again tile by
+// tile and leave as probabilities in bf16, then the piece's part of the rows'
+// gradients and of W's is a product each.
+//
+// Roundings to bf16: the products' operands have to be bf16. dX is formed from
+// the probabilities alone and the label's row of W is subtracted in fp32 at
+// the end, so that what is rounded (2^-8 of a probability at most) is a part of
+// a small mean of W's rows, not of the label's row. For fp32 gradients a
+// probability is split into two bf16 numbers (2^-16 is lost) and the products
+// have twice the terms.
+//
+// The tile loop is the dense stage's of the linear layer (gemm_nt.hip has its
+// description): 256 x 256 tiles, four waves of 128 x 128 on
+// v_mfma_f32_32x32x16_bf16, operands by direct-to-LDS loads, a in a ring of three
+// pairs of steps, b in a ring of four steps.
+#include <type_traits>
+
+#include "head.h"
+#include "rows.h"
+
+namespace qlora {
+namespace {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+__device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// ------------------------------------------------------------- live rows
+constexpr int kRowThreads = 1024;
+
+// One workgroup: a thread counts the live rows of its run of rows, the counts
+// are summed over the threads, and it writes its own.
+__global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadRows a) {
+  __shared__ int32_t sums[kRowThreads / 64];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int64_t per = (a.M + kRowThreads - 1) / kRowThreads;
+  const int64_t first = t * per < a.M ? t * per : a.M;
+  const int64_t last = first + per < a.M ? first + per : a.M;
+  const auto live = [&](int64_t m, int64_t& label) {
+    label = load_index(a.labels, a.ids64, m);
+    return label >= 0 && label < a.V && (!a.dloss || a.dloss[m] != 0.0f);
+  };
+  int32_t n = 0;
+  int64_t label;
+  for (int64_t m = first; m < last; ++m) n += live(m, label);
+  int32_t upto = n;  // inclusive over the wave
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t o = __shfl_up(upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 63) sums[wave] = upto;
+  __syncthreads();
+  int32_t before = 0, all = 0;
+  for (int w = 0; w < kRowThreads / 64; ++w) {
+    if (w < wave) before += sums[w];
+    all += sums[w];
+  }
+  int32_t j = before + upto - n;
+  for (int64_t m = first; m < last; ++m) {
+    const bool is = live(m, label);
+    a.inv[m] = is ? j : -1;
+    if (!is) continue;
+    a.map[j] = (int32_t)m;
+    HeadColumn c{0.0f, 0.0f, 0.0f, (int32_t)label};
+    if (a.stats) {
+      c.most = a.stats[m];
+      c.over = exp2_fast(-a.stats[a.M + m] * kLog2e);
+      c.factor = a.dloss[m] * a.scale;
+    }
+    a.cols[j++] = c;
+  }
+  const int32_t end = (all + kTile - 1) / kTile * kTile;
+  for (int32_t k = all + t; k < end; k += kRowThreads) a.cols[k] = HeadColumn{0.0f, 0.0f, 0.0f, -1};
+  if (t == 0) *a.count = all;
+}
+
+// ------------------------------------------------------------- b operands
+// A thread takes 8 columns of a row: 16 bytes of a step.
+__global__ __launch_bounds__(256) void head_pack_rows_kernel(const uint16_t* src, int64_t ld,
+                                                             const int32_t* map,
+                                                             const int32_t* count, int64_t rows,
+                                                             int64_t K, uint16_t* out) {
+  const int64_t steps = (K + kStep - 1) / kStep, vecs = steps * 4;
+  const int64_t n = count ? *count : rows;
+  const int64_t end = (n + kTile - 1) / kTile * kTile;
+  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t j = at / vecs, c = at - j * vecs;
+  if (j >= end) return;
+  Vec<true, 8> v = zero_vec<true, 8>();
+  if (j < n) {
+    const uint16_t* p = src + (map ? (int64_t)map[j] : j) * ld + 8 * c;
+    const int have = count_below<8>(8 * c, K);
+    v = have == 8 ? load_vec<true, 8>(p) : load_part<true, 8>(p, have);
+  }
+  uint16_t* to = out + ((j / kTile) * steps + c / 4) * (kTile * kStep) + (j % kTile) * kStep + (c % 4) * 8;
+  *reinterpret_cast<u32x4_t*>(to) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
+}
+
+// A workgroup turns 32 rows by 256 columns, a whole step of a tile (16 KB)
+// through LDS.
+__global__ __launch_bounds__(256) void head_pack_cols_kernel(const uint16_t* src, int64_t ld,
+                                                             const int32_t* map,
+                                                             const int32_t* count, int64_t rows,
+                                                             int64_t K, int64_t steps,
+                                                             uint16_t* out) {
+  constexpr int kPitch = kTile + 8;
+  __shared__ __attribute__((aligned(16))) uint16_t tile[kStep * kPitch];
+  const int64_t n = count ? *count : rows;
+  const int64_t r0 = (int64_t)blockIdx.y * kStep, k0 = (int64_t)blockIdx.x * kTile;
+  if (r0 >= (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep)) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = i * 256 + threadIdx.x, r = at / 32, c = at % 32 * 8;
+    Vec<true, 8> v = zero_vec<true, 8>();
+    if (r0 + r < n) {
+      const uint16_t* p = src + (map ? (int64_t)map[r0 + r] : r0 + r) * ld + k0 + c;
+      const int have = count_below<8>(k0 + c, K);
+      v = have == 8 ? load_vec<true, 8>(p) : load_part<true, 8>(p, have);
+    }
+    *reinterpret_cast<u32x4_t*>(&tile[r * kPitch + c]) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
+  }
+  __syncthreads();
+  uint16_t* to = out + ((int64_t)blockIdx.x * steps + blockIdx.y) * (kTile * kStep);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int at = i * 256 + threadIdx.x, c = at / 4, r = at % 4 * 8;
+    uint32_t w[4];
+#pragma unroll
+    for (int h = 0; h < 4; ++h)
+      w[h] = tile[(r + 2 * h) * kPitch + c] | (uint32_t)tile[(r + 2 * h + 1) * kPitch + c] << 16;
+    *reinterpret_cast<u32x4_t*>(to + at * 8) = u32x4_t{w[0], w[1], w[2], w[3]};
+  }
+}
+
+__global__ __launch_bounds__(256) void head_pad_kernel(const uint16_t* src, int64_t ld,
+                                                       int64_t rows, int64_t K, int64_t Kp,
+                                                       uint16_t* out) {
+  const int64_t vecs = Kp / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t r = at / vecs, c = (at - r * vecs) * 8;
+  if (r >= rows) return;
+  const int have = count_below<8>(c, K);
+  const uint16_t* p = src + r * ld + c;
+  const Vec<true, 8> v = have == 8 ? load_vec<true, 8>(p) : load_part<true, 8>(p, have);
+  *reinterpret_cast<u32x4_t*>(out + at * 8) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
+}
+
+// ------------------------------------------------------------------ tiles
+constexpr int kOp = kTile * kStep;  // bf16 elements of one step of an operand (16 KB)
+constexpr int kPair = 2 * kOp;      // of two steps
+constexpr int kGroup = 4;           // tile rows per group in the tile order
+
+// Tile of workgroup `wg`: each XCD (wg % 8) gets a contiguous range of an order
+// that walks groups of kGroup tile rows column by column, so that the tiles
+// that run together on it share row panels of a and column panels of b.
+__device__ __forceinline__ void tile_of(int wg, int tiles_m, int tiles_n, int& tm, int& tn) {
+  const int T = tiles_m * tiles_n;
+  const int xcd = wg & 7, idx = wg >> 3;
+  const int per = T >> 3, extra = T & 7;
+  const int t = xcd * per + (xcd < extra ? xcd : extra) + idx;
+  const int group = t / (kGroup * tiles_n);
+  const int first = group * kGroup;
+  const int rows = tiles_m - first < kGroup ? tiles_m - first : kGroup;
+  const int in = t - group * kGroup * tiles_n;
+  tm = first + in % rows;
+  tn = in / rows;
+}
+
+// At most n vector-memory operations in flight, no LDS operation.
+template <int n>
+__device__ __forceinline__ void wait_vmem_lgkm0() {
+  static_assert(n >= 0 && n < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (0x7 << 4));
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+__device__ __forceinline__ const void* uniform_ptr(const void* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const void*>(((uint64_t)hi << 32) | lo);
+}
+
+template <int S, int N, typename T>
+__device__ __forceinline__ T* pick(T* const (&arr)[N]) {
+  static_assert(S >= 0 && S < N, "stage index");
+  return arr[S];
+}
+
+constexpr int kStats = 0, kProbs = 1, kDx = 2, kDw = 3;
+
+__device__ __forceinline__ int ceil_tile(int64_t n) { return (int)((n + kTile - 1) / kTile); }
+__device__ __forceinline__ int64_t whole_pairs(int64_t n) { return (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep); }
+
+// Splits of the live rows' gradient: as many as give each of 256 CUs a tile, with
+// at least 16 steps each. With more than one, tiles times splits is at most 256.
+constexpr int kMostSplits = 8;
+__device__ __forceinline__ int dx_splits(int tiles, int steps) {
+  int s = 256 / tiles;
+  s = s > kMostSplits ? kMostSplits : s;
+  while (s > 1 && steps / s < 16) --s;
+  return s < 1 ? 1 : s;
+}
+
+template <int kMode>
+__global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
+  __shared__ __attribute__((aligned(1024))) uint16_t sa0[kPair];
+  __shared__ __attribute__((aligned(1024))) uint16_t sa1[kPair];
+  __shared__ __attribute__((aligned(1024))) uint16_t sa2[kPair];
+  __shared__ __attribute__((aligned(1024))) uint16_t sb0[kOp];
+  __shared__ __attribute__((aligned(1024))) uint16_t sb1[kOp];
+  __shared__ __attribute__((aligned(1024))) uint16_t sb2[kOp];
+  __shared__ __attribute__((aligned(1024))) uint16_t sb3[kOp];
+  uint16_t* const sa[3] = {sa0, sa1, sa2};
+  uint16_t* const sb[4] = {sb0, sb1, sb2, sb3};
+  const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
+  const int wm = w >> 1, wn = w & 1;
+  const int live = __builtin_amdgcn_readfirstlane(*p.count);
+  // Rows, columns and steps of this product; half: steps of one term.
+  const int64_t M = kMode == kDx ? live : p.vocab;
+  const int64_t N = kMode == kStats || kMode == kProbs ? live : p.K;
+  const int half = kMode == kDx   ? (int)(whole_pairs(p.vocab) / kStep)
+                   : kMode == kDw ? (int)(whole_pairs(live) / kStep)
+                                  : (int)p.steps;
+  const int all = kMode == kDx ? half * p.p_terms : kMode == kDw ? half * p.q_terms : half;
+  const int tiles_m = ceil_tile(M), tiles_n = ceil_tile(N);
+  const int splits = kMode == kDx ? dx_splits(max(tiles_m * tiles_n, 1), all) : 1;
+  if ((int)blockIdx.x >= tiles_m * tiles_n * splits) return;
+  int tm, tn;
+  const int split = kMode == kDx ? (int)blockIdx.x % splits : 0;
+  tile_of(kMode == kDx ? (int)blockIdx.x / splits : (int)blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
+  // A split has a whole number of pairs of steps.
+  const int per = kMode == kDx ? (all / 2 + splits - 1) / splits * 2 : all;
+  const int ks0 = split * per;
+  const int nsteps = kMode == kDx ? min(per, all - ks0) : all;
+
+  f32x16_t acc[4][4];
+#pragma unroll
+  for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[mt][nt][e] = 0.0f;
+
+  if (nsteps > 0) {
+    const int npairs = (nsteps + 1) / 2;
+    const int64_t k0 = (int64_t)ks0 * kStep;
+    // Direct-to-LDS roles. a: wave w loads rows 64w + 8q + L/8 (q = 0..7) of
+    // each pair, lane L at LDS position L%8 (global chunk (L%8) ^ ((row>>1)&7)).
+    // b: wave w loads windows 4w .. 4w+3 (16 rows each) of each step. Rows of a
+    // past the matrix read its last row; b has whole tiles.
+    uint32_t aoff[8], boff[4];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      const int row = 64 * w + 8 * q + (lane >> 3);
+      const int c = (lane & 7) ^ ((row >> 1) & 7);
+      const int64_t ar = m0 + row < M ? row : M - 1 - m0;
+      aoff[q] = (uint32_t)(ar * p.lda * 2 + 16 * c);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 16 * (4 * w + j) + (lane >> 2);
+      const int c = (lane & 3) ^ ((row >> 2) & 3);
+      boff[j] = (uint32_t)(row * 64 + 16 * c);
+    }
+    // a ends with its last row's last step: what a final odd pair has past it
+    // in that row reads zeros (in other rows the next row; it is not used).
+    const int64_t a_bytes = min(((M - 1 - m0) * p.lda + (int64_t)(all - ks0) * kStep) * 2, (int64_t)0x7FFFFFFF);
+    const __amdgpu_buffer_rsrc_t ares = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)uniform_ptr(p.a + m0 * p.lda + k0), (short)0, (int)a_bytes, 0x00020000);
+    const __amdgpu_buffer_rsrc_t bres = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)uniform_ptr(p.b + (int64_t)tn * p.b_steps * kOp), (short)0, (int)0x7FFFFFFF, 0x00020000);
+    typedef __attribute__((address_space(3))) void lds_void;
+    auto dma_a = [&](int q, int pair, uint16_t* slot) {
+      const int ps = pair < npairs ? pair : npairs - 1;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void*)(slot + (64 * w + 8 * q) * 64), 16,
+                                               aoff[q], 128 * ps, 0, 0);
+    };
+    auto dma_b = [&](int j, int kb, uint16_t* stage) {
+      int ks = ks0 + (kb < nsteps ? kb : nsteps - 1);
+      if (kMode == kDx || kMode == kDw) ks -= ks >= half ? half : 0;  // the second term's
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(bres, (lds_void*)(stage + 512 * (4 * w + j)), 16,
+                                               boff[j], kOp * 2 * ks, 0, 0);
+    };
+    // Fragment reads: A fragment (mt, step half par, substep s): tile row
+    // 128wm + 32mt + i, chunk 4par + 2s + h, at position chunk ^ ((i >> 1) & 7).
+    // B fragment (nt, s): tile row 128wn + 32nt + i, chunk 2s + h at (2s + h) ^
+    // ((i >> 2) & 3).
+    const int swa = (i >> 1) & 7, swb = (i >> 2) & 3;
+    int fa[2][2];
+#pragma unroll
+    for (int par = 0; par < 2; ++par)
+#pragma unroll
+      for (int ss = 0; ss < 2; ++ss)
+        fa[par][ss] = (128 * wm + i) * 64 + 8 * ((4 * par + 2 * ss + h) ^ swa);
+    const int fb0 = (128 * wn + i) * 32 + 8 * (h ^ swb);
+    const int fb1 = (128 * wn + i) * 32 + 8 * ((2 + h) ^ swb);
+
+    // Prologue: pair 0, steps 0 and 1 of b, pair 1, step 2 of b; wait for the
+    // first three, all that steps 0 and 1 read before the loop's first barrier.
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dma_a(q, 0, sa0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dma_b(j, 0, sb0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dma_b(j, 1, sb1);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) dma_a(q, 1, sa1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) dma_b(j, 2, sb2);
+    wait_vmem_lgkm0<12>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    u32x4_t a0[4], b0[4], a1[4], b1[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      a0[t] = *reinterpret_cast<const u32x4_t*>(&sa0[fa[0][0] + 2048 * t]);
+      b0[t] = *reinterpret_cast<const u32x4_t*>(&sb0[fb0 + 1024 * t]);
+    }
+    // One step kb (b stage kb % 4 = SB, a slot (kb / 2) % 3 = SA, half PAR):
+    // substep 0 computes on (a0, b0) while (kb, 1) is read into (a1, b1);
+    // substep 1 computes on (a1, b1) while (kb+1, 0) is read into (a0, b0). One
+    // load after every fourth MFMA: b of step kb+3 in substep 0, four a loads of
+    // pair kb/2 + 2 in substep 1.
+    auto step = [&](int kb, auto sbc, auto sac, auto parc) {
+      constexpr int SB = decltype(sbc)::value, SA = decltype(sac)::value;
+      constexpr int PAR = decltype(parc)::value;
+      constexpr int SA1 = PAR ? (SA + 1) % 3 : SA;  // slot of step kb+1
+      constexpr int PAR1 = PAR ^ 1;
+      uint16_t* const acur = pick<SA>(sa);
+      uint16_t* const anxt = pick<SA1>(sa);
+      uint16_t* const ald = pick<(SA + 2) % 3>(sa);
+      uint16_t* const bcur = pick<SB>(sb);
+      uint16_t* const bnxt = pick<(SB + 1) % 4>(sb);
+      uint16_t* const bld = pick<(SB + 3) % 4>(sb);
+#pragma unroll
+      for (int g = 0; g < 16; ++g) {
+        const int mt = g >> 2, nt = g & 3;
+        acc[mt][nt] = mfma_32x32x16(a0[mt], b0[nt], acc[mt][nt]);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (g < 8) {
+          const int t = g >> 1;
+          if (g & 1)
+            b1[t] = *reinterpret_cast<const u32x4_t*>(&bcur[fb1 + 1024 * t]);
+          else
+            a1[t] = *reinterpret_cast<const u32x4_t*>(&acur[fa[PAR][1] + 2048 * t]);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if ((g & 3) == 3) {
+          dma_b(g >> 2, kb + 3, bld);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int g = 0; g < 16; ++g) {
+        const int mt = g >> 2, nt = g & 3;
+        acc[mt][nt] = mfma_32x32x16(a1[mt], b1[nt], acc[mt][nt]);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if (g < 8) {
+          const int t = g >> 1;
+          if (g & 1)
+            b0[t] = *reinterpret_cast<const u32x4_t*>(&bnxt[fb0 + 1024 * t]);
+          else
+            a0[t] = *reinterpret_cast<const u32x4_t*>(&anxt[fa[PAR1][0] + 2048 * t]);
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        }
+        if ((g & 3) == 3) {
+          dma_a(4 * PAR + (g >> 2), kb / 2 + 2, ald);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // This step's eight loads may still fly; everything earlier has landed.
+      wait_vmem_lgkm0<8>();
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    using I2 = std::integral_constant<int, 2>;
+    using I3 = std::integral_constant<int, 3>;
+    int kb = 0;
+    for (; kb + 12 <= nsteps; kb += 12) {
+      step(kb + 0, I0(), I0(), I0());
+      step(kb + 1, I1(), I0(), I1());
+      step(kb + 2, I2(), I1(), I0());
+      step(kb + 3, I3(), I1(), I1());
+      step(kb + 4, I0(), I2(), I0());
+      step(kb + 5, I1(), I2(), I1());
+      step(kb + 6, I2(), I0(), I0());
+      step(kb + 7, I3(), I0(), I1());
+      step(kb + 8, I0(), I1(), I0());
+      step(kb + 9, I1(), I1(), I1());
+      step(kb + 10, I2(), I2(), I0());
+      step(kb + 11, I3(), I2(), I1());
+    }
+    if (kb + 0 < nsteps) step(kb + 0, I0(), I0(), I0());
+    if (kb + 1 < nsteps) step(kb + 1, I1(), I0(), I1());
+    if (kb + 2 < nsteps) step(kb + 2, I2(), I1(), I0());
+    if (kb + 3 < nsteps) step(kb + 3, I3(), I1(), I1());
+    if (kb + 4 < nsteps) step(kb + 4, I0(), I2(), I0());
+    if (kb + 5 < nsteps) step(kb + 5, I1(), I2(), I1());
+    if (kb + 6 < nsteps) step(kb + 6, I2(), I0(), I0());
+    if (kb + 7 < nsteps) step(kb + 7, I3(), I0(), I1());
+    if (kb + 8 < nsteps) step(kb + 8, I0(), I1(), I0());
+    if (kb + 9 < nsteps) step(kb + 9, I1(), I1(), I1());
+    if (kb + 10 < nsteps) step(kb + 10, I2(), I2(), I0());
+    // Direct-to-LDS loads still in flight must land before LDS is used again or
+    // the workgroup ends.
+    wait_vmem_lgkm0<0>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Accumulator element e of (mt, nt) is row 32mt + 8(e/4) + 4h + e%4, column
+  // 32nt + i of this wave's 128 x 128 block.
+  const int64_t mw = m0 + 128 * wm + 4 * h, nw = n0 + 128 * wn + i;
+  if constexpr (kMode == kStats) {
+    // A lane has 64 entries of the vocabulary of each of its four rows; the
+    // other half of the wave and the other wave of the rows have the rest.
+    float2* red = reinterpret_cast<float2*>(sa0);
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const bool in = mw + 32 * mt + 8 * (e >> 2) + (e & 3) < M;
+          acc[mt][nt][e] = in ? acc[mt][nt][e] * p.scale : -INFINITY;
+          m = fmaxf(m, acc[mt][nt][e]);
+        }
+      m = fmaxf(m, __shfl_xor(m, 32));
+      const float from = m == -INFINITY ? 0.0f : m;  // none of the vocabulary, or none above it
+      float s = 0.0f;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += exp2_fast((acc[mt][nt][e] - from) * kLog2e);
+      s += __shfl_xor(s, 32);
+      if (h == 0) red[wm * kTile + 128 * wn + 32 * nt + i] = float2{m, s};
+      // The label's logit, where this wave has it.
+      const int64_t n = nw + 32 * nt;
+      const int label = n < N ? p.cols[n].label : -1;
+      const int64_t d = label - (p.v0 + mw);
+      const bool mine = label >= 0 && d >= 0 && d < 128 && !(d & 4);
+      if (__ballot(mine)) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (mine && d == 32 * mt + 8 * (e >> 2) + (e & 3)) p.at_label[n] = acc[mt][nt][e];
+      }
+    }
+    __syncthreads();
+    if (n0 + tid < N) {
+      const float2 x = red[tid], y = red[kTile + tid];
+      const float m = fmaxf(x.x, y.x), from = m == -INFINITY ? 0.0f : m;
+      const float s = x.y * exp2_fast((x.x - from) * kLog2e) + y.y * exp2_fast((y.x - from) * kLog2e);
+      p.part[(p.v0 / kTile + tm) * p.rows_pad + n0 + tid] = float2{m, s};
+    }
+  } else if constexpr (kMode == kProbs) {
+    const int64_t phalf = whole_pairs(p.vocab), qhalf = whole_pairs(live);
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const int64_t n = nw + 32 * nt;
+      const HeadColumn c = p.cols[n];  // whole tiles: zeros behind the live rows
+      const int64_t d = c.label < 0 ? -1 : c.label - (p.v0 + mw);
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          float pr[4];
+          const int64_t v = mw + 32 * mt + 8 * g;
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            pr[e] = v + e < M && c.label >= 0 ? exp2_fast(fmaf(acc[mt][nt][4 * g + e], p.scale, -c.most) * kLog2e) * c.over
+                              : 0.0f;
+          if (p.P && n < N && v < phalf) {
+            const u32x2_t hi = {pack_bf16x2(pr[0], pr[1]), pack_bf16x2(pr[2], pr[3])};
+            uint16_t* to = p.P + n * p.ldp + v;
+            *reinterpret_cast<u32x2_t*>(to) = hi;
+            if (p.p_terms == 2)
+              *reinterpret_cast<u32x2_t*>(to + phalf) =
+                  u32x2_t{pack_bf16x2(pr[0] - bf16_lo(hi[0]), pr[1] - bf16_hi(hi[0])),
+                          pack_bf16x2(pr[2] - bf16_lo(hi[1]), pr[3] - bf16_hi(hi[1]))};
+          }
+          if (p.Q && n < qhalf) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if (v + e >= M) continue;
+              const float q = (pr[e] - (d == 32 * mt + 8 * g + e ? 1.0f : 0.0f)) * c.factor;
+              const uint32_t hi = pack_bf16x2(q, 0.0f);
+              uint16_t* to = p.Q + (v + e) * p.ldq + n;
+              *to = (uint16_t)hi;
+              if (p.q_terms == 2) to[qhalf] = (uint16_t)pack_bf16x2(q - bf16_lo(hi), 0.0f);
+            }
+          }
+        }
+    }
+  } else {
+    const int64_t ldo = p.K;
+    float* to = kMode == kDx ? p.acc + (int64_t)split * tiles_m * kTile * ldo : nullptr;
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      const int64_t n = nw + 32 * nt;
+      if (n >= N) continue;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int64_t m = mw + 32 * mt + 8 * (e >> 2) + (e & 3);
+          if (m >= M) continue;
+          if constexpr (kMode == kDx) {
+            float v = acc[mt][nt][e];
+            if (p.add) v += to[m * ldo + n];
+            to[m * ldo + n] = v;
+          } else {
+            const int64_t at = (p.v0 + m) * ldo + n;
+            float v = acc[mt][nt][e];
+            if (p.dw_bf16) {
+              uint16_t* o = static_cast<uint16_t*>(p.dW) + at;
+              if (p.accumulate) v += bf16_lo(*o);
+              store1<true>(o, v);
+            } else {
+              float* o = static_cast<float*>(p.dW) + at;
+              if (p.accumulate) v += *o;
+              *o = v;
+            }
+          }
+        }
+    }
+  }
+}
+
+// -------------------------------------------------------------- the results
+// 16 rows a workgroup, the tiles of the vocabulary in 16 ranges.
+__global__ __launch_bounds__(256) void head_loss_kernel(const float2* part, int64_t tiles,
+                                                        int64_t rows_pad, const float* at_label,
+                                                        const int32_t* inv, int64_t M, float* loss,
+                                                        float* stats) {
+  __shared__ float2 red[16][16];
+  const int r = threadIdx.x % 16, range = threadIdx.x / 16;
+  const int64_t row = (int64_t)blockIdx.x * 16 + r;
+  const int32_t j = row < M ? inv[row] : -1;
+  const int64_t per = (tiles + 15) / 16;
+  float m = -INFINITY, s = 0.0f;
+  if (j >= 0) {
+    const int64_t end = (range + 1) * per < tiles ? (range + 1) * per : tiles;
+#pragma unroll 4
+    for (int64_t t = range * per; t < end; ++t) {
+      const float2 v = part[t * rows_pad + j];
+      const float to = fmaxf(m, v.x), from = to == -INFINITY ? 0.0f : to;
+      s = s * exp2_fast((m - from) * kLog2e) + v.y * exp2_fast((v.x - from) * kLog2e);
+      m = to;
+    }
+  }
+  red[range][r] = float2{m, s};
+  __syncthreads();
+  if (threadIdx.x >= 16 || row >= M) return;
+  for (int k = 1; k < 16; ++k) {
+    const float2 v = red[k][r];
+    const float to = fmaxf(m, v.x), from = to == -INFINITY ? 0.0f : to;
+    s = s * exp2_fast((m - from) * kLog2e) + v.y * exp2_fast((v.x - from) * kLog2e);
+    m = to;
+  }
+  const float L = logf(s);
+  loss[row] = j >= 0 ? L + (m - at_label[j]) : 0.0f;
+  if (stats) {
+    stats[row] = j >= 0 ? m : 0.0f;
+    stats[M + row] = j >= 0 ? L : 0.0f;
+  }
+}
+
+// A thread takes 8 columns of a row.
+template <bool kBf16>
+__global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
+  constexpr int E = 8;
+  const int64_t vecs = (a.K + E - 1) / E, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = at / vecs, k = (at - row * vecs) * E;
+  if (row >= a.M) return;
+  const int n = count_below<E>(k, a.K);
+  const int32_t j = a.inv[row];
+  float v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  if (j >= 0) {
+    const int tiles_m = ceil_tile(*a.count);
+    const int splits = dx_splits(tiles_m * ceil_tile(a.K), a.steps);
+    const HeadColumn c = a.cols[j];
+    const float* from = a.acc + (int64_t)j * a.K + k;
+    for (int s = 0; s < splits; ++s, from += (int64_t)tiles_m * kTile * a.K) {
+      const Vec<false, E> r = n == E ? load_vec<false, E>(from) : load_part<false, E>(from, n);
+      float o[E];
+      to_float<false, E>(r, o);
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += o[e];
+    }
+    const uint16_t* w = a.W + (int64_t)c.label * a.ldw + k;
+    const Vec<true, E> r = n == E ? load_vec<true, E>(w) : load_part<true, E>(w, n);
+    float o[E];
+    to_float<true, E>(r, o);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = (v[e] - o[e]) * c.factor;
+  }
+  elem_t<kBf16>* to = static_cast<elem_t<kBf16>*>(a.dX) + row * a.lddx + k;
+  if (n == E)
+    store_vec<kBf16, E>(to, v);
+  else
+    store_part<kBf16, E>(to, v, n);
+}
+
+unsigned blocks_of(int64_t n) { return (unsigned)((n + 255) / 256); }
+int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
+
+template <int kMode>
+hipError_t tiles(const HeadTiles& a, int64_t grid, hipStream_t st) {
+  hipLaunchKernelGGL(head_tile_kernel<kMode>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_head_rows(const HeadRows& a, hipStream_t st) {
+  hipLaunchKernelGGL(head_rows_kernel, dim3(1), dim3(kRowThreads), 0, st, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_pack_rows(const uint16_t* src, int64_t ld, const int32_t* map,
+                                 const int32_t* count, int64_t rows, int64_t K, uint16_t* out,
+                                 hipStream_t st) {
+  const int64_t vecs = (K + kStep - 1) / kStep * 4;
+  hipLaunchKernelGGL(head_pack_rows_kernel, dim3(blocks_of(tiles_of(rows) * kTile * vecs)), dim3(256),
+                     0, st, src, ld, map, count, rows, K, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_pack_cols(const uint16_t* src, int64_t ld, const int32_t* map,
+                                 const int32_t* count, int64_t rows, int64_t K, int64_t steps,
+                                 uint16_t* out, hipStream_t st) {
+  const int64_t used = (rows + 2 * kStep - 1) / (2 * kStep) * 2;
+  hipLaunchKernelGGL(head_pack_cols_kernel, dim3((unsigned)tiles_of(K), (unsigned)used), dim3(256), 0,
+                     st, src, ld, map, count, rows, K, steps, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_pad(const uint16_t* src, int64_t ld, int64_t rows, int64_t K, int64_t Kp,
+                           uint16_t* out, hipStream_t st) {
+  hipLaunchKernelGGL(head_pad_kernel, dim3(blocks_of(rows * (Kp / 8))), dim3(256), 0, st, src, ld,
+                     rows, K, Kp, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_stats(const HeadTiles& a, hipStream_t st) {
+  return tiles<kStats>(a, tiles_of(a.vocab) * tiles_of(a.rows_most), st);
+}
+
+hipError_t launch_head_probs(const HeadTiles& a, hipStream_t st) {
+  return tiles<kProbs>(a, tiles_of(a.vocab) * tiles_of(a.rows_most), st);
+}
+
+hipError_t launch_head_dx(const HeadTiles& a, hipStream_t st) {
+  const int64_t grid = tiles_of(a.rows_most) * tiles_of(a.K);
+  return tiles<kDx>(a, grid > 256 ? grid : 256, st);
+}
+
+hipError_t launch_head_dw(const HeadTiles& a, hipStream_t st) {
+  return tiles<kDw>(a, tiles_of(a.vocab) * tiles_of(a.K), st);
+}
+
+hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
+                            const float* at_label, const int32_t* inv, int64_t M, float* loss,
+                            float* stats, hipStream_t st) {
+  hipLaunchKernelGGL(head_loss_kernel, dim3((unsigned)((M + 15) / 16)), dim3(256), 0, st, part, tiles,
+                     rows_pad, at_label, inv, M, loss, stats);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st) {
+  const dim3 grid(blocks_of(a.M * ((a.K + 7) / 8)));
+  if (bf16)
+    hipLaunchKernelGGL(head_dx_finish_kernel<true>, grid, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL(head_dx_finish_kernel<false>, grid, dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace qlora
