@@ -43,43 +43,43 @@ hipError_t launch_head_rows(const HeadRows& a, hipStream_t st);
 hipError_t launch_head_pack_rows(const uint16_t* src, int64_t ld, const int32_t* map,
                                  const int32_t* count, int64_t rows, int64_t K, uint16_t* out,
                                  hipStream_t st);
-// The transpose: rows are the K columns of src, the reduction runs over its rows,
-// zero up to two whole steps. `steps`: those that a tile has room for.
-hipError_t launch_head_pack_cols(const uint16_t* src, int64_t ld, const int32_t* map,
-                                 const int32_t* count, int64_t rows, int64_t K, int64_t steps,
-                                 uint16_t* out, hipStream_t st);
-// out[rows][Kp] = src with zeros behind its K columns.
-hipError_t launch_head_pad(const uint16_t* src, int64_t ld, int64_t rows, int64_t K, int64_t Kp,
-                           uint16_t* out, hipStream_t st);
+// out[j] = row map[j] of src (row j without a map) with zeros behind its K columns
+// up to Kp; with `count` for j < *count, and rows of zeros up to two whole steps.
+hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
+                            const int32_t* count, int64_t rows, int64_t K, int64_t Kp, uint16_t* out,
+                            hipStream_t st);
 
-// A product's tiles: rows of a [rows, red] (row stride lda elements, a multiple
-// of 8, 16-byte aligned) against columns of b, fp32 sums.
+// A product's tiles; what a and b are depends on the launch.
 struct HeadTiles {
-  const uint16_t* a;
-  int64_t lda;
+  const uint16_t* a;  // 16-byte aligned rows
+  int64_t lda;        // a multiple of 8
+  int64_t a_plane;    // launch_head_dw: elements to the second term
   const uint16_t* b;
-  int64_t b_steps;  // steps that a tile of b has room for
+  int64_t b_steps;    // steps that a tile of b has room for (logits)
+  int64_t ldb, b_width, vocab_left;  // gradients: b's rows, columns; entries of the vocabulary from v0 on
   const int32_t* count;
   int64_t v0, vocab;  // the piece's first entry of the vocabulary, its entries
   int64_t rows_most;  // the most live rows there can be
   int64_t K;          // the hidden size
   int64_t steps;      // of the logits' reduction
   float scale;
-  // logits: partial statistics [tile of the vocabulary][rows_pad][2]
+  // logits: partial statistics [tile of the vocabulary][rows_pad]
   const HeadColumn* cols;
   float2* part;
   int64_t rows_pad;
   float* at_label;
-  // probabilities: live rows by vocabulary, and their gradients transposed
+  // probabilities P and the logits' gradients Q, live rows by vocabulary; the
+  // second term of P lies behind the first in its row, that of Q a plane on
   uint16_t* P;
   int64_t ldp;
   int p_terms;
   uint16_t* Q;
-  int64_t ldq;
+  int64_t ldq, q_plane;
   int q_terms;
   // gradients
-  float* acc;  // [splits][live rows up to a whole tile][K]
+  float* acc;  // sums of the live rows' gradient, [split][tile][256 x 256]
   bool add;    // to what acc holds
+  int pairs;   // pairs of steps of the first piece's product, which decide the splits
   void* dW;
   bool dw_bf16, accumulate;
 };
@@ -89,11 +89,15 @@ hipError_t launch_head_stats(const HeadTiles& a, hipStream_t st);
 hipError_t launch_head_probs(const HeadTiles& a, hipStream_t st);
 hipError_t launch_head_dx(const HeadTiles& a, hipStream_t st);
 hipError_t launch_head_dw(const HeadTiles& a, hipStream_t st);
-// Floats of acc: the rows' sums, or the splits' where rows are few (they have
-// 256 tiles at most).
-inline int64_t head_acc_floats(int64_t rows_pad, int64_t K) {
-  const int64_t few = (int64_t)256 * kTile * kTile;
-  return rows_pad * K > few ? rows_pad * K : few;
+// Splits of the live rows' gradient at most, and tiles times splits at most
+// where there is more than one.
+constexpr int kMostSplits = 16, kMostSums = 512;
+// Sums of 256 x 256 that acc holds: tiles times splits, at most, for any count of
+// live rows.
+inline int64_t head_sums(int64_t rows_most, int64_t K) {
+  const int64_t tiles = (rows_most + kTile - 1) / kTile * ((K + kTile - 1) / kTile);
+  const int64_t split = tiles * kMostSplits < kMostSums ? tiles * kMostSplits : kMostSums;
+  return tiles > split ? tiles : split;
 }
 
 // loss and stats (may be NULL) of all M rows from the partial statistics.
@@ -101,11 +105,11 @@ hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
                             const float* at_label, const int32_t* inv, int64_t M, float* loss,
                             float* stats, hipStream_t st);
 // dX of all M rows: factor (sum of the splits - the label's row of W), or 0.
-// steps: of the reduction of the first piece's product, which has the most
-// splits.
+// pairs: as of launch_head_dx.
 struct HeadDx {
   const float* acc;
-  int steps;
+  int pairs;
+  const int32_t* map;
   const int32_t* inv;
   const int32_t* count;
   const HeadColumn* cols;

@@ -114,51 +114,23 @@ __global__ __launch_bounds__(256) void head_pack_rows_kernel(const uint16_t* src
   *reinterpret_cast<u32x4_t*>(to) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
 }
 
-// A workgroup turns 32 rows by 256 columns, a whole step of a tile (16 KB)
-// through LDS.
-__global__ __launch_bounds__(256) void head_pack_cols_kernel(const uint16_t* src, int64_t ld,
-                                                             const int32_t* map,
-                                                             const int32_t* count, int64_t rows,
-                                                             int64_t K, int64_t steps,
-                                                             uint16_t* out) {
-  constexpr int kPitch = kTile + 8;
-  __shared__ __attribute__((aligned(16))) uint16_t tile[kStep * kPitch];
+// A thread copies 8 columns of a row: rows map[j] (or j) of src with zeros behind
+// its K columns, and whole rows of zeros up to two whole steps.
+__global__ __launch_bounds__(256) void head_copy_kernel(const uint16_t* src, int64_t ld,
+                                                        const int32_t* map, const int32_t* count,
+                                                        int64_t rows, int64_t K, int64_t Kp,
+                                                        uint16_t* out) {
   const int64_t n = count ? *count : rows;
-  const int64_t r0 = (int64_t)blockIdx.y * kStep, k0 = (int64_t)blockIdx.x * kTile;
-  if (r0 >= (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep)) return;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = i * 256 + threadIdx.x, r = at / 32, c = at % 32 * 8;
-    Vec<true, 8> v = zero_vec<true, 8>();
-    if (r0 + r < n) {
-      const uint16_t* p = src + (map ? (int64_t)map[r0 + r] : r0 + r) * ld + k0 + c;
-      const int have = count_below<8>(k0 + c, K);
-      v = have == 8 ? load_vec<true, 8>(p) : load_part<true, 8>(p, have);
-    }
-    *reinterpret_cast<u32x4_t*>(&tile[r * kPitch + c]) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
-  }
-  __syncthreads();
-  uint16_t* to = out + ((int64_t)blockIdx.x * steps + blockIdx.y) * (kTile * kStep);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int at = i * 256 + threadIdx.x, c = at / 4, r = at % 4 * 8;
-    uint32_t w[4];
-#pragma unroll
-    for (int h = 0; h < 4; ++h)
-      w[h] = tile[(r + 2 * h) * kPitch + c] | (uint32_t)tile[(r + 2 * h + 1) * kPitch + c] << 16;
-    *reinterpret_cast<u32x4_t*>(to + at * 8) = u32x4_t{w[0], w[1], w[2], w[3]};
-  }
-}
-
-__global__ __launch_bounds__(256) void head_pad_kernel(const uint16_t* src, int64_t ld,
-                                                       int64_t rows, int64_t K, int64_t Kp,
-                                                       uint16_t* out) {
+  const int64_t end = count ? (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
   const int64_t vecs = Kp / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int64_t r = at / vecs, c = (at - r * vecs) * 8;
-  if (r >= rows) return;
-  const int have = count_below<8>(c, K);
-  const uint16_t* p = src + r * ld + c;
-  const Vec<true, 8> v = have == 8 ? load_vec<true, 8>(p) : load_part<true, 8>(p, have);
+  if (r >= end) return;
+  Vec<true, 8> v = zero_vec<true, 8>();
+  if (r < n) {
+    const int have = count_below<8>(c, K);
+    const uint16_t* p = src + (map ? (int64_t)map[r] : r) * ld + c;
+    v = have == 8 ? load_vec<true, 8>(p) : load_part<true, 8>(p, have);
+  }
   *reinterpret_cast<u32x4_t*>(out + at * 8) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
 }
 
@@ -167,20 +139,32 @@ constexpr int kOp = kTile * kStep;  // bf16 elements of one step of an operand (
 constexpr int kPair = 2 * kOp;      // of two steps
 constexpr int kGroup = 4;           // tile rows per group in the tile order
 
-// Tile of workgroup `wg`: each XCD (wg % 8) gets a contiguous range of an order
-// that walks groups of kGroup tile rows column by column, so that the tiles
-// that run together on it share row panels of a and column panels of b.
-__device__ __forceinline__ void tile_of(int wg, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int T = tiles_m * tiles_n;
-  const int xcd = wg & 7, idx = wg >> 3;
-  const int per = T >> 3, extra = T & 7;
-  const int t = xcd * per + (xcd < extra ? xcd : extra) + idx;
+// Place of workgroup `wg` in an order of T: workgroups are dealt to the eight
+// XCDs round robin, and each XCD gets a contiguous range of the order.
+__device__ __forceinline__ int xcd_order(int wg, int T) {
+  const int xcd = wg & 7, per = T >> 3, extra = T & 7;
+  return xcd * per + (xcd < extra ? xcd : extra) + (wg >> 3);
+}
+
+// The order walks groups of kGroup tile rows column by column: the tiles that run
+// together on an XCD share row panels of a and column panels of b.
+__device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
   const int group = t / (kGroup * tiles_n);
   const int first = group * kGroup;
   const int rows = tiles_m - first < kGroup ? tiles_m - first : kGroup;
   const int in = t - group * kGroup * tiles_n;
   tm = first + in % rows;
   tn = in / rows;
+}
+
+// Four values in bf16, and with two terms what they lost, `plane` elements on.
+__device__ __forceinline__ void store_terms(uint16_t* to, int64_t plane, int terms, const float (&v)[4]) {
+  const u32x2_t hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  *reinterpret_cast<u32x2_t*>(to) = hi;
+  if (terms == 2)
+    *reinterpret_cast<u32x2_t*>(to + plane) =
+        u32x2_t{pack_bf16x2(v[0] - bf16_lo(hi[0]), v[1] - bf16_hi(hi[0])),
+                pack_bf16x2(v[2] - bf16_lo(hi[1]), v[3] - bf16_hi(hi[1]))};
 }
 
 // At most n vector-memory operations in flight, no LDS operation.
@@ -209,26 +193,65 @@ constexpr int kStats = 0, kProbs = 1, kDx = 2, kDw = 3;
 __device__ __forceinline__ int ceil_tile(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 __device__ __forceinline__ int64_t whole_pairs(int64_t n) { return (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep); }
 
-// Splits of the live rows' gradient: as many as give each of 256 CUs a tile, with
-// at least 16 steps each. With more than one, tiles times splits is at most 256.
-constexpr int kMostSplits = 8;
-__device__ __forceinline__ int dx_splits(int tiles, int steps) {
-  int s = 256 / tiles;
-  s = s > kMostSplits ? kMostSplits : s;
-  while (s > 1 && steps / s < 16) --s;
-  return s < 1 ? 1 : s;
+// Splits of the live rows' gradient along its reduction of `pairs` pairs of steps:
+// those with the least rounds of 256 workgroups, where a workgroup takes its
+// share of the reduction and the time of 20 pairs besides (first loads, 256 KB
+// of sums read and written). `pairs` is the first piece's throughout, so that
+// every piece adds to the same sums.
+__device__ __forceinline__ int dx_splits(int tiles, int pairs) {
+  int best = 1, least = 0x7FFFFFFF;
+  for (int s = 1; s <= kMostSplits && (s == 1 || tiles * s <= kMostSums) && s <= pairs; ++s) {
+    const int cost = (tiles * s + 255) / 256 * ((pairs + s - 1) / s + 20);
+    if (cost < least) least = cost, best = s;
+  }
+  return best;
 }
 
+// Rows of a matrix from one of its columns on: their first byte, and the bytes up
+// to the matrix's end.
+struct Window {
+  const void* p;
+  int size;
+};
+
+typedef __attribute__((ext_vector_type(4))) short s16x4_t;
+typedef __attribute__((address_space(3))) s16x4_t lds_s16x4;
+
+// A fragment of 8 reduction elements of one column from a tile that lies with
+// its reduction along the rows: in each group of 16 lanes the transposing read
+// takes 4 rows of 16 columns and gives each lane a column. p: the lane's 8 bytes
+// of the first four rows; the other four lie 4 rows on.
+__device__ __forceinline__ u32x4_t read_columns(const uint16_t* p) {
+  const s16x4_t lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+  const s16x4_t hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * kTile));
+  const u32x2_t a = __builtin_bit_cast(u32x2_t, lo), b = __builtin_bit_cast(u32x2_t, hi);
+  return u32x4_t{a[0], a[1], b[0], b[1]};
+}
+
+// The tile loop. Operands come in three forms:
+//   rows    (a of kStats, kProbs, kDx): row-major, the reduction along a row. LDS
+//           has three slots of a 256 x 64 tile (a pair of steps), 16-byte chunk c
+//           of row r at c ^ ((r >> 1) & 7).
+//   steps   (b of kStats, kProbs): [tile][step][256][32]. Four stages of a 256 x
+//           32 tile, chunk c of row r at c ^ ((r >> 2) & 3).
+//   columns (b of kDx, both of kDw): row-major, the reduction down the rows, as
+//           W, the live rows and the logits' gradients lie: no transposed copy is
+//           made. Four stages of a 32 x 256 tile, chunk c of row r at c ^ 2 g(r)
+//           with g = 0, 5, 2, 7 for r % 4: the 4 rows by 32 bytes that 16 lanes
+//           read lie in different banks, as do the 64 bytes of 32 lanes.
+// A pair of slots is loaded two pairs ahead, a stage three steps.
 template <int kMode>
 __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
+  constexpr bool kACols = kMode == kDw, kBCols = kMode == kDx || kMode == kDw;
   __shared__ __attribute__((aligned(1024))) uint16_t sa0[kPair];
   __shared__ __attribute__((aligned(1024))) uint16_t sa1[kPair];
-  __shared__ __attribute__((aligned(1024))) uint16_t sa2[kPair];
+  __shared__ __attribute__((aligned(1024))) uint16_t sa2[kACols ? kOp : kPair];
+  __shared__ __attribute__((aligned(1024))) uint16_t sa3[kACols ? kOp : 8];
   __shared__ __attribute__((aligned(1024))) uint16_t sb0[kOp];
   __shared__ __attribute__((aligned(1024))) uint16_t sb1[kOp];
   __shared__ __attribute__((aligned(1024))) uint16_t sb2[kOp];
   __shared__ __attribute__((aligned(1024))) uint16_t sb3[kOp];
-  uint16_t* const sa[3] = {sa0, sa1, sa2};
+  uint16_t* const sa[4] = {sa0, sa1, sa2, sa3};  // columns: four stages in the first 16 KB of each
   uint16_t* const sb[4] = {sb0, sb1, sb2, sb3};
   const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
@@ -241,12 +264,13 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
                    : kMode == kDw ? (int)(whole_pairs(live) / kStep)
                                   : (int)p.steps;
   const int all = kMode == kDx ? half * p.p_terms : kMode == kDw ? half * p.q_terms : half;
-  const int tiles_m = ceil_tile(M), tiles_n = ceil_tile(N);
-  const int splits = kMode == kDx ? dx_splits(max(tiles_m * tiles_n, 1), all) : 1;
-  if ((int)blockIdx.x >= tiles_m * tiles_n * splits) return;
-  int tm, tn;
-  const int split = kMode == kDx ? (int)blockIdx.x % splits : 0;
-  tile_of(kMode == kDx ? (int)blockIdx.x / splits : (int)blockIdx.x, tiles_m, tiles_n, tm, tn);
+  const int tiles_m = ceil_tile(M), tiles_n = ceil_tile(N), tiles = tiles_m * tiles_n;
+  const int splits = kMode == kDx ? dx_splits(max(tiles, 1), p.pairs) : 1;
+  if ((int)blockIdx.x >= tiles * splits) return;
+  // Each XCD (blockIdx.x % 8) gets a contiguous range of the splits' tiles.
+  int order = xcd_order((int)blockIdx.x, tiles * splits), tm, tn;
+  const int split = kMode == kDx ? order / tiles : 0;
+  tile_of(order - split * tiles, tiles_m, tiles_n, tm, tn);
   const int64_t m0 = (int64_t)tm * kTile, n0 = (int64_t)tn * kTile;
   // A split has a whole number of pairs of steps.
   const int per = kMode == kDx ? (all / 2 + splits - 1) / splits * 2 : all;
@@ -264,47 +288,81 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
   if (nsteps > 0) {
     const int npairs = (nsteps + 1) / 2;
     const int64_t k0 = (int64_t)ks0 * kStep;
-    // Direct-to-LDS roles. a: wave w loads rows 64w + 8q + L/8 (q = 0..7) of
-    // each pair, lane L at LDS position L%8 (global chunk (L%8) ^ ((row>>1)&7)).
-    // b: wave w loads windows 4w .. 4w+3 (16 rows each) of each step. Rows of a
-    // past the matrix read its last row; b has whole tiles.
+    typedef __attribute__((address_space(3))) void lds_void;
+    // Direct-to-LDS roles. rows: wave w loads rows 64w + 8q + L/8 (q = 0..7) of
+    // each pair, lane L at LDS position L%8; rows past the matrix read its last
+    // row. steps: wave w loads windows 4w .. 4w+3 (16 rows each) of each step;
+    // there are whole tiles. columns: wave w loads rows 8w + 2q + L/32 (q = 0..3)
+    // of each step, lane L at position L%32.
     uint32_t aoff[8], boff[4];
+    const int crow = 8 * w + (lane >> 5);  // of the first load; the others 2 rows on each
+    const auto chunk_of = [&](int row) { return (lane & 31) ^ (2 * ((row & 3) ^ ((row & 1) << 2))); };
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
       const int row = 64 * w + 8 * q + (lane >> 3);
       const int c = (lane & 7) ^ ((row >> 1) & 7);
       const int64_t ar = m0 + row < M ? row : M - 1 - m0;
-      aoff[q] = (uint32_t)(ar * p.lda * 2 + 16 * c);
+      if constexpr (!kACols)
+        aoff[q] = (uint32_t)(ar * p.lda * 2 + 16 * c);
+      else if (q < 4)
+        aoff[q] = (uint32_t)((crow + 2 * q) * p.lda * 2 + 16 * chunk_of(crow + 2 * q));
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int row = 16 * (4 * w + j) + (lane >> 2);
       const int c = (lane & 3) ^ ((row >> 2) & 3);
-      boff[j] = (uint32_t)(row * 64 + 16 * c);
+      if constexpr (kBCols)
+        boff[j] = (uint32_t)((crow + 2 * j) * p.ldb * 2 + 16 * chunk_of(crow + 2 * j));
+      else
+        boff[j] = (uint32_t)(row * 64 + 16 * c);
     }
-    // a ends with its last row's last step: what a final odd pair has past it
-    // in that row reads zeros (in other rows the next row; it is not used).
+    // rows: a ends with its last row's last step; what a final odd pair has past
+    // it in that row reads zeros (in other rows the next row; it is not used).
     const int64_t a_bytes = min(((M - 1 - m0) * p.lda + (int64_t)(all - ks0) * kStep) * 2, (int64_t)0x7FFFFFFF);
     const __amdgpu_buffer_rsrc_t ares = __builtin_amdgcn_make_buffer_rsrc(
         (void*)uniform_ptr(p.a + m0 * p.lda + k0), (short)0, (int)a_bytes, 0x00020000);
     const __amdgpu_buffer_rsrc_t bres = __builtin_amdgcn_make_buffer_rsrc(
         (void*)uniform_ptr(p.b + (int64_t)tn * p.b_steps * kOp), (short)0, (int)0x7FFFFFFF, 0x00020000);
-    typedef __attribute__((address_space(3))) void lds_void;
-    auto dma_a = [&](int q, int pair, uint16_t* slot) {
+    // columns: the rows of step ks, 32 of them, as a buffer that ends with the
+    // matrix (a step may pass its last row: zeros).
+    const auto rows_of = [&](const uint16_t* m, int64_t ld, int64_t col, int64_t rows, int64_t width, int ks) {
+      const int64_t r = (int64_t)ks * kStep;
+      const int64_t left = ((rows - 1 - r) * ld + width - col) * 2;
+      const int size = left < 0 || r >= rows ? 0 : left > 0x7FFFFFFF ? 0x7FFFFFFF : (int)left;
+      return Window{uniform_ptr(m + r * ld + col), size};
+    };
+    const auto dma_cols = [&](const Window& from, uint32_t off, int q, uint16_t* stage) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          __builtin_amdgcn_make_buffer_rsrc((void*)from.p, (short)0, from.size, 0x00020000),
+          (lds_void*)(stage + (8 * w + 2 * q) * kTile), 16, off, 0, 0, 0);
+    };
+    const auto step_at = [&](int kb) {  // the step of the whole product
+      return ks0 + (kb < nsteps ? kb : nsteps - 1);
+    };
+    const auto dma_a_rows = [&](int q, int pair, uint16_t* slot) {
       const int ps = pair < npairs ? pair : npairs - 1;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void*)(slot + (64 * w + 8 * q) * 64), 16,
                                                aoff[q], 128 * ps, 0, 0);
     };
-    auto dma_b = [&](int j, int kb, uint16_t* stage) {
-      int ks = ks0 + (kb < nsteps ? kb : nsteps - 1);
-      if (kMode == kDx || kMode == kDw) ks -= ks >= half ? half : 0;  // the second term's
+    const auto from_a = [&](int kb) {  // the second term lies a plane on
+      const int ks = step_at(kb), term = ks >= half;
+      return rows_of(p.a + term * p.a_plane, p.lda, m0, p.rows_pad, p.lda, ks - term * half);
+    };
+    const auto dma_b_steps = [&](int j, int kb, uint16_t* stage) {
+      const int ks = step_at(kb);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(bres, (lds_void*)(stage + 512 * (4 * w + j)), 16,
                                                boff[j], kOp * 2 * ks, 0, 0);
     };
-    // Fragment reads: A fragment (mt, step half par, substep s): tile row
+    const int64_t b_rows = kMode == kDx ? p.vocab_left : p.rows_pad;
+    const auto from_b = [&](int kb) {
+      const int ks = step_at(kb);
+      return rows_of(p.b, p.ldb, n0, b_rows, p.b_width, ks >= half ? ks - half : ks);
+    };
+    // Fragment reads. rows: fragment (mt, step half par, substep s) is tile row
     // 128wm + 32mt + i, chunk 4par + 2s + h, at position chunk ^ ((i >> 1) & 7).
-    // B fragment (nt, s): tile row 128wn + 32nt + i, chunk 2s + h at (2s + h) ^
-    // ((i >> 2) & 3).
+    // steps: (nt, s) is tile row 128wn + 32nt + i, chunk 2s + h at (2s + h) ^
+    // ((i >> 2) & 3). columns: lane 16q + l reads rows 16s + 8(q/2) + l/4 (and 4
+    // on), 8 bytes at columns 128wn + 32nt + 16(q%2) + 4(l%4).
     const int swa = (i >> 1) & 7, swb = (i >> 2) & 3;
     int fa[2][2];
 #pragma unroll
@@ -314,44 +372,86 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         fa[par][ss] = (128 * wm + i) * 64 + 8 * ((4 * par + 2 * ss + h) ^ swa);
     const int fb0 = (128 * wn + i) * 32 + 8 * (h ^ swb);
     const int fb1 = (128 * wn + i) * 32 + 8 * ((2 + h) ^ swb);
+    const int trow = 8 * h + ((lane >> 2) & 3), tg = 2 * ((trow & 3) ^ ((trow & 1) << 2));
+    int ca[4], cb[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int c = 4 * t + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+      ca[t] = trow * kTile + 8 * ((16 * wm + c) ^ tg) + 4 * (lane & 1);
+      cb[t] = trow * kTile + 8 * ((16 * wn + c) ^ tg) + 4 * (lane & 1);
+    }
+    const auto frag_a = [&](const uint16_t* s, int t, int par, int ss) {
+      if constexpr (kACols)
+        return read_columns(s + ca[t] + 16 * ss * kTile);
+      else
+        return *reinterpret_cast<const u32x4_t*>(s + fa[par][ss] + 2048 * t);
+    };
+    const auto frag_b = [&](const uint16_t* s, int t, int ss) {
+      if constexpr (kBCols)
+        return read_columns(s + cb[t] + 16 * ss * kTile);
+      else
+        return *reinterpret_cast<const u32x4_t*>(s + (ss ? fb1 : fb0) + 1024 * t);
+    };
 
-    // Prologue: pair 0, steps 0 and 1 of b, pair 1, step 2 of b; wait for the
-    // first three, all that steps 0 and 1 read before the loop's first barrier.
+    // Prologue: what steps 0 and 1 read, then a's pair 1 or step 2 and b's step
+    // 2; wait for the former.
+    const auto load_a = [&](int n, uint16_t* s) {  // pair or step n
+      if constexpr (kACols) {
+        const Window from = from_a(n);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dma_a(q, 0, sa0);
+        for (int q = 0; q < 4; ++q) dma_cols(from, aoff[q], q, s);
+      } else {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dma_b(j, 0, sb0);
+        for (int q = 0; q < 8; ++q) dma_a_rows(q, n, s);
+      }
+    };
+    const auto load_b = [&](int kb, uint16_t* stage) {
+      if constexpr (kBCols) {
+        const Window from = from_b(kb);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) dma_b(j, 1, sb1);
+        for (int j = 0; j < 4; ++j) dma_cols(from, boff[j], j, stage);
+      } else {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) dma_a(q, 1, sa1);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) dma_b(j, 2, sb2);
-    wait_vmem_lgkm0<12>();
+        for (int j = 0; j < 4; ++j) dma_b_steps(j, kb, stage);
+      }
+    };
+    load_a(0, sa0);
+    if constexpr (kACols) load_a(1, sa1);
+    load_b(0, sb0);
+    load_b(1, sb1);
+    load_a(kACols ? 2 : 1, kACols ? sa2 : sa1);
+    load_b(2, sb2);
+    wait_vmem_lgkm0<kACols ? 8 : 12>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
     u32x4_t a0[4], b0[4], a1[4], b1[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      a0[t] = *reinterpret_cast<const u32x4_t*>(&sa0[fa[0][0] + 2048 * t]);
-      b0[t] = *reinterpret_cast<const u32x4_t*>(&sb0[fb0 + 1024 * t]);
+      a0[t] = frag_a(sa0, t, 0, 0);
+      b0[t] = frag_b(sb0, t, 0);
     }
-    // One step kb (b stage kb % 4 = SB, a slot (kb / 2) % 3 = SA, half PAR):
+    constexpr int kAReads = kACols ? 2 : 1, kBReads = kBCols ? 2 : 1;
+    // One step kb (stage kb % 4 = SB, pair slot (kb / 2) % 3 = SA, half PAR):
     // substep 0 computes on (a0, b0) while (kb, 1) is read into (a1, b1);
     // substep 1 computes on (a1, b1) while (kb+1, 0) is read into (a0, b0). One
-    // load after every fourth MFMA: b of step kb+3 in substep 0, four a loads of
-    // pair kb/2 + 2 in substep 1.
+    // load after every fourth MFMA: b of step kb+3 in substep 0, a of pair kb/2 + 2
+    // or of step kb+3 in substep 1.
     auto step = [&](int kb, auto sbc, auto sac, auto parc) {
       constexpr int SB = decltype(sbc)::value, SA = decltype(sac)::value;
       constexpr int PAR = decltype(parc)::value;
       constexpr int SA1 = PAR ? (SA + 1) % 3 : SA;  // slot of step kb+1
       constexpr int PAR1 = PAR ^ 1;
-      uint16_t* const acur = pick<SA>(sa);
-      uint16_t* const anxt = pick<SA1>(sa);
-      uint16_t* const ald = pick<(SA + 2) % 3>(sa);
+      constexpr int kACur = kACols ? SB : SA, kANxt = kACols ? (SB + 1) % 4 : SA1;
+      constexpr int kALd = kACols ? (SB + 3) % 4 : (SA + 2) % 3;
+      uint16_t* const acur = pick<kACur>(sa);
+      uint16_t* const anxt = pick<kANxt>(sa);
+      uint16_t* const ald = pick<kALd>(sa);
       uint16_t* const bcur = pick<SB>(sb);
       uint16_t* const bnxt = pick<(SB + 1) % 4>(sb);
       uint16_t* const bld = pick<(SB + 3) % 4>(sb);
+      Window bnew{nullptr, 0}, anew{nullptr, 0};
+      if constexpr (kBCols) bnew = from_b(kb + 3);
+      if constexpr (kACols) anew = from_a(kb + 3);
 #pragma unroll
       for (int g = 0; g < 16; ++g) {
         const int mt = g >> 2, nt = g & 3;
@@ -359,14 +459,19 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         if (g < 8) {
           const int t = g >> 1;
-          if (g & 1)
-            b1[t] = *reinterpret_cast<const u32x4_t*>(&bcur[fb1 + 1024 * t]);
-          else
-            a1[t] = *reinterpret_cast<const u32x4_t*>(&acur[fa[PAR][1] + 2048 * t]);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          if (g & 1) {
+            b1[t] = frag_b(bcur, t, 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, kBReads, 0);
+          } else {
+            a1[t] = frag_a(acur, t, PAR, 1);
+            __builtin_amdgcn_sched_group_barrier(0x100, kAReads, 0);
+          }
         }
         if ((g & 3) == 3) {
-          dma_b(g >> 2, kb + 3, bld);
+          if constexpr (kBCols)
+            dma_cols(bnew, boff[g >> 2], g >> 2, bld);
+          else
+            dma_b_steps(g >> 2, kb + 3, bld);
           __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
       }
@@ -378,14 +483,19 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
         if (g < 8) {
           const int t = g >> 1;
-          if (g & 1)
-            b0[t] = *reinterpret_cast<const u32x4_t*>(&bnxt[fb0 + 1024 * t]);
-          else
-            a0[t] = *reinterpret_cast<const u32x4_t*>(&anxt[fa[PAR1][0] + 2048 * t]);
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          if (g & 1) {
+            b0[t] = frag_b(bnxt, t, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kBReads, 0);
+          } else {
+            a0[t] = frag_a(anxt, t, PAR1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kAReads, 0);
+          }
         }
         if ((g & 3) == 3) {
-          dma_a(4 * PAR + (g >> 2), kb / 2 + 2, ald);
+          if constexpr (kACols)
+            dma_cols(anew, aoff[g >> 2], g >> 2, ald);
+          else
+            dma_a_rows(4 * PAR + (g >> 2), kb / 2 + 2, ald);
           __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
         }
       }
@@ -399,6 +509,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     using I1 = std::integral_constant<int, 1>;
     using I2 = std::integral_constant<int, 2>;
     using I3 = std::integral_constant<int, 3>;
+    // Twelve steps bring all rings back to their first stage and slot.
     int kb = 0;
     for (; kb + 12 <= nsteps; kb += 12) {
       step(kb + 0, I0(), I0(), I0());
@@ -480,6 +591,8 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
       p.part[(p.v0 / kTile + tm) * p.rows_pad + n0 + tid] = float2{m, s};
     }
   } else if constexpr (kMode == kProbs) {
+    // Whole pairs of steps of what the products reduce over are written: along
+    // the vocabulary for P, along the live rows for Q.
     const int64_t phalf = whole_pairs(p.vocab), qhalf = whole_pairs(live);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
@@ -494,33 +607,35 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
           const int64_t v = mw + 32 * mt + 8 * g;
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            pr[e] = v + e < M && c.label >= 0 ? exp2_fast(fmaf(acc[mt][nt][4 * g + e], p.scale, -c.most) * kLog2e) * c.over
-                              : 0.0f;
-          if (p.P && n < N && v < phalf) {
-            const u32x2_t hi = {pack_bf16x2(pr[0], pr[1]), pack_bf16x2(pr[2], pr[3])};
-            uint16_t* to = p.P + n * p.ldp + v;
-            *reinterpret_cast<u32x2_t*>(to) = hi;
-            if (p.p_terms == 2)
-              *reinterpret_cast<u32x2_t*>(to + phalf) =
-                  u32x2_t{pack_bf16x2(pr[0] - bf16_lo(hi[0]), pr[1] - bf16_hi(hi[0])),
-                          pack_bf16x2(pr[2] - bf16_lo(hi[1]), pr[3] - bf16_hi(hi[1]))};
-          }
+            pr[e] = v + e < M && c.label >= 0
+                        ? exp2_fast(fmaf(acc[mt][nt][4 * g + e], p.scale, -c.most) * kLog2e) * c.over
+                        : 0.0f;
+          if (p.P && n < N && v < phalf)
+            store_terms(p.P + n * p.ldp + v, phalf, p.p_terms, pr);
           if (p.Q && n < qhalf) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if (v + e >= M) continue;
-              const float q = (pr[e] - (d == 32 * mt + 8 * g + e ? 1.0f : 0.0f)) * c.factor;
-              const uint32_t hi = pack_bf16x2(q, 0.0f);
-              uint16_t* to = p.Q + (v + e) * p.ldq + n;
-              *to = (uint16_t)hi;
-              if (p.q_terms == 2) to[qhalf] = (uint16_t)pack_bf16x2(q - bf16_lo(hi), 0.0f);
-            }
+            for (int e = 0; e < 4; ++e) pr[e] = (pr[e] - (d == 32 * mt + 8 * g + e ? 1.0f : 0.0f)) * c.factor;
+            store_terms(p.Q + n * p.ldq + v, p.q_plane, p.q_terms, pr);
           }
         }
     }
+  } else if constexpr (kMode == kDx) {
+    // The sums in the order of the registers, 16 bytes a thread: tile by tile,
+    // split by split.
+    float* to = p.acc + ((int64_t)split * tiles + tm * tiles_n + tn) * (kTile * kTile) + 4 * tid;
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4_t* o = reinterpret_cast<f32x4_t*>(to + ((mt * 4 + nt) * 4 + g) * 1024);
+          f32x4_t v = {acc[mt][nt][4 * g], acc[mt][nt][4 * g + 1], acc[mt][nt][4 * g + 2],
+                       acc[mt][nt][4 * g + 3]};
+          if (p.add) v += *o;
+          *o = v;
+        }
   } else {
-    const int64_t ldo = p.K;
-    float* to = kMode == kDx ? p.acc + (int64_t)split * tiles_m * kTile * ldo : nullptr;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       const int64_t n = nw + 32 * nt;
@@ -531,22 +646,16 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         for (int e = 0; e < 16; ++e) {
           const int64_t m = mw + 32 * mt + 8 * (e >> 2) + (e & 3);
           if (m >= M) continue;
-          if constexpr (kMode == kDx) {
-            float v = acc[mt][nt][e];
-            if (p.add) v += to[m * ldo + n];
-            to[m * ldo + n] = v;
+          const int64_t at = (p.v0 + m) * p.K + n;
+          float v = acc[mt][nt][e];
+          if (p.dw_bf16) {
+            uint16_t* o = static_cast<uint16_t*>(p.dW) + at;
+            if (p.accumulate) v += bf16_lo(*o);
+            store1<true>(o, v);
           } else {
-            const int64_t at = (p.v0 + m) * ldo + n;
-            float v = acc[mt][nt][e];
-            if (p.dw_bf16) {
-              uint16_t* o = static_cast<uint16_t*>(p.dW) + at;
-              if (p.accumulate) v += bf16_lo(*o);
-              store1<true>(o, v);
-            } else {
-              float* o = static_cast<float*>(p.dW) + at;
-              if (p.accumulate) v += *o;
-              *o = v;
-            }
+            float* o = static_cast<float*>(p.dW) + at;
+            if (p.accumulate) v += *o;
+            *o = v;
           }
         }
     }
@@ -592,42 +701,48 @@ __global__ __launch_bounds__(256) void head_loss_kernel(const float2* part, int6
   }
 }
 
-// A thread takes 8 columns of a row.
+// Four rows a workgroup, two columns a thread: of live rows 4y .. 4y + 3 in the
+// first half of the grid, whose sums lie as head_tile_kernel's registers had
+// them, and of rows that carry no loss in the second half.
 template <bool kBf16>
 __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
-  constexpr int E = 8;
-  const int64_t vecs = (a.K + E - 1) / E, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t row = at / vecs, k = (at - row * vecs) * E;
-  if (row >= a.M) return;
-  const int n = count_below<E>(k, a.K);
-  const int32_t j = a.inv[row];
-  float v[E];
-#pragma unroll
-  for (int e = 0; e < E; ++e) v[e] = 0.0f;
-  if (j >= 0) {
-    const int tiles_m = ceil_tile(*a.count);
-    const int splits = dx_splits(tiles_m * ceil_tile(a.K), a.steps);
-    const HeadColumn c = a.cols[j];
-    const float* from = a.acc + (int64_t)j * a.K + k;
-    for (int s = 0; s < splits; ++s, from += (int64_t)tiles_m * kTile * a.K) {
-      const Vec<false, E> r = n == E ? load_vec<false, E>(from) : load_part<false, E>(from, n);
-      float o[E];
-      to_float<false, E>(r, o);
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[e] += o[e];
-    }
-    const uint16_t* w = a.W + (int64_t)c.label * a.ldw + k;
-    const Vec<true, E> r = n == E ? load_vec<true, E>(w) : load_part<true, E>(w, n);
-    float o[E];
-    to_float<true, E>(r, o);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = (v[e] - o[e]) * c.factor;
+  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+  if (k >= a.K) return;
+  const bool two = k + 1 < a.K;
+  const auto put = [&](int64_t row, float x, float y) {
+    elem_t<kBf16>* to = static_cast<elem_t<kBf16>*>(a.dX) + row * a.lddx + k;
+    store1<kBf16>(to, x);
+    if (two) store1<kBf16>(to + 1, y);
+  };
+  const int64_t groups = (a.M + 3) / 4;
+  if ((int64_t)blockIdx.y >= groups) {
+    const int64_t m = ((int64_t)blockIdx.y - groups) * 4;
+    for (int e = 0; e < 4; ++e)
+      if (m + e < a.M && a.inv[m + e] < 0) put(m + e, 0.0f, 0.0f);
+    return;
   }
-  elem_t<kBf16>* to = static_cast<elem_t<kBf16>*>(a.dX) + row * a.lddx + k;
-  if (n == E)
-    store_vec<kBf16, E>(to, v);
-  else
-    store_part<kBf16, E>(to, v, n);
+  const int live = *a.count;
+  const int j = (int)blockIdx.y * 4;
+  if (j >= live) return;
+  const int tiles_n = ceil_tile(a.K), tiles = ceil_tile(live) * tiles_n;
+  const int splits = dx_splits(tiles, a.pairs);
+  const int r = j % kTile, c = (int)(k % kTile);
+  const int tid = ((r / 128) * 2 + c / 128) * 64 + ((r / 4) % 2) * 32 + c % 32;
+  const int reg = ((r % 128 / 32) * 4 + c % 128 / 32) * 4 + r % 32 / 8;
+  const float* from = a.acc + ((int64_t)(j / kTile) * tiles_n + k / kTile) * (kTile * kTile) + reg * 1024 + 4 * tid;
+  f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+  for (int s = 0; s < splits; ++s, from += (int64_t)tiles * (kTile * kTile)) {
+    x += *reinterpret_cast<const f32x4_t*>(from);
+    y += *reinterpret_cast<const f32x4_t*>(from + 4);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (j + e >= live) break;
+    const HeadColumn col = a.cols[j + e];
+    const uint16_t* w = a.W + (int64_t)col.label * a.ldw + k;
+    put(a.map[j + e], (x[e] - bf16_lo(w[0])) * col.factor,
+        (y[e] - (two ? bf16_lo(w[1]) : 0.0f)) * col.factor);
+  }
 }
 
 unsigned blocks_of(int64_t n) { return (unsigned)((n + 255) / 256); }
@@ -655,19 +770,12 @@ hipError_t launch_head_pack_rows(const uint16_t* src, int64_t ld, const int32_t*
   return hipGetLastError();
 }
 
-hipError_t launch_head_pack_cols(const uint16_t* src, int64_t ld, const int32_t* map,
-                                 const int32_t* count, int64_t rows, int64_t K, int64_t steps,
-                                 uint16_t* out, hipStream_t st) {
-  const int64_t used = (rows + 2 * kStep - 1) / (2 * kStep) * 2;
-  hipLaunchKernelGGL(head_pack_cols_kernel, dim3((unsigned)tiles_of(K), (unsigned)used), dim3(256), 0,
-                     st, src, ld, map, count, rows, K, steps, out);
-  return hipGetLastError();
-}
-
-hipError_t launch_head_pad(const uint16_t* src, int64_t ld, int64_t rows, int64_t K, int64_t Kp,
-                           uint16_t* out, hipStream_t st) {
-  hipLaunchKernelGGL(head_pad_kernel, dim3(blocks_of(rows * (Kp / 8))), dim3(256), 0, st, src, ld,
-                     rows, K, Kp, out);
+hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
+                            const int32_t* count, int64_t rows, int64_t K, int64_t Kp, uint16_t* out,
+                            hipStream_t st) {
+  const int64_t most = count ? (rows + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
+  hipLaunchKernelGGL(head_copy_kernel, dim3(blocks_of(most * (Kp / 8))), dim3(256), 0, st, src, ld,
+                     map, count, rows, K, Kp, out);
   return hipGetLastError();
 }
 
@@ -680,8 +788,7 @@ hipError_t launch_head_probs(const HeadTiles& a, hipStream_t st) {
 }
 
 hipError_t launch_head_dx(const HeadTiles& a, hipStream_t st) {
-  const int64_t grid = tiles_of(a.rows_most) * tiles_of(a.K);
-  return tiles<kDx>(a, grid > 256 ? grid : 256, st);
+  return tiles<kDx>(a, head_sums(a.rows_most, a.K), st);
 }
 
 hipError_t launch_head_dw(const HeadTiles& a, hipStream_t st) {
@@ -697,7 +804,7 @@ hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
 }
 
 hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st) {
-  const dim3 grid(blocks_of(a.M * ((a.K + 7) / 8)));
+  const dim3 grid(blocks_of((a.K + 1) / 2), (unsigned)((a.M + 3) / 4 * 2));
   if (bf16)
     hipLaunchKernelGGL(head_dx_finish_kernel<true>, grid, dim3(256), 0, st, a);
   else

@@ -34,7 +34,7 @@ int64_t copy_rows(int64_t V, int64_t Kp) {
 struct Layout {
   int64_t rows_pad = 0, Kp = 0, piece = 0;
   size_t map = 0, inv = 0, count = 0, cols = 0, xs = 0, at_label = 0, part = 0, copy = 0;
-  size_t P = 0, Q = 0, Wt = 0, xt = 0, acc = 0, total = 0;
+  size_t P = 0, Q = 0, xr = 0, acc = 0, total = 0;
 };
 
 void rows_layout(Layout& L, Carve& c, int64_t M, int64_t K) {
@@ -78,16 +78,14 @@ Layout bwd_layout(int64_t M, int64_t V, int64_t K, bool copy, int dx, int dw) {
   Carve c;
   rows_layout(L, c, M, K);
   L.piece = piece_of(M, V);
-  const size_t k_tiles = (size_t)up(K, kTile);
   if (copy) L.copy = c.take((size_t)L.piece * L.Kp * 2);
   if (dx >= 0) {
     L.P = c.take((size_t)L.rows_pad * L.piece * terms(dx) * 2);
-    L.Wt = c.take(k_tiles * L.piece * 2);
-    L.acc = c.take((size_t)head_acc_floats(L.rows_pad, K) * 4);
+    L.acc = c.take((size_t)head_sums(M, K) * kTile * kTile * 4);
   }
   if (dw >= 0) {
     L.Q = c.take((size_t)L.rows_pad * L.piece * terms(dw) * 2);
-    L.xt = c.take(k_tiles * L.rows_pad * 2);
+    L.xr = c.take((size_t)L.rows_pad * L.Kp * 2);
   }
   L.total = c.off;
   return L;
@@ -160,7 +158,7 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     t.lda = ldw;
     if (copy) {
       uint16_t* Wc = at<uint16_t>(workspace, L.copy);
-      e = launch_head_pad(t.a, ldw, t.vocab, K, L.Kp, Wc, st);
+      e = launch_head_copy(t.a, ldw, nullptr, nullptr, t.vocab, K, L.Kp, Wc, st);
       t.a = Wc;
       t.lda = L.Kp;
     }
@@ -223,12 +221,11 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   r.count = at<int32_t>(workspace, L.count);
   r.cols = at<HeadColumn>(workspace, L.cols);
   uint16_t* xs = at<uint16_t>(workspace, L.xs);
-  uint16_t* xt = at<uint16_t>(workspace, L.xt);
-  uint16_t* Wt = at<uint16_t>(workspace, L.Wt);
+  uint16_t* xr = at<uint16_t>(workspace, L.xr);
   hipError_t e = launch_head_rows(r, st);
   if (e == hipSuccess) e = launch_head_pack_rows(x, ldx, r.map, r.count, M, K, xs, st);
   if (e == hipSuccess && dW)
-    e = launch_head_pack_cols(x, ldx, r.map, r.count, M, K, L.rows_pad / kStep, xt, st);
+    e = launch_head_copy(x, ldx, r.map, r.count, M, K, L.Kp, xr, st);
   HeadTiles t{};
   t.count = r.count;
   t.rows_most = M;
@@ -240,7 +237,9 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   t.p_terms = dX ? terms(dx_dtype) : 0;
   t.q_terms = dW ? terms(grad_dtype) : 0;
   t.ldp = L.piece * t.p_terms;
-  t.ldq = L.rows_pad * t.q_terms;
+  t.ldq = L.piece;
+  t.q_plane = L.rows_pad * L.piece;
+  t.pairs = (int)(up(V < L.piece ? V : L.piece, 2 * kStep) / (2 * kStep) * t.p_terms);
   t.acc = at<float>(workspace, L.acc);
   t.dW = dW;
   t.dw_bf16 = grad_dtype == QLORA_DTYPE_BF16;
@@ -248,41 +247,42 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   for (int64_t v0 = 0; v0 < V && e == hipSuccess; v0 += L.piece) {
     t.v0 = v0;
     t.vocab = V - v0 < L.piece ? V - v0 : L.piece;
-    const uint16_t* Wv = W + v0 * ldw;
-    t.a = Wv;
-    t.lda = ldw;
+    const uint16_t* Wv = W + v0 * ldw;  // the piece's rows, as the kernels read them
+    int64_t ldv = ldw;
     if (copy) {
       uint16_t* Wc = at<uint16_t>(workspace, L.copy);
-      e = launch_head_pad(Wv, ldw, t.vocab, K, L.Kp, Wc, st);
-      t.a = Wc;
-      t.lda = L.Kp;
+      e = launch_head_copy(Wv, ldw, nullptr, nullptr, t.vocab, K, L.Kp, Wc, st);
+      Wv = Wc;
+      ldv = L.Kp;
     }
+    t.a = Wv;
+    t.lda = ldv;
     t.b = xs;
     t.b_steps = t.steps;
     t.P = dX ? at<uint16_t>(workspace, L.P) : nullptr;
     t.Q = dW ? at<uint16_t>(workspace, L.Q) : nullptr;
     if (e == hipSuccess) e = launch_head_probs(t, st);
     if (e == hipSuccess && dX) {
-      e = launch_head_pack_cols(Wv, ldw, nullptr, nullptr, t.vocab, K, L.piece / kStep, Wt, st);
       t.a = t.P;
       t.lda = t.ldp;
-      t.b = Wt;
-      t.b_steps = L.piece / kStep;
+      t.b = Wv;
+      t.ldb = ldv;
+      t.b_width = copy ? ldv : K;
+      t.vocab_left = copy ? t.vocab : V - v0;
       t.add = v0 > 0;
-      if (e == hipSuccess) e = launch_head_dx(t, st);
+      e = launch_head_dx(t, st);
     }
     if (e == hipSuccess && dW) {
       t.a = t.Q;
       t.lda = t.ldq;
-      t.b = xt;
-      t.b_steps = L.rows_pad / kStep;
+      t.a_plane = t.q_plane;
+      t.b = xr;
+      t.ldb = t.b_width = L.Kp;
       e = launch_head_dw(t, st);
     }
   }
   if (e == hipSuccess && dX) {
-    const int64_t first = V < L.piece ? V : L.piece;
-    const HeadDx d{t.acc, (int)(up(first, 2 * kStep) / kStep * t.p_terms), r.inv, r.count, r.cols,
-                   W, ldw, M, K, dX, lddx};
+    const HeadDx d{t.acc, t.pairs, r.map, r.inv, r.count, r.cols, W, ldw, M, K, dX, lddx};
     e = launch_head_dx_finish(d, dx_dtype == QLORA_DTYPE_BF16, st);
   }
   return launch_status(e);
