@@ -100,6 +100,39 @@ inline int64_t head_sums(int64_t rows_most, int64_t K) {
   return tiles > split ? tiles : split;
 }
 
+// The logits of at most kFewRows rows, one pass over W at any row stride and
+// alignment. Statistics: of rows j themselves, joined over 128 entries of the
+// vocabulary: part[row][parts]. Probabilities: of live rows, as
+// launch_head_probs leaves them; p_plane: elements of P to the second term.
+constexpr int64_t kFewRows = 64;
+constexpr int64_t kFewEntries = 128;
+struct HeadFew {
+  const uint16_t* W;  // the piece's rows
+  int64_t ldw;
+  const uint16_t* x;
+  int64_t ldx, M, K, v0, vocab;
+  float scale;
+  const void* labels;
+  bool ids64;
+  float2* part;
+  int64_t parts;
+  float* at_label;
+  const int32_t* map;
+  const int32_t* count;
+  const HeadColumn* cols;
+  uint16_t* P;
+  int64_t ldp, p_plane;
+  int p_terms;
+  uint16_t* Q;
+  int64_t ldq, q_plane;
+  int q_terms;
+};
+hipError_t launch_head_few_stats(const HeadFew& a, hipStream_t st);
+hipError_t launch_head_few_probs(const HeadFew& a, hipStream_t st);
+hipError_t launch_head_few_loss(const float2* part, int64_t parts, const float* at_label,
+                                const void* labels, bool ids64, int64_t M, int64_t V, float* loss,
+                                float* stats, hipStream_t st);
+
 // loss and stats (may be NULL) of all M rows from the partial statistics.
 hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
                             const float* at_label, const int32_t* inv, int64_t M, float* loss,

@@ -33,8 +33,7 @@
 // pairs of steps, b in a ring of four steps.
 #include <type_traits>
 
-#include "head.h"
-#include "rows.h"
+#include "head_terms.h"
 
 namespace qlora {
 namespace {
@@ -155,16 +154,6 @@ __device__ __forceinline__ void tile_of(int t, int tiles_m, int tiles_n, int& tm
   const int in = t - group * kGroup * tiles_n;
   tm = first + in % rows;
   tn = in / rows;
-}
-
-// Four values in bf16, and with two terms what they lost, `plane` elements on.
-__device__ __forceinline__ void store_terms(uint16_t* to, int64_t plane, int terms, const float (&v)[4]) {
-  const u32x2_t hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  *reinterpret_cast<u32x2_t*>(to) = hi;
-  if (terms == 2)
-    *reinterpret_cast<u32x2_t*>(to + plane) =
-        u32x2_t{pack_bf16x2(v[0] - bf16_lo(hi[0]), v[1] - bf16_hi(hi[0])),
-                pack_bf16x2(v[2] - bf16_lo(hi[1]), v[3] - bf16_hi(hi[1]))};
 }
 
 // At most n vector-memory operations in flight, no LDS operation.
@@ -624,7 +613,8 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     // split by split.
     float* to = p.acc + ((int64_t)split * tiles + tm * tiles_n + tn) * (kTile * kTile) + 4 * tid;
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int mt = 0; mt < 4; ++mt) {
+      if (m0 + 128 * wm + 32 * mt >= M) continue;  // no live row in these 32
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
@@ -635,6 +625,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
           if (p.add) v += *o;
           *o = v;
         }
+    }
   } else {
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
@@ -731,6 +722,7 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
   const int reg = ((r % 128 / 32) * 4 + c % 128 / 32) * 4 + r % 32 / 8;
   const float* from = a.acc + ((int64_t)(j / kTile) * tiles_n + k / kTile) * (kTile * kTile) + reg * 1024 + 4 * tid;
   f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+#pragma unroll 4
   for (int s = 0; s < splits; ++s, from += (int64_t)tiles * (kTile * kTile)) {
     x += *reinterpret_cast<const f32x4_t*>(from);
     y += *reinterpret_cast<const f32x4_t*>(from + 4);

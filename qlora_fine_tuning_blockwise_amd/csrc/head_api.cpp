@@ -47,10 +47,18 @@ void rows_layout(Layout& L, Carve& c, int64_t M, int64_t K) {
   L.xs = c.take((size_t)L.rows_pad * L.Kp * 2);
 }
 
+int64_t few_parts(int64_t V) { return (V + kFewEntries - 1) / kFewEntries; }
+
 Layout fwd_layout(int64_t M, int64_t V, int64_t K, bool copy) {
   Layout L;
   if (M == 0) return L;
   Carve c;
+  if (M <= kFewRows) {  // one pass over W where it lies
+    L.at_label = c.take((size_t)M * 4);
+    L.part = c.take((size_t)few_parts(V) * M * sizeof(float2));
+    L.total = c.off;
+    return L;
+  }
   rows_layout(L, c, M, K);
   L.at_label = c.take((size_t)L.rows_pad * 4);
   L.part = c.take((size_t)(up(V, kTile) / kTile) * L.rows_pad * sizeof(float2));
@@ -61,10 +69,11 @@ Layout fwd_layout(int64_t M, int64_t V, int64_t K, bool copy) {
 }
 
 // Entries of the vocabulary in a piece of the backward: 2^26 probabilities (128
-// MB of bf16) at 2048 to 32768 entries, all pieces alike.
-int64_t piece_of(int64_t M, int64_t V) {
+// MB of bf16), 2048 entries at least, all pieces alike; where W is copied 32768 of
+// its rows at most.
+int64_t piece_of(int64_t M, int64_t V, bool copy) {
   int64_t n = ((int64_t)1 << 26) / up(M, kTile) / kTile * kTile;
-  n = n < 2048 ? 2048 : n > 32768 ? 32768 : n;
+  n = n < 2048 ? 2048 : n > 32768 && copy ? 32768 : n;
   const int64_t pieces = (V + n - 1) / n;
   return up((V + pieces - 1) / pieces, kTile);
 }
@@ -77,7 +86,7 @@ Layout bwd_layout(int64_t M, int64_t V, int64_t K, bool copy, int dx, int dw) {
   if (M == 0) return L;
   Carve c;
   rows_layout(L, c, M, K);
-  L.piece = piece_of(M, V);
+  L.piece = piece_of(M, V, copy);
   if (copy) L.copy = c.take((size_t)L.piece * L.Kp * 2);
   if (dx >= 0) {
     L.P = c.take((size_t)L.rows_pad * L.piece * terms(dx) * 2);
@@ -124,6 +133,26 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
                 array(labels, M, ids_dtype)}))
     return QLORA_ERR_INVALID_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (M <= kFewRows) {
+    HeadFew f{};
+    f.W = W;
+    f.ldw = ldw;
+    f.x = x;
+    f.ldx = ldx;
+    f.M = M;
+    f.K = K;
+    f.vocab = V;
+    f.scale = scale;
+    f.labels = labels;
+    f.ids64 = ids_dtype == QLORA_DTYPE_I64;
+    f.part = at<float2>(workspace, L.part);
+    f.parts = few_parts(V);
+    f.at_label = at<float>(workspace, L.at_label);
+    hipError_t e = launch_head_few_stats(f, st);
+    if (e == hipSuccess)
+      e = launch_head_few_loss(f.part, f.parts, f.at_label, labels, f.ids64, M, V, loss, stats, st);
+    return launch_status(e);
+  }
   HeadRows r{};
   r.labels = labels;
   r.ids64 = ids_dtype == QLORA_DTYPE_I64;
@@ -223,7 +252,8 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   uint16_t* xs = at<uint16_t>(workspace, L.xs);
   uint16_t* xr = at<uint16_t>(workspace, L.xr);
   hipError_t e = launch_head_rows(r, st);
-  if (e == hipSuccess) e = launch_head_pack_rows(x, ldx, r.map, r.count, M, K, xs, st);
+  const bool few = M <= kFewRows;
+  if (e == hipSuccess && !few) e = launch_head_pack_rows(x, ldx, r.map, r.count, M, K, xs, st);
   if (e == hipSuccess && dW)
     e = launch_head_copy(x, ldx, r.map, r.count, M, K, L.Kp, xr, st);
   HeadTiles t{};
@@ -261,7 +291,32 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     t.b_steps = t.steps;
     t.P = dX ? at<uint16_t>(workspace, L.P) : nullptr;
     t.Q = dW ? at<uint16_t>(workspace, L.Q) : nullptr;
-    if (e == hipSuccess) e = launch_head_probs(t, st);
+    if (e == hipSuccess && few) {
+      HeadFew f{};
+      f.W = W + v0 * ldw;
+      f.ldw = ldw;
+      f.x = x;
+      f.ldx = ldx;
+      f.M = M;
+      f.K = K;
+      f.v0 = v0;
+      f.vocab = t.vocab;
+      f.scale = scale;
+      f.map = r.map;
+      f.count = r.count;
+      f.cols = r.cols;
+      f.P = t.P;
+      f.ldp = t.ldp;
+      f.p_plane = up(t.vocab, 2 * kStep);
+      f.p_terms = t.p_terms;
+      f.Q = t.Q;
+      f.ldq = t.ldq;
+      f.q_plane = t.q_plane;
+      f.q_terms = t.q_terms;
+      e = launch_head_few_probs(f, st);
+    } else if (e == hipSuccess) {
+      e = launch_head_probs(t, st);
+    }
     if (e == hipSuccess && dX) {
       t.a = t.P;
       t.lda = t.ldp;
