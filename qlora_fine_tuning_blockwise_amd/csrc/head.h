@@ -53,7 +53,6 @@ hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
 struct HeadTiles {
   const uint16_t* a;  // 16-byte aligned rows
   int64_t lda;        // a multiple of 8
-  int64_t a_plane;    // launch_head_dw: elements to the second term
   const uint16_t* b;
   int64_t b_steps;    // steps that a tile of b has room for (logits)
   int64_t ldb, b_width, vocab_left;  // gradients: b's rows, columns; entries of the vocabulary from v0 on

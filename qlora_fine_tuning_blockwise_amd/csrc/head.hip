@@ -217,6 +217,59 @@ __device__ __forceinline__ u32x4_t read_columns(const uint16_t* p) {
   return u32x4_t{a[0], a[1], b[0], b[1]};
 }
 
+// A wave's 128 x 128 block of dW (rows of the block are columns of dW) by way of
+// its 16 KB of LDS, 32 rows of dW at a time: 16-byte part c of row i at c ^ i. In
+// LDS the sums are bf16 where that is all that is written, fp32 (kWide) where dW
+// is, or where they are added to it.
+template <bool kBf16, bool kWide>
+__device__ __forceinline__ void put_dw(const f32x16_t (&acc)[4][4], char* own, const HeadTiles& p,
+                                       int64_t k0, int64_t v0, int lane) {
+  constexpr int E = kWide ? 4 : 8, kParts = 128 / E, kRow = kParts * 16;
+  const int i = lane & 31, h = lane >> 5;
+#pragma unroll
+  for (int nt = 0; nt < 4; ++nt) {
+#pragma unroll
+    for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const f32x16_t& v = acc[mt][nt];
+        if constexpr (kWide)
+          *reinterpret_cast<f32x4_t*>(own + i * kRow + 16 * ((8 * mt + 2 * g + h) ^ i)) =
+              f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+        else
+          *reinterpret_cast<u32x2_t*>(own + i * kRow + 16 * ((4 * mt + g) ^ (i & 15)) + 8 * h) =
+              u32x2_t{pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+      }
+#pragma unroll
+    for (int r = 0; r < 32 * kParts / 64; ++r) {
+      const int row = r * (64 / kParts) + lane / kParts, part = lane % kParts;
+      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(own + row * kRow + 16 * (part ^ (row & (kParts - 1))));
+      const int64_t n = v0 + 32 * nt + row, k = k0 + E * part;
+      if (n >= p.vocab || k >= p.K) continue;
+      elem_t<kBf16>* to = static_cast<elem_t<kBf16>*>(p.dW) + (p.v0 + n) * p.K + k;
+      const int have = count_below<E>(k, p.K);
+      float v[E];
+      if constexpr (kWide) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(q[e]);
+        if (p.accumulate) {
+          float old[E];
+          to_float<kBf16, E>(have == E ? load_vec<kBf16, E>(to) : load_part<kBf16, E>(to, have), old);
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[e] += old[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = e & 1 ? bf16_hi(q[e / 2]) : bf16_lo(q[e / 2]);
+      }
+      if (have == E)
+        store_vec<kBf16, E>(to, v);
+      else
+        store_part<kBf16, E>(to, v, have);
+    }
+  }
+}
+
 // The tile loop. Operands come in three forms:
 //   rows    (a of kStats, kProbs, kDx): row-major, the reduction along a row. LDS
 //           has three slots of a 256 x 64 tile (a pair of steps), 16-byte chunk c
@@ -247,8 +300,8 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
   const int wm = w >> 1, wn = w & 1;
   const int live = __builtin_amdgcn_readfirstlane(*p.count);
   // Rows, columns and steps of this product; half: steps of one term.
-  const int64_t M = kMode == kDx ? live : p.vocab;
-  const int64_t N = kMode == kStats || kMode == kProbs ? live : p.K;
+  const int64_t M = kMode == kDx ? live : kMode == kDw ? p.K : p.vocab;
+  const int64_t N = kMode == kStats || kMode == kProbs ? live : kMode == kDx ? p.K : p.vocab;
   const int half = kMode == kDx   ? (int)(whole_pairs(p.vocab) / kStep)
                    : kMode == kDw ? (int)(whole_pairs(live) / kStep)
                                   : (int)p.steps;
@@ -333,9 +386,9 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ares, (lds_void*)(slot + (64 * w + 8 * q) * 64), 16,
                                                aoff[q], 128 * ps, 0, 0);
     };
-    const auto from_a = [&](int kb) {  // the second term lies a plane on
-      const int ks = step_at(kb), term = ks >= half;
-      return rows_of(p.a + term * p.a_plane, p.lda, m0, p.rows_pad, p.lda, ks - term * half);
+    const auto from_a = [&](int kb) {
+      const int ks = step_at(kb);
+      return rows_of(p.a, p.lda, m0, p.rows_pad, p.lda, ks >= half ? ks - half : ks);
     };
     const auto dma_b_steps = [&](int j, int kb, uint16_t* stage) {
       const int ks = step_at(kb);
@@ -343,9 +396,10 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
                                                boff[j], kOp * 2 * ks, 0, 0);
     };
     const int64_t b_rows = kMode == kDx ? p.vocab_left : p.rows_pad;
-    const auto from_b = [&](int kb) {
-      const int ks = step_at(kb);
-      return rows_of(p.b, p.ldb, n0, b_rows, p.b_width, ks >= half ? ks - half : ks);
+    const auto from_b = [&](int kb) {  // of Q the second term lies a plane on
+      const int ks = step_at(kb), term = ks >= half;
+      return rows_of(p.b + term * (kMode == kDw ? p.q_plane : 0), p.ldb, n0, b_rows, p.b_width,
+                     ks - term * half);
     };
     // Fragment reads. rows: fragment (mt, step half par, substep s) is tile row
     // 128wm + 32mt + i, chunk 4par + 2s + h, at position chunk ^ ((i >> 1) & 7).
@@ -581,8 +635,12 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     }
   } else if constexpr (kMode == kProbs) {
     // Whole pairs of steps of what the products reduce over are written: along
-    // the vocabulary for P, along the live rows for Q.
+    // the vocabulary for P, along the live rows for Q. 32 rows by 128 entries go
+    // through the wave's own LDS, so that a store is 256 bytes of four rows (8 bytes
+    // of 64 from the registers: 390 us a piece of 1536 x 32000 instead of 350).
     const int64_t phalf = whole_pairs(p.vocab), qhalf = whole_pairs(live);
+    uint16_t* const own = w == 0 ? sb0 : w == 1 ? sb1 : w == 2 ? sb2 : sb3;
+    const int64_t mwave = m0 + 128 * wm;
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       const int64_t n = nw + 32 * nt;
@@ -591,22 +649,45 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          float pr[4];
-          const int64_t v = mw + 32 * mt + 8 * g;
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            pr[e] = v + e < M && c.label >= 0
-                        ? exp2_fast(fmaf(acc[mt][nt][4 * g + e], p.scale, -c.most) * kLog2e) * c.over
-                        : 0.0f;
-          if (p.P && n < N && v < phalf)
-            store_terms(p.P + n * p.ldp + v, phalf, p.p_terms, pr);
-          if (p.Q && n < qhalf) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) pr[e] = (pr[e] - (d == 32 * mt + 8 * g + e ? 1.0f : 0.0f)) * c.factor;
-            store_terms(p.Q + n * p.ldq + v, p.q_plane, p.q_terms, pr);
-          }
+        for (int e = 0; e < 16; ++e) {
+          const bool in = mw + 32 * mt + 8 * (e >> 2) + (e & 3) < M && c.label >= 0;
+          acc[mt][nt][e] =
+              in ? exp2_fast(fmaf(acc[mt][nt][e], p.scale, -c.most) * kLog2e) * c.over : 0.0f;
         }
+      // The values in bf16, or what those lost.
+      const auto put = [&](uint16_t* to, int64_t ld, int64_t cols_end, int64_t rows_end, bool lost) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const f32x16_t& v = acc[mt][nt];
+            u32x2_t q = {pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+            if (lost)
+              q = u32x2_t{pack_bf16x2(v[4 * g] - bf16_lo(q[0]), v[4 * g + 1] - bf16_hi(q[0])),
+                          pack_bf16x2(v[4 * g + 2] - bf16_lo(q[1]), v[4 * g + 3] - bf16_hi(q[1]))};
+            *reinterpret_cast<u32x2_t*>(&own[i * 128 + 8 * ((4 * mt + g) ^ (i & 15)) + 4 * h]) = q;
+          }
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int row = 4 * r + (lane >> 4), part = lane & 15;
+          const u32x4_t q = *reinterpret_cast<const u32x4_t*>(&own[row * 128 + 8 * (part ^ (row & 15))]);
+          const int64_t at = n0 + 128 * wn + 32 * nt + row, v = mwave + 8 * part;
+          if (at < rows_end && v < cols_end) *reinterpret_cast<u32x4_t*>(to + at * ld + v) = q;
+        }
+      };
+      if (p.P)
+        for (int term = 0; term < p.p_terms; ++term)
+          put(p.P + term * phalf, p.ldp, phalf, N, term > 0);
+      if (p.Q) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            acc[mt][nt][e] =
+                (acc[mt][nt][e] - (d == 32 * mt + 8 * (e >> 2) + (e & 3) ? 1.0f : 0.0f)) * c.factor;
+        for (int term = 0; term < p.q_terms; ++term)
+          put(p.Q + term * p.q_plane, p.ldq, p.ldq, qhalf, term > 0);
+      }
     }
   } else if constexpr (kMode == kDx) {
     // The sums in the order of the registers, 16 bytes a thread: tile by tile,
@@ -627,29 +708,15 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         }
     }
   } else {
-#pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const int64_t n = nw + 32 * nt;
-      if (n >= N) continue;
-#pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int64_t m = mw + 32 * mt + 8 * (e >> 2) + (e & 3);
-          if (m >= M) continue;
-          const int64_t at = (p.v0 + m) * p.K + n;
-          float v = acc[mt][nt][e];
-          if (p.dw_bf16) {
-            uint16_t* o = static_cast<uint16_t*>(p.dW) + at;
-            if (p.accumulate) v += bf16_lo(*o);
-            store1<true>(o, v);
-          } else {
-            float* o = static_cast<float*>(p.dW) + at;
-            if (p.accumulate) v += *o;
-            *o = v;
-          }
-        }
-    }
+    uint16_t* const own = w == 0 ? sb0 : w == 1 ? sb1 : w == 2 ? sb2 : sb3;
+    const int64_t mwave = m0 + 128 * wm, nwave = n0 + 128 * wn;
+    char* const lds = reinterpret_cast<char*>(own);
+    if (!p.dw_bf16)
+      put_dw<false, true>(acc, lds, p, mwave, nwave, lane);
+    else if (p.accumulate)
+      put_dw<true, true>(acc, lds, p, mwave, nwave, lane);
+    else
+      put_dw<true, false>(acc, lds, p, mwave, nwave, lane);
   }
 }
 

@@ -24,11 +24,11 @@ bool shape_ok(int64_t M, int64_t V, int64_t K) {
          K <= QLORA_MAX_HEAD_WIDTH && V <= kMaxElems / K;
 }
 
-// Entries of the vocabulary in a copy of W's rows: about 64 MB of them.
+// Entries of the vocabulary in a copy of W's rows: 128 MB of them at most, all
+// copies alike.
 int64_t copy_rows(int64_t V, int64_t Kp) {
-  const int64_t n = ((int64_t)1 << 25) / Kp / kTile * kTile;
-  const int64_t most = up(V, kTile);
-  return n < kTile ? kTile : n > most ? most : n;
+  const int64_t most = ((int64_t)1 << 26) / Kp, pieces = (V + most - 1) / most;
+  return up((V + pieces - 1) / pieces, kTile);
 }
 
 struct Layout {
@@ -328,11 +328,10 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
       e = launch_head_dx(t, st);
     }
     if (e == hipSuccess && dW) {
-      t.a = t.Q;
-      t.lda = t.ldq;
-      t.a_plane = t.q_plane;
-      t.b = xr;
-      t.ldb = t.b_width = L.Kp;
+      t.a = xr;
+      t.lda = L.Kp;
+      t.b = t.Q;
+      t.ldb = t.b_width = t.ldq;
       e = launch_head_dw(t, st);
     }
   }
