@@ -641,6 +641,15 @@ typedef struct qlora_tensor {
   int32_t reserved; /* 0 */
 } qlora_tensor;
 
+/* A table of the tensors' pieces for a program whose tensors stay where they are:
+ * qlora_tensor_table writes it to host memory (16-byte aligned, of at least
+ * qlora_tensor_table_bytes, else QLORA_ERR_ALIGN and QLORA_ERR_WORKSPACE), the
+ * program copies it to the device once and passes that copy with every call on
+ * exactly these tensors. Host only; the sizes are 0 for invalid tensors and for
+ * no elements; errors as qlora_grad_norm. */
+size_t qlora_tensor_table_bytes(const qlora_tensor* tensors, int64_t count);
+int qlora_tensor_table(const qlora_tensor* tensors, int64_t count, void* table, size_t table_bytes);
+
 /* Device workspace, in bytes, of qlora_grad_norm for these tensors (their sizes
  * alone count). Host only; 0 for invalid ones and for no elements. */
 size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* grads, int64_t count);
@@ -650,27 +659,33 @@ size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* grads, int64_t count)
  *   result[0] = norm = sqrt(sum over all elements of g^2)
  *   result[1] = max_norm / norm where norm > max_norm, else 1
  *   grads   host array of count descriptors, read during the call only;
+ *   table   their table on the device, or NULL (a launch for every 128 tensors
+ *           then, instead of one for all);
  *   result  fp32 [2], device;  max_norm >= 0 (infinity: the factor is 1).
  * Squares and sums are in 64 bits, so values of every size have their norm. A
  * norm that is infinite gives the factor 0, a NaN gives NaN: a caller that skips
  * such steps looks at the norm. A tensor that is listed twice counts twice. No
  * elements: norm 0, factor 1. QLORA_ERR_INVALID_ARG for count < 0, n < 0,
- * reserved != 0, a NULL array, max_norm < 0 or NaN; QLORA_ERR_SHAPE past
- * QLORA_MAX_TENSORS tensors or 2^40 elements; QLORA_ERR_DTYPE, QLORA_ERR_ALIGN
- * and QLORA_ERR_WORKSPACE as elsewhere. */
-int qlora_grad_norm(const qlora_tensor* grads, int64_t count, float max_norm, float* result,
-                    void* workspace, size_t workspace_bytes, void* stream);
+ * reserved != 0, a NULL array, max_norm < 0 or NaN, and a result or workspace over
+ * a tensor or the table; QLORA_ERR_SHAPE past QLORA_MAX_TENSORS tensors or 2^40
+ * elements; QLORA_ERR_DTYPE, QLORA_ERR_ALIGN and QLORA_ERR_WORKSPACE as
+ * elsewhere. */
+int qlora_grad_norm(const qlora_tensor* grads, int64_t count, const void* table, float max_norm,
+                    float* result, void* workspace, size_t workspace_bytes, void* stream);
 
 /* out[i] = RN(grads[i] * factor) for every tensor, in its own type.
  *   out     host array of count descriptors with the sizes and types of grads
  *           (QLORA_ERR_SHAPE, QLORA_ERR_DTYPE otherwise), or NULL: in place. An
  *           out[i] may be grads[i]; a factor of 1 then leaves it untouched.
+ *   table, out_table  the tables of grads and of out on the device, or NULL (in
+ *           place table alone counts);
  *   factor  fp32, device: for instance result + 1 of qlora_grad_norm.
  * QLORA_ERR_INVALID_ARG where an output shares memory with another output (a
- * tensor listed twice, in place), another input or the factor. Other errors as
- * qlora_grad_norm; QLORA_ERR_INTERNAL if the host has no memory for that check. */
+ * tensor listed twice, in place), another input, a table or the factor. Other
+ * errors as qlora_grad_norm; QLORA_ERR_INTERNAL if the host has no memory for that
+ * check. */
 int qlora_grad_scale(const qlora_tensor* grads, const qlora_tensor* out, int64_t count,
-                     const float* factor, void* stream);
+                     const void* table, const void* out_table, const float* factor, void* stream);
 
 /* qlora_adamw_step on the gradient grad * factor, each product rounded to fp32
  * before the step's first operation; factor is fp32 on the device (NULL:

@@ -907,9 +907,11 @@ def qlora_head_loss_bwd(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
 class TensorList:
     """Tensors as qlora_grad_norm and qlora_grad_scale take them: contiguous,
     fp32 or bf16, on one device. A program whose gradients stay where they are
-    makes the list once; it holds the tensors, which must keep their storage."""
+    makes the list once (qlora_tensor_list), outside of a graph's capture; it
+    holds the tensors, which must keep their storage, and a table of their pieces
+    on the device, with which a call is one launch for all of them."""
 
-    def __init__(self, tensors):
+    def __init__(self, tensors, table=True):
         self.tensors = tuple(tensors)
         self.device = self.tensors[0].device if self.tensors else None
         self.array = (_lib.Tensor * max(1, len(self.tensors)))()
@@ -922,8 +924,15 @@ class TensorList:
                 raise ValueError(f"tensors: on {t.device} and on {self.device}")
             d.data, d.n, d.dtype, d.reserved = t.data_ptr(), t.numel(), _FLOATS[t.dtype], 0
         self.address = ctypes.addressof(self.array)
-        self.workspace_bytes = int(_lib.load().qlora_grad_norm_workspace_bytes(
-            self.address, len(self.tensors)))
+        lib, count = _lib.load(), len(self.tensors)
+        self.workspace_bytes = int(lib.qlora_grad_norm_workspace_bytes(self.address, count))
+        self.table = None
+        need = int(lib.qlora_tensor_table_bytes(self.address, count)) if table else 0
+        if need:
+            rows = torch.empty(need, dtype=torch.uint8)
+            _lib.check(lib.qlora_tensor_table(self.address, count, rows.data_ptr(), need),
+                       "qlora_tensor_table")
+            self.table = rows.to(self.device)
 
     def __len__(self):
         return len(self.tensors)
@@ -934,8 +943,13 @@ def qlora_tensor_list(tensors) -> TensorList:
     return tensors if isinstance(tensors, TensorList) else TensorList(tensors)
 
 
+def _tensors(tensors) -> TensorList:
+    """A list that the program keeps, or one for this call alone."""
+    return tensors if isinstance(tensors, TensorList) else TensorList(tensors, table=False)
+
+
 def qlora_grad_norm_workspace_bytes(grads) -> int:
-    return qlora_tensor_list(grads).workspace_bytes
+    return _tensors(grads).workspace_bytes
 
 
 def qlora_grad_norm(grads, max_norm: float = float("inf"), result: torch.Tensor | None = None,
@@ -943,7 +957,7 @@ def qlora_grad_norm(grads, max_norm: float = float("inf"), result: torch.Tensor 
     """fp32 [2] on the device: the global norm of all gradients (a TensorList or
     tensors), and the factor that clips it to max_norm (1 where the norm is not
     above it)."""
-    grads = qlora_tensor_list(grads)
+    grads = _tensors(grads)
     dev = grads.device
     if dev is None:
         if result is None:
@@ -958,9 +972,9 @@ def qlora_grad_norm(grads, max_norm: float = float("inf"), result: torch.Tensor 
         result = torch.empty(2, dtype=torch.float32, device=dev)
     if grads.workspace_bytes or workspace is not None:
         workspace = _bytes(workspace, grads.workspace_bytes, dev)
-    st = _lib.load().qlora_grad_norm(grads.address, len(grads), max_norm, _at(result),
-                                     _at(workspace), 0 if workspace is None else workspace.numel(),
-                                     _here(dev))
+    st = _lib.load().qlora_grad_norm(grads.address, len(grads), _at(grads.table), max_norm,
+                                     _at(result), _at(workspace),
+                                     0 if workspace is None else workspace.numel(), _here(dev))
     if st:
         _lib.check(st, "qlora_grad_norm")
     return result
@@ -970,7 +984,7 @@ def qlora_grad_scale(grads, factor: torch.Tensor, out=None, stream=None) -> None
     """Every gradient times factor (one fp32 value on the device, such as
     qlora_grad_norm's result[1:]), in place or into out (a TensorList or tensors
     of the same sizes and dtypes)."""
-    grads = qlora_tensor_list(grads)
+    grads = _tensors(grads)
     dev = grads.device
     _one_factor(factor, "factor")
     if dev is None:
@@ -978,13 +992,15 @@ def qlora_grad_scale(grads, factor: torch.Tensor, out=None, stream=None) -> None
     if factor.device != dev:
         raise ValueError(f"factor: on {factor.device}, expected {dev}")
     if out is not None:
-        out = qlora_tensor_list(out)
+        out = _tensors(out)
         if len(out) != len(grads) or out.device != dev:
             raise ValueError("qlora_grad_scale: out needs as many tensors, on the same device")
     if _elsewhere(dev, stream):
         with _place(dev, stream):
             return qlora_grad_scale(grads, factor, out)
     st = _lib.load().qlora_grad_scale(grads.address, None if out is None else out.address,
-                                      len(grads), _at(factor), _here(dev))
+                                      len(grads), _at(grads.table),
+                                      None if out is None else _at(out.table), _at(factor),
+                                      _here(dev))
     if st:
         _lib.check(st, "qlora_grad_scale")

@@ -93,8 +93,10 @@ SIGNATURES = {
     "qlora_head_loss_bwd": (INT, [P, I64, P, I64, I64, I64, I64, P, INT, FLT, P, P, P, I64, INT, P,
                                   INT, INT, P, SZ, P]),
     "qlora_grad_norm_workspace_bytes": (SZ, [P, I64]),
-    "qlora_grad_norm": (INT, [P, I64, FLT, P, P, SZ, P]),
-    "qlora_grad_scale": (INT, [P, P, I64, P, P]),
+    "qlora_tensor_table_bytes": (SZ, [P, I64]),
+    "qlora_tensor_table": (INT, [P, I64, P, SZ]),
+    "qlora_grad_norm": (INT, [P, I64, P, FLT, P, P, SZ, P]),
+    "qlora_grad_scale": (INT, [P, P, I64, P, P, P, P]),
     "qlora_adamw_step_scaled": (INT, [P, P, INT, P, P, P, P, I64, DBL, DBL, DBL, DBL, DBL, I64, P]),
 }
 

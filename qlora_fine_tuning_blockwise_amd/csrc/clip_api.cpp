@@ -31,22 +31,26 @@ int tensors_check(const qlora_tensor* t, int64_t count, int64_t* total) {
   return QLORA_OK;
 }
 
-// Elements of a chunk: 16384 (32 KB of bf16), and more where that leaves over
-// 2^14 chunks, so that the sums stay few (2^14 of them are 128 KB).
-int64_t chunk_elems(int64_t total) {
-  int64_t c = 16384;
-  while (total / c > 16384) c *= 2;
+int64_t tensor_bytes(const qlora_tensor& t) { return t.n * tensor_elem(t); }
+
+// Bytes of a chunk: 32 KB, and more where that leaves over 2^14 chunks, so that
+// the sums stay few (2^14 of them are 128 KB).
+int64_t chunk_bytes(const qlora_tensor* t, int64_t count) {
+  int64_t all = 0, c = 32768;
+  for (int64_t i = 0; i < count; ++i) all += tensor_bytes(t[i]);
+  while (all / c > 16384) c *= 2;
   return c;
 }
 
+int64_t chunks_of(const qlora_tensor& t, int64_t chunk) { return (tensor_bytes(t) + chunk - 1) / chunk; }
 int64_t chunks_of(const qlora_tensor* t, int64_t count, int64_t chunk) {
   int64_t c = 0;
-  for (int64_t i = 0; i < count; ++i) c += (t[i].n + chunk - 1) / chunk;
+  for (int64_t i = 0; i < count; ++i) c += chunks_of(t[i], chunk);
   return c;
 }
 
-size_t norm_bytes(const qlora_tensor* t, int64_t count, int64_t total) {
-  return round_up((size_t)chunks_of(t, count, chunk_elems(total)) * sizeof(double));
+size_t norm_bytes(const qlora_tensor* t, int64_t count) {
+  return round_up((size_t)chunks_of(t, count, chunk_bytes(t, count)) * sizeof(double));
 }
 
 // Calls launch(table, chunks, chunks before) for the tensors, kSpans at a time.
@@ -67,7 +71,7 @@ hipError_t in_launches(const qlora_tensor* in, const qlora_tensor* out, int64_t 
       t.out[k] = out ? out[i].data : nullptr;
       t.n[k] = in[i].n;
       if (in[i].dtype == QLORA_DTYPE_BF16) t.bf16_bits[k >> 6] |= (uint64_t)1 << (k & 63);
-      chunks += (uint32_t)((in[i].n + chunk - 1) / chunk);
+      chunks += (uint32_t)chunks_of(in[i], chunk);
       t.end[k] = chunks;
     }
     if (t.count == 0) break;
@@ -83,22 +87,31 @@ hipError_t in_launches(const qlora_tensor* in, const qlora_tensor* out, int64_t 
   return hipSuccess;
 }
 
-Span tensor_span(const qlora_tensor& t) { return span_of(t.data, t.n * tensor_elem(t)); }
+Span tensor_span(const qlora_tensor& t) { return span_of(t.data, tensor_bytes(t)); }
 
 struct Run {
   uintptr_t first, end;
-  bool written;
   bool operator<(const Run& o) const { return first < o.first; }
 };
 
-// Whether a written run shares memory with another run (read runs may share).
-bool runs_meet(Run* r, int64_t n) {
+// Runs in the order of their addresses, as the tensors of one buffer come.
+void in_order(Run* r, int64_t n) {
   if (!std::is_sorted(r, r + n)) std::sort(r, r + n);
-  uintptr_t written = 0, read = 0;  // the furthest ends so far
-  for (int64_t i = 0; i < n; ++i) {
-    if (r[i].first < written || (r[i].written && r[i].first < read)) return true;
-    uintptr_t& far = r[i].written ? written : read;
-    if (r[i].end > far) far = r[i].end;
+}
+
+// Whether a written run shares memory with another written one, or with one that
+// is read (of these some may share with each other).
+bool runs_meet(Run* written, int64_t n, Run* read, int64_t m) {
+  in_order(written, n);
+  in_order(read, m);
+  for (int64_t i = 0; i + 1 < n; ++i)
+    if (written[i + 1].first < written[i].end) return true;
+  // Written runs lie apart now, so their ends are in order too: each read run
+  // against the first one that ends behind its start.
+  int64_t i = 0;
+  for (int64_t j = 0; j < m; ++j) {
+    while (i < n && written[i].end <= read[j].first) ++i;
+    if (i < n && written[i].first < read[j].end) return true;
   }
   return false;
 }
@@ -125,68 +138,112 @@ using namespace qlora;
 
 extern "C" {
 
-size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* grads, int64_t count) {
+size_t qlora_tensor_table_bytes(const qlora_tensor* tensors, int64_t count) {
   int64_t total;
-  return tensors_check(grads, count, &total) == QLORA_OK ? norm_bytes(grads, count, total) : 0;
+  if (tensors_check(tensors, count, &total) != QLORA_OK) return 0;
+  return (size_t)chunks_of(tensors, count, chunk_bytes(tensors, count)) * sizeof(ChunkEntry);
 }
 
-int qlora_grad_norm(const qlora_tensor* grads, int64_t count, float max_norm, float* result,
-                    void* workspace, size_t workspace_bytes, void* stream) {
+int qlora_tensor_table(const qlora_tensor* tensors, int64_t count, void* table,
+                       size_t table_bytes) {
+  int64_t total;
+  if (const int st = tensors_check(tensors, count, &total)) return st;
+  const int64_t chunk = chunk_bytes(tensors, count);
+  const int64_t chunks = chunks_of(tensors, count, chunk);
+  if (chunks == 0) return QLORA_OK;
+  if (!table) return QLORA_ERR_INVALID_ARG;
+  if (!aligned16(table)) return QLORA_ERR_ALIGN;
+  if (table_bytes < (size_t)chunks * sizeof(ChunkEntry)) return QLORA_ERR_WORKSPACE;
+  ChunkEntry* e = static_cast<ChunkEntry*>(table);
+  for (int64_t i = 0; i < count; ++i) {
+    const int64_t size = tensor_elem(tensors[i]), bytes = tensor_bytes(tensors[i]);
+    for (int64_t at = 0; at < bytes; at += chunk)
+      *e++ = ChunkEntry{(uint64_t)reinterpret_cast<uintptr_t>(tensors[i].data) + (uint64_t)at,
+                        (uint32_t)((bytes - at < chunk ? bytes - at : chunk) / size),
+                        (uint32_t)(tensors[i].dtype == QLORA_DTYPE_BF16)};
+  }
+  return QLORA_OK;
+}
+
+size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* grads, int64_t count) {
+  int64_t total;
+  return tensors_check(grads, count, &total) == QLORA_OK ? norm_bytes(grads, count) : 0;
+}
+
+int qlora_grad_norm(const qlora_tensor* grads, int64_t count, const void* table, float max_norm,
+                    float* result, void* workspace, size_t workspace_bytes, void* stream) {
   if (!(max_norm >= 0.0f)) return QLORA_ERR_INVALID_ARG;
   int64_t total;
   if (const int st = tensors_check(grads, count, &total)) return st;
   if (!result) return QLORA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(result) & 3) || !aligned16(workspace)) return QLORA_ERR_ALIGN;
-  const size_t need = norm_bytes(grads, count, total);
+  if ((reinterpret_cast<uintptr_t>(result) & 3) || !aligned16(workspace) || !aligned16(table))
+    return QLORA_ERR_ALIGN;
+  const int64_t chunk = chunk_bytes(grads, count), chunks = chunks_of(grads, count, chunk);
+  const size_t need = round_up((size_t)chunks * sizeof(double));
   if (need > 0 && (!workspace || workspace_bytes < need)) return QLORA_ERR_WORKSPACE;
   const Span out = span_of(result, 8), ws = span_of(workspace, (int64_t)need);
-  if (meet(out, ws)) return QLORA_ERR_INVALID_ARG;
+  const Span entries = span_of(table, chunks * (int64_t)sizeof(ChunkEntry));
+  if (meet(out, ws) || meet(out, entries) || meet(ws, entries)) return QLORA_ERR_INVALID_ARG;
   for (int64_t i = 0; i < count; ++i)
     if (meet(out, tensor_span(grads[i])) || meet(ws, tensor_span(grads[i])))
       return QLORA_ERR_INVALID_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
   double* part = static_cast<double*>(workspace);
-  const int64_t chunk = chunk_elems(total);
-  hipError_t e = in_launches(grads, nullptr, count, chunk,
-                             [&](const SpanTable& t, uint32_t chunks, int64_t before) {
-                               return launch_grad_norm(t, chunks, part + before, st);
-                             });
-  if (e == hipSuccess)
-    e = launch_grad_norm_join(part, chunks_of(grads, count, chunk), max_norm, result, st);
+  hipError_t e = hipSuccess;
+  if (table && chunks > 0)
+    e = launch_grad_norm_table(static_cast<const ChunkEntry*>(table), (uint32_t)chunks, part, st);
+  else
+    e = in_launches(grads, nullptr, count, chunk,
+                    [&](const SpanTable& t, uint32_t n, int64_t before) {
+                      return launch_grad_norm(t, n, part + before, st);
+                    });
+  if (e == hipSuccess) e = launch_grad_norm_join(part, chunks, max_norm, result, st);
   return launch_status(e);
 }
 
 int qlora_grad_scale(const qlora_tensor* grads, const qlora_tensor* out, int64_t count,
-                     const float* factor, void* stream) {
-  if (!out) out = grads;
+                     const void* table, const void* out_table, const float* factor,
+                     void* stream) {
+  if (!out) out = grads, out_table = table;
   int64_t total, same;
   if (const int st = tensors_check(grads, count, &total)) return st;
-  if (const int st = tensors_check(out, count, &same)) return st;
-  for (int64_t i = 0; i < count; ++i) {
-    if (out[i].n != grads[i].n) return QLORA_ERR_SHAPE;
-    if (out[i].dtype != grads[i].dtype) return QLORA_ERR_DTYPE;
+  if (out != grads) {
+    if (const int st = tensors_check(out, count, &same)) return st;
+    for (int64_t i = 0; i < count; ++i) {
+      if (out[i].n != grads[i].n) return QLORA_ERR_SHAPE;
+      if (out[i].dtype != grads[i].dtype) return QLORA_ERR_DTYPE;
+    }
   }
   if (!factor) return QLORA_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(factor) & 3) return QLORA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(factor) & 3) || !aligned16(table) || !aligned16(out_table))
+    return QLORA_ERR_ALIGN;
   if (total == 0) return QLORA_OK;
-  Run* runs = static_cast<Run*>(std::malloc((size_t)(2 * count + 1) * sizeof(Run)));
-  if (!runs) return QLORA_ERR_INTERNAL;
-  int64_t n = 0;
-  const auto add = [&](const Span& s, bool written) {
-    if (!s.empty()) runs[n++] = Run{s.p, s.end(), written};
+  const int64_t chunk = chunk_bytes(grads, count), chunks = chunks_of(grads, count, chunk);
+  Run* written = static_cast<Run*>(std::malloc((size_t)(2 * count + 3) * sizeof(Run)));
+  if (!written) return QLORA_ERR_INTERNAL;
+  Run* const read = written + count;
+  int64_t n = 0, m = 0;
+  const auto add = [](Run* to, int64_t& k, const Span& s) {
+    if (!s.empty()) to[k++] = Run{s.p, s.end()};
   };
-  add(span_of(factor, 4), false);
   for (int64_t i = 0; i < count; ++i) {
-    add(tensor_span(out[i]), true);
-    if (grads[i].data != out[i].data) add(tensor_span(grads[i]), false);
+    add(written, n, tensor_span(out[i]));
+    if (grads[i].data != out[i].data) add(read, m, tensor_span(grads[i]));
   }
-  const bool shared = runs_meet(runs, n);
-  std::free(runs);
+  add(read, m, span_of(factor, 4));
+  add(read, m, span_of(table, chunks * (int64_t)sizeof(ChunkEntry)));
+  add(read, m, span_of(out_table, chunks * (int64_t)sizeof(ChunkEntry)));
+  const bool shared = runs_meet(written, n, read, m);
+  std::free(written);
   if (shared) return QLORA_ERR_INVALID_ARG;
   hipStream_t st = static_cast<hipStream_t>(stream);
-  return launch_status(in_launches(grads, out, count, chunk_elems(total),
-                                   [&](const SpanTable& t, uint32_t chunks, int64_t) {
-                                     return launch_grad_scale(t, chunks, factor, st);
+  if (table && out_table)
+    return launch_status(launch_grad_scale_table(static_cast<const ChunkEntry*>(table),
+                                                 static_cast<const ChunkEntry*>(out_table),
+                                                 (uint32_t)chunks, factor, st));
+  return launch_status(in_launches(grads, out, count, chunk,
+                                   [&](const SpanTable& t, uint32_t k, int64_t) {
+                                     return launch_grad_scale(t, k, factor, st);
                                    }));
 }
 

@@ -245,7 +245,8 @@ def test_grad_norm_and_scale(i, sizes, kinds):
         assert abs(r[0] - w_norm) <= 1.01 * U * w_norm and abs(r[1] - w_factor) <= 1.01 * U * w_factor
         # elsewhere, then in place
         other = grads_of(sizes, kinds, 1, i + 4)
-        q.qlora_grad_scale(lists, result[1:], out=[v for _, _, v in other])
+        out = [v for _, _, v in other]
+        q.qlora_grad_scale(lists, result[1:], out=out if max_norm > norm else q.qlora_tensor_list(out))
         want = [(t.float() * result[1].cpu()).to(t.dtype) for t, _, _ in made]
         for (_, buf, v), w in zip(other, want):
             assert torch.equal(v.cpu(), w) and int(torch.isnan(buf).sum()) == buf.numel() - w.numel()
