@@ -184,13 +184,15 @@ __device__ __forceinline__ int64_t whole_pairs(int64_t n) { return (n + 2 * kSte
 
 // Splits of the live rows' gradient along its reduction of `pairs` pairs of steps:
 // those with the least rounds of 256 workgroups, where a workgroup takes its
-// share of the reduction and the time of 20 pairs besides (first loads, 256 KB
-// of sums read and written). `pairs` is the first piece's throughout, so that
+// share of the reduction and the time of 50 pairs besides (first loads, 256 KB of
+// sums read and written, and the clock, which falls as more CUs multiply: 1536 x
+// 4096 in pieces of 500 pairs takes as long in 192 workgroups of two splits as in
+// 480 of five, and 3% longer in 768 of eight). `pairs` is the first piece's throughout, so that
 // every piece adds to the same sums.
 __device__ __forceinline__ int dx_splits(int tiles, int pairs) {
   int best = 1, least = 0x7FFFFFFF;
   for (int s = 1; s <= kMostSplits && (s == 1 || tiles * s <= kMostSums) && s <= pairs; ++s) {
-    const int cost = (tiles * s + 255) / 256 * ((pairs + s - 1) / s + 20);
+    const int cost = (tiles * s + 255) / 256 * ((pairs + s - 1) / s + 50);
     if (cost < least) least = cost, best = s;
   }
   return best;
@@ -759,48 +761,65 @@ __global__ __launch_bounds__(256) void head_loss_kernel(const float2* part, int6
   }
 }
 
-// Four rows a workgroup, two columns a thread: of live rows 4y .. 4y + 3 in the
+// Four rows a workgroup, four columns a thread: of live rows 4y .. 4y + 3 in the
 // first half of the grid, whose sums lie as head_tile_kernel's registers had
 // them, and of rows that carry no loss in the second half.
 template <bool kBf16>
 __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
-  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 2;
+  constexpr int E = 4;
+  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E;
   if (k >= a.K) return;
-  const bool two = k + 1 < a.K;
-  const auto put = [&](int64_t row, float x, float y) {
+  const int n = count_below<E>(k, a.K);
+  const auto put = [&](int64_t row, const float (&v)[E]) {
     elem_t<kBf16>* to = static_cast<elem_t<kBf16>*>(a.dX) + row * a.lddx + k;
-    store1<kBf16>(to, x);
-    if (two) store1<kBf16>(to + 1, y);
+    if (n == E)
+      store_vec<kBf16, E>(to, v);
+    else
+      store_part<kBf16, E>(to, v, n);
   };
   const int64_t groups = (a.M + 3) / 4;
   if ((int64_t)blockIdx.y >= groups) {
     const int64_t m = ((int64_t)blockIdx.y - groups) * 4;
+    const float none[E] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int e = 0; e < 4; ++e)
-      if (m + e < a.M && a.inv[m + e] < 0) put(m + e, 0.0f, 0.0f);
+      if (m + e < a.M && a.inv[m + e] < 0) put(m + e, none);
     return;
   }
   const int live = *a.count;
   const int j = (int)blockIdx.y * 4;
   if (j >= live) return;
+  // The labels' rows of W, requested before the sums.
+  HeadColumn col[4];
+  Vec<true, E> w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) col[e] = a.cols[j + e < live ? j + e : j];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const uint16_t* from = a.W + (int64_t)col[e].label * a.ldw + k;
+    w[e] = n == E ? load_vec<true, E>(from) : load_part<true, E>(from, n);
+  }
   const int tiles_n = ceil_tile(a.K), tiles = ceil_tile(live) * tiles_n;
   const int splits = dx_splits(tiles, a.pairs);
   const int r = j % kTile, c = (int)(k % kTile);
   const int tid = ((r / 128) * 2 + c / 128) * 64 + ((r / 4) % 2) * 32 + c % 32;
   const int reg = ((r % 128 / 32) * 4 + c % 128 / 32) * 4 + r % 32 / 8;
   const float* from = a.acc + ((int64_t)(j / kTile) * tiles_n + k / kTile) * (kTile * kTile) + reg * 1024 + 4 * tid;
-  f32x4_t x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
-#pragma unroll 4
+  f32x4_t sum[E];  // of a column, its four rows
+#pragma unroll
+  for (int e = 0; e < E; ++e) sum[e] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
   for (int s = 0; s < splits; ++s, from += (int64_t)tiles * (kTile * kTile)) {
-    x += *reinterpret_cast<const f32x4_t*>(from);
-    y += *reinterpret_cast<const f32x4_t*>(from + 4);
+#pragma unroll
+    for (int e = 0; e < E; ++e) sum[e] += *reinterpret_cast<const f32x4_t*>(from + 4 * e);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (j + e >= live) break;
-    const HeadColumn col = a.cols[j + e];
-    const uint16_t* w = a.W + (int64_t)col.label * a.ldw + k;
-    put(a.map[j + e], (x[e] - bf16_lo(w[0])) * col.factor,
-        (y[e] - (two ? bf16_lo(w[1]) : 0.0f)) * col.factor);
+  for (int row = 0; row < 4; ++row) {
+    if (j + row >= live) break;
+    float o[E], v[E];
+    to_float<true, E>(w[row], o);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = (sum[e][row] - o[e]) * col[row].factor;
+    put(a.map[j + row], v);
   }
 }
 
@@ -863,7 +882,7 @@ hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
 }
 
 hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st) {
-  const dim3 grid(blocks_of((a.K + 1) / 2), (unsigned)((a.M + 3) / 4 * 2));
+  const dim3 grid(blocks_of((a.K + 3) / 4), (unsigned)((a.M + 3) / 4 * 2));
   if (bf16)
     hipLaunchKernelGGL(head_dx_finish_kernel<true>, grid, dim3(256), 0, st, a);
   else
