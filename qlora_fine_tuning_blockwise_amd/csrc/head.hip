@@ -807,7 +807,7 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
   f32x4_t sum[E];  // of a column, its four rows
 #pragma unroll
   for (int e = 0; e < E; ++e) sum[e] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
+#pragma unroll 4
   for (int s = 0; s < splits; ++s, from += (int64_t)tiles * (kTile * kTile)) {
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[e] += *reinterpret_cast<const f32x4_t*>(from + 4 * e);

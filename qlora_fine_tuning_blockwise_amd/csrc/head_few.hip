@@ -8,7 +8,10 @@
 // registers, two chunks ahead of the one that is multiplied; those of x are shared
 // by the eight waves through LDS, two chunks in turn (from the caches, each wave
 // for itself, they cost 16 rows a third and 64 rows twice the time). Unaligned
-// rows and odd widths run the same loads; the last chunk of K is masked.
+// rows and odd widths run the same loads; the last chunk of K is masked. The
+// statistics read W with the nontemporal hint; the probabilities do not, since the
+// product behind them reads W again and finds a part of it in the Infinity Cache
+// (8 rows, 32000 x 4096: 124 instead of 131 us for the gradient).
 #include "head_terms.h"
 
 namespace qlora {
@@ -60,7 +63,7 @@ __global__ __launch_bounds__(kThreads) void head_few_kernel(HeadFew p) {
 #pragma unroll
     for (int t = 0; t < NT; ++t) xv[S][t] = load_vec<true, 8>(xrow[t] + k0 + 8 * xc);
 #pragma unroll
-    for (int f = 0; f < kFrags; ++f) wv[S][f] = load_vec<true, 8, true>(wrow + k0 + 32 * f + 8 * g);
+    for (int f = 0; f < kFrags; ++f) wv[S][f] = load_vec<true, 8, !kProbs>(wrow + k0 + 32 * f + 8 * g);
   };
   const auto put_x = [&](auto sc) {
     constexpr int S = decltype(sc)::value;
