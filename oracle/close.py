@@ -108,7 +108,7 @@ def head_loss_fwd(x, W, labels, scale=1.0):
 def head_loss_bwd(x, W, labels, dloss, scale=1.0, terms=1):
     """(dX, err), (dW, err), for statistics as an fp32 forward gives them. terms:
     into how many bf16 numbers a probability (for dX) and a logit's gradient (for
-    dW) are split before the matrix products, 1 or 2."""
+    dW) are split before the matrix products: 1 for bf16 outputs, 3 for fp32."""
     V, K = W.shape
     live, ids = _live(labels, V)
     live = live & (np.asarray(dloss) != 0)

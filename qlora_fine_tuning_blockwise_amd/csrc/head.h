@@ -20,14 +20,16 @@ struct HeadColumn {
 };
 
 // The rows that carry loss, in order: map[j] is the row of live row j, inv[m]
-// the live row of row m or -1, *count how many there are.
+// the live row of row m or -1, count[0] how many there are, count[1] the splits of
+// their gradient's product.
 struct HeadRows {
   const void* labels;
   bool ids64;
   const float* dloss;  // rows with 0 carry nothing either; NULL in the forward
   const float* stats;  // [2, M]; NULL in the forward
   float scale;
-  int64_t M, V;
+  int64_t M, V, K;
+  int pairs;  // of launch_head_dx; 0 without it
   int32_t* map;
   int32_t* inv;
   int32_t* count;
@@ -68,7 +70,7 @@ struct HeadTiles {
   int64_t rows_pad;
   float* at_label;
   // probabilities P and the logits' gradients Q, live rows by vocabulary; the
-  // second term of P lies behind the first in its row, that of Q a plane on
+  // terms of P lie one behind another in a row, those of Q a plane apart
   uint16_t* P;
   int64_t ldp;
   int p_terms;
@@ -78,7 +80,6 @@ struct HeadTiles {
   // gradients
   float* acc;  // sums of the live rows' gradient, [split][tile][256 x 256]
   bool add;    // to what acc holds
-  int pairs;   // pairs of steps of the first piece's product, which decide the splits
   void* dW;
   bool dw_bf16, accumulate;
 };
@@ -100,16 +101,17 @@ inline int64_t head_sums(int64_t rows_most, int64_t K) {
 }
 
 // The logits of at most kFewRows rows, one pass over W at any row stride and
-// alignment. Statistics: of rows j themselves, joined over 128 entries of the
-// vocabulary: part[row][parts]. Probabilities: of live rows, as
-// launch_head_probs leaves them; p_plane: elements of P to the second term.
+// alignment. Statistics: of rows j themselves, joined over `entries`
+// entries of the vocabulary (few_entries): part[row][parts]. Probabilities: of live rows, as
+// launch_head_probs leaves them; p_plane: elements between P's terms.
 constexpr int64_t kFewRows = 64;
-constexpr int64_t kFewEntries = 128;
+// Entries of the vocabulary that a workgroup takes.
+inline int64_t few_entries(int64_t V) { return V >= 192 * 128 ? 128 : 32; }
 struct HeadFew {
   const uint16_t* W;  // the piece's rows
   int64_t ldw;
   const uint16_t* x;
-  int64_t ldx, M, K, v0, vocab;
+  int64_t ldx, M, K, v0, vocab, entries;
   float scale;
   const void* labels;
   bool ids64;
@@ -137,10 +139,8 @@ hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
                             const float* at_label, const int32_t* inv, int64_t M, float* loss,
                             float* stats, hipStream_t st);
 // dX of all M rows: factor (sum of the splits - the label's row of W), or 0.
-// pairs: as of launch_head_dx.
 struct HeadDx {
   const float* acc;
-  int pairs;
   const int32_t* map;
   const int32_t* inv;
   const int32_t* count;

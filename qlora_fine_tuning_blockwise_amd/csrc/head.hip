@@ -24,8 +24,8 @@
 // the probabilities alone and the label's row of W is subtracted in fp32 at
 // the end, so that what is rounded (2^-8 of a probability at most) is a part of
 // a small mean of W's rows, not of the label's row. For fp32 gradients a
-// probability is split into two bf16 numbers (2^-16 is lost) and the products
-// have twice the terms.
+// value is split into three bf16 numbers (24 bits, as fp32 has) and the products
+// have three times the terms.
 //
 // The tile loop is the dense stage's of the linear layer (gemm_nt.hip has its
 // description): 256 x 256 tiles, four waves of 128 x 128 on
@@ -40,6 +40,27 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
+
+__device__ __forceinline__ int ceil_tile(int64_t n) { return (int)((n + kTile - 1) / kTile); }
+
+// Splits of the live rows' gradient along its reduction of `pairs` pairs of steps:
+// those with the least rounds of 256 workgroups, where a workgroup takes its
+// share of the reduction and the time of 50 pairs besides (first loads, 256 KB of
+// sums read and written, and the clock, which falls as more CUs multiply: 1536 x
+// 4096 in pieces of 500 pairs takes as long in 192 workgroups of two splits as in
+// 480 of five, and 3% longer in 768 of eight). A wave weighs all of them at once.
+__device__ __forceinline__ int dx_splits(int tiles, int pairs) {
+  const int s = (threadIdx.x & 63) + 1;
+  int best = 0x7FFFFFFF;  // the cost, then the number of splits
+  if (s == 1 || (s <= kMostSplits && tiles * s <= kMostSums && s <= pairs)) {
+    const int64_t cost = (int64_t)((tiles * s + 255) / 256) * ((pairs + s - 1) / s + 50);
+    best = (int)(cost < (1 << 26) ? cost : (1 << 26) - 1) * 16 + (s - 1);
+  }
+#pragma unroll
+  for (int d = 32; d; d >>= 1) best = min(best, __shfl_xor(best, d));
+  return best % 16 + 1;
+}
+static_assert(kMostSplits <= 16, "splits of a key");
 
 // ------------------------------------------------------------- live rows
 constexpr int kRowThreads = 1024;
@@ -88,7 +109,12 @@ __global__ __launch_bounds__(kRowThreads) void head_rows_kernel(HeadRows a) {
   }
   const int32_t end = (all + kTile - 1) / kTile * kTile;
   for (int32_t k = all + t; k < end; k += kRowThreads) a.cols[k] = HeadColumn{0.0f, 0.0f, 0.0f, -1};
-  if (t == 0) *a.count = all;
+  if (t >= 64) return;
+  const int splits = a.pairs ? dx_splits(max(ceil_tile(all) * ceil_tile(a.K), 1), a.pairs) : 1;
+  if (t == 0) {
+    a.count[0] = all;
+    a.count[1] = splits;
+  }
 }
 
 // ------------------------------------------------------------- b operands
@@ -177,26 +203,11 @@ __device__ __forceinline__ T* pick(T* const (&arr)[N]) {
   return arr[S];
 }
 
+// kTerms: of kProbs those that are written at most; of kDw 1 where bf16 sums are all
+// that is written.
 constexpr int kStats = 0, kProbs = 1, kDx = 2, kDw = 3;
 
-__device__ __forceinline__ int ceil_tile(int64_t n) { return (int)((n + kTile - 1) / kTile); }
 __device__ __forceinline__ int64_t whole_pairs(int64_t n) { return (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep); }
-
-// Splits of the live rows' gradient along its reduction of `pairs` pairs of steps:
-// those with the least rounds of 256 workgroups, where a workgroup takes its
-// share of the reduction and the time of 50 pairs besides (first loads, 256 KB of
-// sums read and written, and the clock, which falls as more CUs multiply: 1536 x
-// 4096 in pieces of 500 pairs takes as long in 192 workgroups of two splits as in
-// 480 of five, and 3% longer in 768 of eight). `pairs` is the first piece's throughout, so that
-// every piece adds to the same sums.
-__device__ __forceinline__ int dx_splits(int tiles, int pairs) {
-  int best = 1, least = 0x7FFFFFFF;
-  for (int s = 1; s <= kMostSplits && (s == 1 || tiles * s <= kMostSums) && s <= pairs; ++s) {
-    const int cost = (tiles * s + 255) / 256 * ((pairs + s - 1) / s + 50);
-    if (cost < least) least = cost, best = s;
-  }
-  return best;
-}
 
 // Rows of a matrix from one of its columns on: their first byte, and the bytes up
 // to the matrix's end.
@@ -220,36 +231,42 @@ __device__ __forceinline__ u32x4_t read_columns(const uint16_t* p) {
 }
 
 // A wave's 128 x 128 block of dW (rows of the block are columns of dW) by way of
-// its 16 KB of LDS, 32 rows of dW at a time: 16-byte part c of row i at c ^ i. In
-// LDS the sums are bf16 where that is all that is written, fp32 (kWide) where dW
-// is, or where they are added to it.
+// its 16 KB of LDS: 16-byte part c of row i at c ^ i. In LDS the sums are bf16
+// where that is all that is written, 64 rows of dW at a time; fp32 (kWide) where dW
+// is, or where they are added to it, 32 rows at a time.
 template <bool kBf16, bool kWide>
-__device__ __forceinline__ void put_dw(const f32x16_t (&acc)[4][4], char* own, const HeadTiles& p,
-                                       int64_t k0, int64_t v0, int lane) {
-  constexpr int E = kWide ? 4 : 8, kParts = 128 / E, kRow = kParts * 16;
+__device__ __forceinline__ void put_dw(const f32x16_t (&acc)[4][4], uint16_t* own,
+                                       const HeadTiles& p, int64_t k0, int64_t v0, int lane) {
+  constexpr int E = kWide ? 4 : 8, kParts = 128 / E;
+  constexpr int kPasses = kWide ? 4 : 2, kRows = 128 / kPasses;
   const int i = lane & 31, h = lane >> 5;
+  const int part = lane % kParts, have = count_below<E>(k0 + E * part, p.K);
+  const int rows = have <= 0 ? 0 : (int)min(p.vocab - v0, (int64_t)128);
+  const int row0 = lane / kParts;
+  elem_t<kBf16>* to = static_cast<elem_t<kBf16>*>(p.dW) + (p.v0 + v0 + row0) * p.K + k0 + E * part;
+  char* const lds = reinterpret_cast<char*>(own);
 #pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
+  for (int pass = 0; pass < kPasses; ++pass) {
 #pragma unroll
-    for (int mt = 0; mt < 4; ++mt)
+    for (int n = 0; n < 4 / kPasses; ++n) {
+      char* const at = lds + (32 * n + i) * (kParts * 16);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const f32x16_t& v = acc[mt][nt];
-        if constexpr (kWide)
-          *reinterpret_cast<f32x4_t*>(own + i * kRow + 16 * ((8 * mt + 2 * g + h) ^ i)) =
-              f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
-        else
-          *reinterpret_cast<u32x2_t*>(own + i * kRow + 16 * ((4 * mt + g) ^ (i & 15)) + 8 * h) =
-              u32x2_t{pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
-      }
+      for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-    for (int r = 0; r < 32 * kParts / 64; ++r) {
-      const int row = r * (64 / kParts) + lane / kParts, part = lane % kParts;
-      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(own + row * kRow + 16 * (part ^ (row & (kParts - 1))));
-      const int64_t n = v0 + 32 * nt + row, k = k0 + E * part;
-      if (n >= p.vocab || k >= p.K) continue;
-      elem_t<kBf16>* to = static_cast<elem_t<kBf16>*>(p.dW) + (p.v0 + n) * p.K + k;
-      const int have = count_below<E>(k, p.K);
+        for (int g = 0; g < 4; ++g) {
+          const f32x16_t& v = acc[mt][4 / kPasses * pass + n];
+          if constexpr (kWide)
+            *reinterpret_cast<f32x4_t*>(at + 16 * ((8 * mt + 2 * g + h) ^ i)) =
+                f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+          else
+            *reinterpret_cast<u32x2_t*>(at + 16 * ((4 * mt + g) ^ (i & 15)) + 8 * h) =
+                u32x2_t{pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+        }
+    }
+#pragma unroll 2
+    for (int r = row0; r < kRows; r += 64 / kParts, to += (64 / kParts) * p.K) {
+      const u32x4_t q = *reinterpret_cast<const u32x4_t*>(lds + (r * kParts + (part ^ (r & (kParts - 1)))) * 16);
+      if (kRows * pass + r >= rows) continue;
       float v[E];
       if constexpr (kWide) {
 #pragma unroll
@@ -284,7 +301,7 @@ __device__ __forceinline__ void put_dw(const f32x16_t (&acc)[4][4], char* own, c
 //           with g = 0, 5, 2, 7 for r % 4: the 4 rows by 32 bytes that 16 lanes
 //           read lie in different banks, as do the 64 bytes of 32 lanes.
 // A pair of slots is loaded two pairs ahead, a stage three steps.
-template <int kMode>
+template <int kMode, int kTerms = 1>
 __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
   constexpr bool kACols = kMode == kDw, kBCols = kMode == kDx || kMode == kDw;
   __shared__ __attribute__((aligned(1024))) uint16_t sa0[kPair];
@@ -297,8 +314,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
   __shared__ __attribute__((aligned(1024))) uint16_t sb3[kOp];
   uint16_t* const sa[4] = {sa0, sa1, sa2, sa3};  // columns: four stages in the first 16 KB of each
   uint16_t* const sb[4] = {sb0, sb1, sb2, sb3};
-  const int tid = threadIdx.x, lane = tid & 63, i = lane & 31, h = lane >> 5;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);  // wave-uniform
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);  // wave-uniform
   const int wm = w >> 1, wn = w & 1;
   const int live = __builtin_amdgcn_readfirstlane(*p.count);
   // Rows, columns and steps of this product; half: steps of one term.
@@ -309,7 +325,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
                                   : (int)p.steps;
   const int all = kMode == kDx ? half * p.p_terms : kMode == kDw ? half * p.q_terms : half;
   const int tiles_m = ceil_tile(M), tiles_n = ceil_tile(N), tiles = tiles_m * tiles_n;
-  const int splits = kMode == kDx ? dx_splits(max(tiles, 1), p.pairs) : 1;
+  const int splits = kMode == kDx ? __builtin_amdgcn_readfirstlane(p.count[1]) : 1;
   if ((int)blockIdx.x >= tiles * splits) return;
   // Each XCD (blockIdx.x % 8) gets a contiguous range of the splits' tiles.
   int order = xcd_order((int)blockIdx.x, tiles * splits), tm, tn;
@@ -330,6 +346,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
       for (int e = 0; e < 16; ++e) acc[mt][nt][e] = 0.0f;
 
   if (nsteps > 0) {
+    const int lane = threadIdx.x & 63, i = lane & 31, h = lane >> 5;
     const int npairs = (nsteps + 1) / 2;
     const int64_t k0 = (int64_t)ks0 * kStep;
     typedef __attribute__((address_space(3))) void lds_void;
@@ -390,7 +407,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     };
     const auto from_a = [&](int kb) {
       const int ks = step_at(kb);
-      return rows_of(p.a, p.lda, m0, p.rows_pad, p.lda, ks >= half ? ks - half : ks);
+      return rows_of(p.a, p.lda, m0, p.rows_pad, p.lda, ks - ((ks >= half) + (ks >= 2 * half)) * half);
     };
     const auto dma_b_steps = [&](int j, int kb, uint16_t* stage) {
       const int ks = step_at(kb);
@@ -398,8 +415,8 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
                                                boff[j], kOp * 2 * ks, 0, 0);
     };
     const int64_t b_rows = kMode == kDx ? p.vocab_left : p.rows_pad;
-    const auto from_b = [&](int kb) {  // of Q the second term lies a plane on
-      const int ks = step_at(kb), term = ks >= half;
+    const auto from_b = [&](int kb) {  // of Q the terms lie a plane apart
+      const int ks = step_at(kb), term = (ks >= half) + (ks >= 2 * half);
       return rows_of(p.b + term * (kMode == kDw ? p.q_plane : 0), p.ldb, n0, b_rows, p.b_width,
                      ks - term * half);
     };
@@ -588,24 +605,39 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     __builtin_amdgcn_sched_barrier(0);
   }
 
+  // What follows starts from a thread id of its own: derived from the one above, its
+  // values were kept in registers through the loop, which has none to spare.
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int lane = tid & 63, i = lane & 31, h = lane >> 5;
   // Accumulator element e of (mt, nt) is row 32mt + 8(e/4) + 4h + e%4, column
   // 32nt + i of this wave's 128 x 128 block.
   const int64_t mw = m0 + 128 * wm + 4 * h, nw = n0 + 128 * wn + i;
+  uint16_t* const own = w == 0 ? sb0 : w == 1 ? sb1 : w == 2 ? sb2 : sb3;  // a wave's 16 KB of LDS
   if constexpr (kMode == kStats) {
     // A lane has 64 entries of the vocabulary of each of its four rows; the
     // other half of the wave and the other wave of the rows have the rest.
     float2* red = reinterpret_cast<float2*>(sa0);
+    const bool whole = m0 + kTile <= M;  // all of the tile's entries exist
+    const int left = (int)min(M - mw, (int64_t)kTile);
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       float m = -INFINITY;
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const bool in = mw + 32 * mt + 8 * (e >> 2) + (e & 3) < M;
-          acc[mt][nt][e] = in ? acc[mt][nt][e] * p.scale : -INFINITY;
-          m = fmaxf(m, acc[mt][nt][e]);
-        }
+        for (int e = 0; e < 16; ++e) acc[mt][nt][e] *= p.scale;
+      if (!whole) {
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (32 * mt + 8 * (e >> 2) + (e & 3) >= left) acc[mt][nt][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fmaxf(m, acc[mt][nt][e]);
       m = fmaxf(m, __shfl_xor(m, 32));
       const float from = m == -INFINITY ? 0.0f : m;  // none of the vocabulary, or none above it
       float s = 0.0f;
@@ -618,8 +650,9 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
       // The label's logit, where this wave has it.
       const int64_t n = nw + 32 * nt;
       const int label = n < N ? p.cols[n].label : -1;
-      const int64_t d = label - (p.v0 + mw);
-      const bool mine = label >= 0 && d >= 0 && d < 128 && !(d & 4);
+      const int64_t away = label - (p.v0 + mw);
+      const bool mine = label >= 0 && away >= 0 && away < 128 && !(away & 4);
+      const int d = (int)away;
       if (__ballot(mine)) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
@@ -637,59 +670,113 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     }
   } else if constexpr (kMode == kProbs) {
     // Whole pairs of steps of what the products reduce over are written: along
-    // the vocabulary for P, along the live rows for Q. 32 rows by 128 entries go
-    // through the wave's own LDS, so that a store is 256 bytes of four rows (8 bytes
-    // of 64 from the registers: 390 us a piece of 1536 x 32000 instead of 350).
+    // the vocabulary for P, along the live rows for Q. The wave's block goes through
+    // its own LDS, a term at a time, so that a store is 256 bytes of four rows.
     const int64_t phalf = whole_pairs(p.vocab), qhalf = whole_pairs(live);
-    uint16_t* const own = w == 0 ? sb0 : w == 1 ? sb1 : w == 2 ? sb2 : sb3;
-    const int64_t mwave = m0 + 128 * wm;
+    const int64_t mwave = m0 + 128 * wm, nwave = n0 + 128 * wn;
+    const bool whole = m0 + kTile <= M;
+    const int left = (int)min(M - mw, (int64_t)kTile);
+    int hot[4];  // the label's place among this lane's entries
+    float factor[4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const int64_t n = nw + 32 * nt;
-      const HeadColumn c = p.cols[n];  // whole tiles: zeros behind the live rows
-      const int64_t d = c.label < 0 ? -1 : c.label - (p.v0 + mw);
+      const HeadColumn c = p.cols[nw + 32 * nt];  // whole tiles: zeros behind the live rows
+      const int64_t away = c.label - (p.v0 + mw);
+      hot[nt] = c.label < 0 || away < 0 || away >= kTile ? -1 : (int)away;
+      factor[nt] = c.factor;
 #pragma unroll
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const bool in = mw + 32 * mt + 8 * (e >> 2) + (e & 3) < M && c.label >= 0;
-          acc[mt][nt][e] =
-              in ? exp2_fast(fmaf(acc[mt][nt][e], p.scale, -c.most) * kLog2e) * c.over : 0.0f;
+          const float v = exp2_fast(fmaf(acc[mt][nt][e], p.scale, -c.most) * kLog2e) * c.over;
+          acc[mt][nt][e] = c.label >= 0 ? v : 0.0f;
         }
-      // The values in bf16, or what those lost.
-      const auto put = [&](uint16_t* to, int64_t ld, int64_t cols_end, int64_t rows_end, bool lost) {
+    }
+    if (!whole) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            if (32 * mt + 8 * (e >> 2) + (e & 3) >= left) acc[mt][nt][e] = 0.0f;
+    }
+    const int part = lane & 15, row0 = lane >> 4;
+    // One term: bf16 in LDS, 64 rows at a time.
+    const auto put_one = [&](uint16_t* at, int64_t ld, int rows, bool in) __attribute__((always_inline)) {
+      at += (nwave + row0) * ld + mwave + 8 * part;
+#pragma unroll
+      for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          uint16_t* const to = own + (32 * n + i) * 128 + 4 * h;
+#pragma unroll
+          for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const f32x16_t& v = acc[mt][2 * pass + n];
+              *reinterpret_cast<u32x2_t*>(to + 8 * ((4 * mt + g) ^ (i & 15))) =
+                  term_of<0>(v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]);
+            }
+        }
+#pragma unroll 4
+        for (int r = 0; r < 16; ++r) {
+          const int row = row0 + 4 * r;
+          const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * 128 + 8 * (part ^ (row & 15)));
+          if (in && 64 * pass + row < rows) *reinterpret_cast<u32x4_t*>(at) = v;
+          at += 4 * ld;
+        }
+      }
+    };
+    // Three terms: fp32 in LDS, 32 rows at a time, split when they are read back.
+    const auto put_three = [&](uint16_t* at, int64_t plane, int64_t ld, int rows, bool in) __attribute__((always_inline)) {
+      f32x4_t* const lds = reinterpret_cast<f32x4_t*>(own);
+      at += (nwave + row0) * ld + mwave + 8 * part;
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
             const f32x16_t& v = acc[mt][nt];
-            u32x2_t q = {pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
-            if (lost)
-              q = u32x2_t{pack_bf16x2(v[4 * g] - bf16_lo(q[0]), v[4 * g + 1] - bf16_hi(q[0])),
-                          pack_bf16x2(v[4 * g + 2] - bf16_lo(q[1]), v[4 * g + 3] - bf16_hi(q[1]))};
-            *reinterpret_cast<u32x2_t*>(&own[i * 128 + 8 * ((4 * mt + g) ^ (i & 15)) + 4 * h]) = q;
+            lds[i * 32 + ((8 * mt + 2 * g + h) ^ i)] =
+                f32x4_t{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
           }
-#pragma unroll
+#pragma unroll 2
         for (int r = 0; r < 8; ++r) {
-          const int row = 4 * r + (lane >> 4), part = lane & 15;
-          const u32x4_t q = *reinterpret_cast<const u32x4_t*>(&own[row * 128 + 8 * (part ^ (row & 15))]);
-          const int64_t at = n0 + 128 * wn + 32 * nt + row, v = mwave + 8 * part;
-          if (at < rows_end && v < cols_end) *reinterpret_cast<u32x4_t*>(to + at * ld + v) = q;
+          const int row = row0 + 4 * r;
+          const f32x4_t x = lds[row * 32 + ((2 * part) ^ row)], y = lds[row * 32 + ((2 * part + 1) ^ row)];
+          if (in && 32 * nt + row < rows) {
+            const auto store = [&](uint16_t* to, u32x2_t a, u32x2_t b) {
+              *reinterpret_cast<u32x4_t*>(to) = u32x4_t{a[0], a[1], b[0], b[1]};
+            };
+            store(at, term_of<0>(x[0], x[1], x[2], x[3]), term_of<0>(y[0], y[1], y[2], y[3]));
+            store(at + plane, term_of<1>(x[0], x[1], x[2], x[3]), term_of<1>(y[0], y[1], y[2], y[3]));
+            store(at + 2 * plane, term_of<2>(x[0], x[1], x[2], x[3]), term_of<2>(y[0], y[1], y[2], y[3]));
+          }
+          at += 4 * ld;
         }
-      };
-      if (p.P)
-        for (int term = 0; term < p.p_terms; ++term)
-          put(p.P + term * phalf, p.ldp, phalf, N, term > 0);
-      if (p.Q) {
+      }
+    };
+    const auto put = [&](uint16_t* to, int64_t plane, int terms, int64_t ld, int rows, bool in) __attribute__((always_inline)) {
+      if (kTerms > 1 && terms > 1)
+        put_three(to, plane, ld, rows, in);
+      else
+        put_one(to, ld, rows, in);
+    };
+    if (p.P)
+      put(p.P, phalf, p.p_terms, p.ldp, (int)min(N - nwave, (int64_t)128), mwave + 8 * part < phalf);
+    if (p.Q) {
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            acc[mt][nt][e] =
-                (acc[mt][nt][e] - (d == 32 * mt + 8 * (e >> 2) + (e & 3) ? 1.0f : 0.0f)) * c.factor;
-        for (int term = 0; term < p.q_terms; ++term)
-          put(p.Q + term * p.q_plane, p.ldq, p.ldq, qhalf, term > 0);
-      }
+            acc[mt][nt][e] = (acc[mt][nt][e] - (hot[nt] == 32 * mt + 8 * (e >> 2) + (e & 3) ? 1.0f : 0.0f)) *
+                             factor[nt];
+      put(p.Q, p.q_plane, p.q_terms, p.ldq, (int)min(qhalf - nwave, (int64_t)128),
+          mwave + 8 * part < p.ldq);
     }
   } else if constexpr (kMode == kDx) {
     // The sums in the order of the registers, 16 bytes a thread: tile by tile,
@@ -710,15 +797,15 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         }
     }
   } else {
-    uint16_t* const own = w == 0 ? sb0 : w == 1 ? sb1 : w == 2 ? sb2 : sb3;
     const int64_t mwave = m0 + 128 * wm, nwave = n0 + 128 * wn;
-    char* const lds = reinterpret_cast<char*>(own);
-    if (!p.dw_bf16)
-      put_dw<false, true>(acc, lds, p, mwave, nwave, lane);
-    else if (p.accumulate)
-      put_dw<true, true>(acc, lds, p, mwave, nwave, lane);
-    else
-      put_dw<true, false>(acc, lds, p, mwave, nwave, lane);
+    if constexpr (kTerms == 1) {  // bf16, not added to anything
+      put_dw<true, false>(acc, own, p, mwave, nwave, lane);
+    } else {
+      if (p.dw_bf16)
+        put_dw<true, true>(acc, own, p, mwave, nwave, lane);
+      else
+        put_dw<false, true>(acc, own, p, mwave, nwave, lane);
+    }
   }
 }
 
@@ -799,7 +886,7 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
     w[e] = n == E ? load_vec<true, E>(from) : load_part<true, E>(from, n);
   }
   const int tiles_n = ceil_tile(a.K), tiles = ceil_tile(live) * tiles_n;
-  const int splits = dx_splits(tiles, a.pairs);
+  const int splits = a.count[1];
   const int r = j % kTile, c = (int)(k % kTile);
   const int tid = ((r / 128) * 2 + c / 128) * 64 + ((r / 4) % 2) * 32 + c % 32;
   const int reg = ((r % 128 / 32) * 4 + c % 128 / 32) * 4 + r % 32 / 8;
@@ -826,9 +913,9 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
 unsigned blocks_of(int64_t n) { return (unsigned)((n + 255) / 256); }
 int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 
-template <int kMode>
+template <int kMode, int kTerms = 1>
 hipError_t tiles(const HeadTiles& a, int64_t grid, hipStream_t st) {
-  hipLaunchKernelGGL(head_tile_kernel<kMode>, dim3((unsigned)grid), dim3(256), 0, st, a);
+  hipLaunchKernelGGL((head_tile_kernel<kMode, kTerms>), dim3((unsigned)grid), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
@@ -862,7 +949,8 @@ hipError_t launch_head_stats(const HeadTiles& a, hipStream_t st) {
 }
 
 hipError_t launch_head_probs(const HeadTiles& a, hipStream_t st) {
-  return tiles<kProbs>(a, tiles_of(a.vocab) * tiles_of(a.rows_most), st);
+  const int64_t grid = tiles_of(a.vocab) * tiles_of(a.rows_most);
+  return a.p_terms > 1 || a.q_terms > 1 ? tiles<kProbs, 3>(a, grid, st) : tiles<kProbs>(a, grid, st);
 }
 
 hipError_t launch_head_dx(const HeadTiles& a, hipStream_t st) {
@@ -870,7 +958,8 @@ hipError_t launch_head_dx(const HeadTiles& a, hipStream_t st) {
 }
 
 hipError_t launch_head_dw(const HeadTiles& a, hipStream_t st) {
-  return tiles<kDw>(a, tiles_of(a.vocab) * tiles_of(a.K), st);
+  const int64_t grid = tiles_of(a.vocab) * tiles_of(a.K);
+  return a.accumulate || !a.dw_bf16 ? tiles<kDw, 3>(a, grid, st) : tiles<kDw>(a, grid, st);
 }
 
 hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,

@@ -42,12 +42,12 @@ void rows_layout(Layout& L, Carve& c, int64_t M, int64_t K) {
   L.Kp = up(K, kStep);
   L.map = c.take((size_t)M * 4);
   L.inv = c.take((size_t)M * 4);
-  L.count = c.take(4);
+  L.count = c.take(8);
   L.cols = c.take((size_t)L.rows_pad * sizeof(HeadColumn));
   L.xs = c.take((size_t)L.rows_pad * L.Kp * 2);
 }
 
-int64_t few_parts(int64_t V) { return (V + kFewEntries - 1) / kFewEntries; }
+int64_t few_parts(int64_t V) { return (V + few_entries(V) - 1) / few_entries(V); }
 
 Layout fwd_layout(int64_t M, int64_t V, int64_t K, bool copy) {
   Layout L;
@@ -78,7 +78,8 @@ int64_t piece_of(int64_t M, int64_t V, bool copy) {
   return up((V + pieces - 1) / pieces, kTile);
 }
 
-int terms(int dtype) { return dtype == QLORA_DTYPE_F32 ? 2 : 1; }
+// bf16 numbers that a probability or a logit's gradient is split into.
+int terms(int dtype) { return dtype == QLORA_DTYPE_F32 ? 3 : 1; }
 
 // dx, dw: the outputs' types, negative for one that is not wanted.
 Layout bwd_layout(int64_t M, int64_t V, int64_t K, bool copy, int dx, int dw) {
@@ -142,6 +143,7 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     f.M = M;
     f.K = K;
     f.vocab = V;
+    f.entries = few_entries(V);
     f.scale = scale;
     f.labels = labels;
     f.ids64 = ids_dtype == QLORA_DTYPE_I64;
@@ -245,6 +247,10 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   r.scale = scale;
   r.M = M;
   r.V = V;
+  r.K = K;
+  // The first piece's pairs of steps decide the splits, so that every piece adds to
+  // the same sums.
+  r.pairs = dX ? (int)(up(V < L.piece ? V : L.piece, 2 * kStep) / (2 * kStep) * terms(dx_dtype)) : 0;
   r.map = at<int32_t>(workspace, L.map);
   r.inv = at<int32_t>(workspace, L.inv);
   r.count = at<int32_t>(workspace, L.count);
@@ -269,7 +275,6 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   t.ldp = L.piece * t.p_terms;
   t.ldq = L.piece;
   t.q_plane = L.rows_pad * L.piece;
-  t.pairs = (int)(up(V < L.piece ? V : L.piece, 2 * kStep) / (2 * kStep) * t.p_terms);
   t.acc = at<float>(workspace, L.acc);
   t.dW = dW;
   t.dw_bf16 = grad_dtype == QLORA_DTYPE_BF16;
@@ -301,6 +306,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
       f.K = K;
       f.v0 = v0;
       f.vocab = t.vocab;
+      f.entries = few_entries(t.vocab);
       f.scale = scale;
       f.map = r.map;
       f.count = r.count;
@@ -336,7 +342,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     }
   }
   if (e == hipSuccess && dX) {
-    const HeadDx d{t.acc, t.pairs, r.map, r.inv, r.count, r.cols, W, ldw, M, K, dX, lddx};
+    const HeadDx d{t.acc, r.map, r.inv, r.count, r.cols, W, ldw, M, K, dX, lddx};
     e = launch_head_dx_finish(d, dx_dtype == QLORA_DTYPE_BF16, st);
   }
   return launch_status(e);

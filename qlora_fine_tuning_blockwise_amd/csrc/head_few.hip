@@ -20,9 +20,6 @@ namespace {
 constexpr float kLog2e = 1.44269504088896340736f;
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kEntries = 16 * kWaves;  // of the vocabulary, a workgroup
-static_assert(kEntries == kFewEntries, "a workgroup's entries");
 constexpr int kFrags = 8, kChunk = 32 * kFrags;  // fragments and elements of a chunk of K
 
 __device__ __forceinline__ u32x4_t words(const Vec<true, 8>& v) {
@@ -34,9 +31,11 @@ __device__ __forceinline__ Vec<true, 8> load_upto(const uint16_t* p, int64_t k, 
   return n == 8 ? load_vec<true, 8>(p + k) : load_part<true, 8>(p + k, n);
 }
 
-// NT groups of 16 rows.
-template <int NT, bool kProbs>
-__global__ __launch_bounds__(kThreads) void head_few_kernel(HeadFew p) {
+// NT groups of 16 rows, kWaves waves.
+template <int NT, int kWaves, bool kProbs>
+__global__ __launch_bounds__(64 * kWaves) void head_few_kernel(HeadFew p) {
+  constexpr int kThreads = 64 * kWaves, kEntries = 16 * kWaves;  // of the vocabulary
+  constexpr int kBring = NT * 16 * 32 / kThreads, kRows = kThreads / 32;  // parts of x a thread, rows apart
   // A row's chunk is 512 bytes, 16-byte part c of row r at c ^ (r & 7).
   __shared__ __attribute__((aligned(16))) uint16_t xs[2][16 * NT * kChunk];
   __shared__ float2 red[kProbs ? 1 : kWaves * 16 * NT];
@@ -46,30 +45,32 @@ __global__ __launch_bounds__(kThreads) void head_few_kernel(HeadFew p) {
   const int64_t K = p.K;
   // This lane's row of W; past the piece the last one, whose results are not used.
   const uint16_t* wrow = p.W + (v0 + i < p.vocab ? v0 + i : p.vocab - 1) * p.ldw;
-  // Parts of x's chunk that this thread brings: rows r, r + 16, ... (past the last
-  // row that one, whose results are not used)
+  // Parts of x's chunk that this thread brings: rows r, r + kRows, ... (past the
+  // last row that one, whose results are not used).
   const int xr = threadIdx.x / 32, xc = threadIdx.x % 32;
-  const uint16_t* xrow[NT];
+  const uint16_t* xrow[kBring];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int j = 16 * t + xr < rows ? 16 * t + xr : rows > 0 ? rows - 1 : 0;
+  for (int t = 0; t < kBring; ++t) {
+    const int j = kRows * t + xr < rows ? kRows * t + xr : rows > 0 ? rows - 1 : 0;
     xrow[t] = p.x + (kProbs ? (int64_t)(rows > 0 ? p.map[j] : 0) : (int64_t)j) * p.ldx;
   }
   // Two chunks in flight: chunk c in set c % 2.
-  Vec<true, 8> wv[2][kFrags], xv[2][NT];
+  Vec<true, 8> wv[2][kFrags], xv[2][kBring];
   const auto load = [&](int c, auto sc) {  // x first: it is waited for while W is in flight
     constexpr int S = decltype(sc)::value;
     const int64_t k0 = (int64_t)c * kChunk;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xv[S][t] = load_vec<true, 8>(xrow[t] + k0 + 8 * xc);
+    for (int t = 0; t < kBring; ++t) xv[S][t] = load_vec<true, 8>(xrow[t] + k0 + 8 * xc);
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) wv[S][f] = load_vec<true, 8, !kProbs>(wrow + k0 + 32 * f + 8 * g);
   };
   const auto put_x = [&](auto sc) {
     constexpr int S = decltype(sc)::value;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      *reinterpret_cast<u32x4_t*>(&xs[S][(16 * t + xr) * kChunk + 8 * (xc ^ (xr & 7))]) = words(xv[S][t]);
+    for (int t = 0; t < kBring; ++t) {
+      const int r = kRows * t + xr;
+      *reinterpret_cast<u32x4_t*>(&xs[S][r * kChunk + 8 * (xc ^ (r & 7))]) = words(xv[S][t]);
+    }
   };
   // LDS written by every wave; loads from memory may still fly.
   const auto meet_waves = [] {
@@ -132,7 +133,7 @@ __global__ __launch_bounds__(kThreads) void head_few_kernel(HeadFew p) {
   }
   if (const int64_t k0 = (int64_t)chunks * kChunk; k0 < K) {  // the rest, masked
 #pragma unroll
-    for (int t = 0; t < NT; ++t) xv[0][t] = load_upto(xrow[t], k0 + 8 * xc, K);
+    for (int t = 0; t < kBring; ++t) xv[0][t] = load_upto(xrow[t], k0 + 8 * xc, K);
 #pragma unroll
     for (int f = 0; f < kFrags; ++f) wv[0][f] = load_upto(wrow, k0 + 32 * f + 8 * g, K);
     meet_waves();  // the last chunk may have been read from this buffer
@@ -242,16 +243,24 @@ __global__ __launch_bounds__(256) void head_few_loss_kernel(const float2* part, 
   }
 }
 
+// Eight waves, or two where those leave CUs idle: a workgroup's loads reach some
+// 35 GB/s on a CU (2048 x 5696, 4 rows: 16 workgroups of eight waves 44 us).
+template <int NT, bool kProbs>
+hipError_t few_rows(const HeadFew& a, hipStream_t st) {
+  // Probabilities are written up to two whole steps of the product behind them.
+  const int64_t to = kProbs ? (a.vocab + 63) / 64 * 64 : a.vocab;
+  const dim3 grid((unsigned)((to + a.entries - 1) / a.entries));
+  if (a.entries == 128)
+    hipLaunchKernelGGL((head_few_kernel<NT, 8, kProbs>), grid, dim3(512), 0, st, a);
+  else
+    hipLaunchKernelGGL((head_few_kernel<NT, 2, kProbs>), grid, dim3(128), 0, st, a);
+  return hipGetLastError();
+}
+
 template <bool kProbs>
 hipError_t few(const HeadFew& a, hipStream_t st) {
-  const dim3 grid((unsigned)((a.vocab + kEntries - 1) / kEntries)), block(kThreads);
-  if (a.M <= 16)
-    hipLaunchKernelGGL((head_few_kernel<1, kProbs>), grid, block, 0, st, a);
-  else if (a.M <= 32)
-    hipLaunchKernelGGL((head_few_kernel<2, kProbs>), grid, block, 0, st, a);
-  else
-    hipLaunchKernelGGL((head_few_kernel<4, kProbs>), grid, block, 0, st, a);
-  return hipGetLastError();
+  if (a.M <= 16) return few_rows<1, kProbs>(a, st);
+  return a.M <= 32 ? few_rows<2, kProbs>(a, st) : few_rows<4, kProbs>(a, st);
 }
 
 }  // namespace

@@ -7,14 +7,23 @@
 
 namespace qlora {
 
-// Four values in bf16, and with two terms what they lost, `plane` elements on.
+// Term kTerm of four values that are written as sums of bf16 numbers: each is the
+// nearest to what those before it leave.
+template <int kTerm>
+__device__ __forceinline__ u32x2_t term_of(float a, float b, float c, float d) {
+  u32x2_t q = {pack_bf16x2(a, b), pack_bf16x2(c, d)};
+  if constexpr (kTerm > 0) {
+    q = term_of<kTerm - 1>(a - bf16_lo(q[0]), b - bf16_hi(q[0]), c - bf16_lo(q[1]), d - bf16_hi(q[1]));
+  }
+  return q;
+}
+
+// One term, or all three, `plane` elements apart.
 __device__ __forceinline__ void store_terms(uint16_t* to, int64_t plane, int terms, const float (&v)[4]) {
-  const u32x2_t hi = {pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-  *reinterpret_cast<u32x2_t*>(to) = hi;
-  if (terms == 2)
-    *reinterpret_cast<u32x2_t*>(to + plane) =
-        u32x2_t{pack_bf16x2(v[0] - bf16_lo(hi[0]), v[1] - bf16_hi(hi[0])),
-                pack_bf16x2(v[2] - bf16_lo(hi[1]), v[3] - bf16_hi(hi[1]))};
+  *reinterpret_cast<u32x2_t*>(to) = term_of<0>(v[0], v[1], v[2], v[3]);
+  if (terms == 1) return;
+  *reinterpret_cast<u32x2_t*>(to + plane) = term_of<1>(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<u32x2_t*>(to + 2 * plane) = term_of<2>(v[0], v[1], v[2], v[3]);
 }
 
 }  // namespace qlora
