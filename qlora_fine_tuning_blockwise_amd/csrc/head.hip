@@ -848,13 +848,13 @@ __global__ __launch_bounds__(256) void head_loss_kernel(const float2* part, int6
   }
 }
 
-// Four rows a workgroup, four columns a thread: of live rows 4y .. 4y + 3 in the
+// Four rows a workgroup, four columns a thread: of live rows 4x .. 4x + 3 in the
 // first half of the grid, whose sums lie as head_tile_kernel's registers had
 // them, and of rows that carry no loss in the second half.
 template <bool kBf16>
 __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
   constexpr int E = 4;
-  const int64_t k = ((int64_t)blockIdx.x * 256 + threadIdx.x) * E;
+  const int64_t k = ((int64_t)blockIdx.y * 256 + threadIdx.x) * E;
   if (k >= a.K) return;
   const int n = count_below<E>(k, a.K);
   const auto put = [&](int64_t row, const float (&v)[E]) {
@@ -865,15 +865,15 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
       store_part<kBf16, E>(to, v, n);
   };
   const int64_t groups = (a.M + 3) / 4;
-  if ((int64_t)blockIdx.y >= groups) {
-    const int64_t m = ((int64_t)blockIdx.y - groups) * 4;
+  if ((int64_t)blockIdx.x >= groups) {
+    const int64_t m = ((int64_t)blockIdx.x - groups) * 4;
     const float none[E] = {0.0f, 0.0f, 0.0f, 0.0f};
     for (int e = 0; e < 4; ++e)
       if (m + e < a.M && a.inv[m + e] < 0) put(m + e, none);
     return;
   }
   const int live = *a.count;
-  const int j = (int)blockIdx.y * 4;
+  const int j = (int)blockIdx.x * 4;
   if (j >= live) return;
   // The labels' rows of W, requested before the sums.
   HeadColumn col[4];
@@ -971,7 +971,7 @@ hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
 }
 
 hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st) {
-  const dim3 grid(blocks_of((a.K + 3) / 4), (unsigned)((a.M + 3) / 4 * 2));
+  const dim3 grid((unsigned)((a.M + 3) / 4 * 2), blocks_of((a.K + 3) / 4));  // rows past the second dimension's 65535
   if (bf16)
     hipLaunchKernelGGL(head_dx_finish_kernel<true>, grid, dim3(256), 0, st, a);
   else

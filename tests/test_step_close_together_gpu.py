@@ -138,6 +138,36 @@ def test_a_replayed_graph_follows_its_labels():
             assert torch.equal(got[k], eager[k]), (share, k)
 
 
+def test_tensors_without_a_list_are_captured_with_their_launch():
+    """Plain tensors travel in the launches' arguments: a replay needs nothing of
+    the call that captured them but the tensors."""
+    g = np.random.default_rng(4)
+    made = [randn(g, 3 * k + 1, (F32, BF16)[k % 2]).to(DEV) for k in range(200)]
+    out = [torch.empty_like(t) for t in made]
+
+    def run():
+        r = q.qlora_grad_norm(made, 1.0)
+        q.qlora_grad_scale(made, r[1:], out=out)
+        return r
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = run()
+    for replay in range(3):
+        for t in made:
+            t.mul_(1.5)
+        for t in out:
+            t.fill_(9.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        got, result = [t.clone() for t in out], r.clone()
+        eager = run()
+        torch.cuda.synchronize()
+        assert torch.equal(result, eager) and all(torch.equal(a, b) for a, b in zip(got, out)), replay
+        assert float(result[1]) < 1
+
+
 def test_two_streams_at_once():
     """Two independent steps on two streams, launched in turn without waits, and
     the stream argument in the place of the current stream."""
@@ -167,11 +197,13 @@ def test_two_streams_at_once():
     assert abs(float(r[0]) - n) <= 2.0 ** -22 * n
 
 
-def test_many_rows_of_a_long_batch():
-    """More rows than a thread of the one workgroup that gathers them has, most
-    without a label; their losses and gradients as the same rows' alone."""
+@pytest.mark.parametrize("M", [20011, 140003])
+def test_many_rows_of_a_long_batch(M):
+    """More rows than threads in the one workgroup that gathers them, and than a
+    grid's second dimension has places for, most without a label; their losses
+    and gradients as the same rows' alone."""
     g = np.random.default_rng(8)
-    M, V, K = 20011, 515, 64
+    V, K = 515, 64
     x, W = randn(g, (M, K), BF16).to(DEV), randn(g, (V, K), BF16, 0.25).to(DEV)
     labels = torch.from_numpy(np.where(g.random(M) < 0.8, -100, g.integers(0, V, M))).to(DEV)
     dloss = randn(g, M).to(DEV)
