@@ -337,6 +337,11 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
   const int ks0 = split * per;
   const int nsteps = kMode == kDx ? min(per, all - ks0) : all;
 
+  // Where the fragments of this wave lie in the tile. A wave takes 128 x 128; along the
+  // live rows that is every other 32 of them, so that a tile that ends early is
+  // less work for all waves.
+  const auto a_at = [&](int mt) { return kMode == kDx ? 64 * mt + 32 * wm : 32 * mt + 128 * wm; };
+  const auto b_at = [&](int nt) { return kMode == kStats || kMode == kProbs ? 64 * nt + 32 * wn : 32 * nt + 128 * wn; };
   f32x16_t acc[4][4];
 #pragma unroll
   for (int mt = 0; mt < 4; ++mt)
@@ -351,10 +356,10 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     const int64_t k0 = (int64_t)ks0 * kStep;
     typedef __attribute__((address_space(3))) void lds_void;
     // Direct-to-LDS roles. rows: wave w loads rows 64w + 8q + L/8 (q = 0..7) of
-    // each pair, lane L at LDS position L%8; rows past the matrix read its last
-    // row. steps: wave w loads windows 4w .. 4w+3 (16 rows each) of each step;
-    // there are whole tiles. columns: wave w loads rows 8w + 2q + L/32 (q = 0..3)
+    // each pair, lane L at LDS position L%8. steps: wave w loads windows 4w .. 4w+3 (16 rows each) of each step.
+    // Of both, rows past the matrix lie past the buffer and read zeros. columns: wave w loads rows 8w + 2q + L/32 (q = 0..3)
     // of each step, lane L at position L%32.
+    constexpr uint32_t kNoRow = 0x80000000u;
     uint32_t aoff[8], boff[4];
     const int crow = 8 * w + (lane >> 5);  // of the first load; the others 2 rows on each
     const auto chunk_of = [&](int row) { return (lane & 31) ^ (2 * ((row & 3) ^ ((row & 1) << 2))); };
@@ -362,9 +367,8 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     for (int q = 0; q < 8; ++q) {
       const int row = 64 * w + 8 * q + (lane >> 3);
       const int c = (lane & 7) ^ ((row >> 1) & 7);
-      const int64_t ar = m0 + row < M ? row : M - 1 - m0;
       if constexpr (!kACols)
-        aoff[q] = (uint32_t)(ar * p.lda * 2 + 16 * c);
+        aoff[q] = m0 + row < M ? (uint32_t)(row * p.lda * 2 + 16 * c) : kNoRow;
       else if (q < 4)
         aoff[q] = (uint32_t)((crow + 2 * q) * p.lda * 2 + 16 * chunk_of(crow + 2 * q));
     }
@@ -375,7 +379,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
       if constexpr (kBCols)
         boff[j] = (uint32_t)((crow + 2 * j) * p.ldb * 2 + 16 * chunk_of(crow + 2 * j));
       else
-        boff[j] = (uint32_t)(row * 64 + 16 * c);
+        boff[j] = n0 + row < N ? (uint32_t)(row * 64 + 16 * c) : kNoRow;
     }
     // rows: a ends with its last row's last step; what a final odd pair has past
     // it in that row reads zeros (in other rows the next row; it is not used).
@@ -421,38 +425,38 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
                      ks - term * half);
     };
     // Fragment reads. rows: fragment (mt, step half par, substep s) is tile row
-    // 128wm + 32mt + i, chunk 4par + 2s + h, at position chunk ^ ((i >> 1) & 7).
-    // steps: (nt, s) is tile row 128wn + 32nt + i, chunk 2s + h at (2s + h) ^
+    // a_at(mt) + i, chunk 4par + 2s + h, at position chunk ^ ((i >> 1) & 7).
+    // steps: (nt, s) is tile row b_at(nt) + i, chunk 2s + h at (2s + h) ^
     // ((i >> 2) & 3). columns: lane 16q + l reads rows 16s + 8(q/2) + l/4 (and 4
-    // on), 8 bytes at columns 128wn + 32nt + 16(q%2) + 4(l%4).
+    // on), 8 bytes at columns b_at(nt) + 16(q%2) + 4(l%4).
     const int swa = (i >> 1) & 7, swb = (i >> 2) & 3;
     int fa[2][2];
 #pragma unroll
     for (int par = 0; par < 2; ++par)
 #pragma unroll
       for (int ss = 0; ss < 2; ++ss)
-        fa[par][ss] = (128 * wm + i) * 64 + 8 * ((4 * par + 2 * ss + h) ^ swa);
-    const int fb0 = (128 * wn + i) * 32 + 8 * (h ^ swb);
-    const int fb1 = (128 * wn + i) * 32 + 8 * ((2 + h) ^ swb);
+        fa[par][ss] = (a_at(0) + i) * 64 + 8 * ((4 * par + 2 * ss + h) ^ swa);
+    const int fb0 = (b_at(0) + i) * 32 + 8 * (h ^ swb);
+    const int fb1 = (b_at(0) + i) * 32 + 8 * ((2 + h) ^ swb);
     const int trow = 8 * h + ((lane >> 2) & 3), tg = 2 * ((trow & 3) ^ ((trow & 1) << 2));
     int ca[4], cb[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int c = 4 * t + 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
-      ca[t] = trow * kTile + 8 * ((16 * wm + c) ^ tg) + 4 * (lane & 1);
-      cb[t] = trow * kTile + 8 * ((16 * wn + c) ^ tg) + 4 * (lane & 1);
+      const int c = 2 * ((lane >> 4) & 1) + ((lane >> 1) & 1);
+      ca[t] = trow * kTile + 8 * ((a_at(t) / 8 + c) ^ tg) + 4 * (lane & 1);
+      cb[t] = trow * kTile + 8 * ((b_at(t) / 8 + c) ^ tg) + 4 * (lane & 1);
     }
     const auto frag_a = [&](const uint16_t* s, int t, int par, int ss) {
       if constexpr (kACols)
         return read_columns(s + ca[t] + 16 * ss * kTile);
       else
-        return *reinterpret_cast<const u32x4_t*>(s + fa[par][ss] + 2048 * t);
+        return *reinterpret_cast<const u32x4_t*>(s + fa[par][ss] + (a_at(1) - a_at(0)) * 64 * t);
     };
     const auto frag_b = [&](const uint16_t* s, int t, int ss) {
       if constexpr (kBCols)
         return read_columns(s + cb[t] + 16 * ss * kTile);
       else
-        return *reinterpret_cast<const u32x4_t*>(s + (ss ? fb1 : fb0) + 1024 * t);
+        return *reinterpret_cast<const u32x4_t*>(s + (ss ? fb1 : fb0) + (b_at(1) - b_at(0)) * 32 * t);
     };
 
     // Prologue: what steps 0 and 1 read, then a's pair 1 or step 2 and b's step
@@ -486,118 +490,133 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     wait_vmem_lgkm0<kACols ? 8 : 12>();
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    u32x4_t a0[4], b0[4], a1[4], b1[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      a0[t] = frag_a(sa0, t, 0, 0);
-      b0[t] = frag_b(sb0, t, 0);
-    }
     constexpr int kAReads = kACols ? 2 : 1, kBReads = kBCols ? 2 : 1;
-    // One step kb (stage kb % 4 = SB, pair slot (kb / 2) % 3 = SA, half PAR):
-    // substep 0 computes on (a0, b0) while (kb, 1) is read into (a1, b1);
-    // substep 1 computes on (a1, b1) while (kb+1, 0) is read into (a0, b0). One
-    // load after every fourth MFMA: b of step kb+3 in substep 0, a of pair kb/2 + 2
-    // or of step kb+3 in substep 1.
-    auto step = [&](int kb, auto sbc, auto sac, auto parc) {
-      constexpr int SB = decltype(sbc)::value, SA = decltype(sac)::value;
-      constexpr int PAR = decltype(parc)::value;
-      constexpr int SA1 = PAR ? (SA + 1) % 3 : SA;  // slot of step kb+1
-      constexpr int PAR1 = PAR ^ 1;
-      constexpr int kACur = kACols ? SB : SA, kANxt = kACols ? (SB + 1) % 4 : SA1;
-      constexpr int kALd = kACols ? (SB + 3) % 4 : (SA + 2) % 3;
-      uint16_t* const acur = pick<kACur>(sa);
-      uint16_t* const anxt = pick<kANxt>(sa);
-      uint16_t* const ald = pick<kALd>(sa);
-      uint16_t* const bcur = pick<SB>(sb);
-      uint16_t* const bnxt = pick<(SB + 1) % 4>(sb);
-      uint16_t* const bld = pick<(SB + 3) % 4>(sb);
-      Window bnew{nullptr, 0}, anew{nullptr, 0};
-      if constexpr (kBCols) bnew = from_b(kb + 3);
-      if constexpr (kACols) anew = from_a(kb + 3);
+    const auto product = [&](auto mfc, auto nfc) __attribute__((always_inline)) {
+      constexpr int MF = decltype(mfc)::value, NF = decltype(nfc)::value;
+      constexpr int kMfmas = MF * NF, kBoth = MF < NF ? MF : NF, kReads = MF + NF;
+      static_assert(kMfmas % 4 == 0 && kReads <= kMfmas, "a read and a load after some MFMA each");
+      u32x4_t a0[MF], b0[NF], a1[MF], b1[NF];
 #pragma unroll
-      for (int g = 0; g < 16; ++g) {
-        const int mt = g >> 2, nt = g & 3;
-        acc[mt][nt] = mfma_32x32x16(a0[mt], b0[nt], acc[mt][nt]);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (g < 8) {
-          const int t = g >> 1;
-          if (g & 1) {
-            b1[t] = frag_b(bcur, t, 1);
-            __builtin_amdgcn_sched_group_barrier(0x100, kBReads, 0);
-          } else {
-            a1[t] = frag_a(acur, t, PAR, 1);
-            __builtin_amdgcn_sched_group_barrier(0x100, kAReads, 0);
+      for (int t = 0; t < MF; ++t) a0[t] = frag_a(sa0, t, 0, 0);
+#pragma unroll
+      for (int t = 0; t < NF; ++t) b0[t] = frag_b(sb0, t, 0);
+      // One step kb (stage kb % 4 = SB, pair slot (kb / 2) % 3 = SA, half PAR):
+      // substep 0 computes on (a0, b0) while (kb, 1) is read into (a1, b1);
+      // substep 1 computes on (a1, b1) while (kb+1, 0) is read into (a0, b0). One
+      // load after every quarter of the MFMAs: b of step kb+3 in substep 0, a of pair kb/2 + 2
+      // or of step kb+3 in substep 1.
+      auto step = [&](int kb, auto sbc, auto sac, auto parc) __attribute__((always_inline)) {
+        constexpr int SB = decltype(sbc)::value, SA = decltype(sac)::value;
+        constexpr int PAR = decltype(parc)::value;
+        constexpr int SA1 = PAR ? (SA + 1) % 3 : SA;  // slot of step kb+1
+        constexpr int PAR1 = PAR ^ 1;
+        constexpr int kACur = kACols ? SB : SA, kANxt = kACols ? (SB + 1) % 4 : SA1;
+        constexpr int kALd = kACols ? (SB + 3) % 4 : (SA + 2) % 3;
+        uint16_t* const acur = pick<kACur>(sa);
+        uint16_t* const anxt = pick<kANxt>(sa);
+        uint16_t* const ald = pick<kALd>(sa);
+        uint16_t* const bcur = pick<SB>(sb);
+        uint16_t* const bnxt = pick<(SB + 1) % 4>(sb);
+        uint16_t* const bld = pick<(SB + 3) % 4>(sb);
+        Window bnew{nullptr, 0}, anew{nullptr, 0};
+        if constexpr (kBCols) bnew = from_b(kb + 3);
+        if constexpr (kACols) anew = from_a(kb + 3);
+#pragma unroll
+        for (int g = 0; g < kMfmas; ++g) {
+          const int mt = g / NF, nt = g % NF;
+          acc[mt][nt] = mfma_32x32x16(a0[mt], b0[nt], acc[mt][nt]);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (g < kReads) {
+            const int t = g < 2 * kBoth ? g >> 1 : g - kBoth;
+            if (g < 2 * kBoth ? g & 1 : NF > MF) {
+              b1[t] = frag_b(bcur, t, 1);
+              __builtin_amdgcn_sched_group_barrier(0x100, kBReads, 0);
+            } else {
+              a1[t] = frag_a(acur, t, PAR, 1);
+              __builtin_amdgcn_sched_group_barrier(0x100, kAReads, 0);
+            }
+          }
+          if ((g + 1) % (kMfmas / 4) == 0) {
+            const int q = g / (kMfmas / 4);
+            if constexpr (kBCols)
+              dma_cols(bnew, boff[q], q, bld);
+            else
+              dma_b_steps(q, kb + 3, bld);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
           }
         }
-        if ((g & 3) == 3) {
-          if constexpr (kBCols)
-            dma_cols(bnew, boff[g >> 2], g >> 2, bld);
-          else
-            dma_b_steps(g >> 2, kb + 3, bld);
-          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        }
-      }
-      __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int g = 0; g < 16; ++g) {
-        const int mt = g >> 2, nt = g & 3;
-        acc[mt][nt] = mfma_32x32x16(a1[mt], b1[nt], acc[mt][nt]);
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if (g < 8) {
-          const int t = g >> 1;
-          if (g & 1) {
-            b0[t] = frag_b(bnxt, t, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, kBReads, 0);
-          } else {
-            a0[t] = frag_a(anxt, t, PAR1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x100, kAReads, 0);
+        for (int g = 0; g < kMfmas; ++g) {
+          const int mt = g / NF, nt = g % NF;
+          acc[mt][nt] = mfma_32x32x16(a1[mt], b1[nt], acc[mt][nt]);
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if (g < kReads) {
+            const int t = g < 2 * kBoth ? g >> 1 : g - kBoth;
+            if (g < 2 * kBoth ? g & 1 : NF > MF) {
+              b0[t] = frag_b(bnxt, t, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, kBReads, 0);
+            } else {
+              a0[t] = frag_a(anxt, t, PAR1, 0);
+              __builtin_amdgcn_sched_group_barrier(0x100, kAReads, 0);
+            }
+          }
+          if ((g + 1) % (kMfmas / 4) == 0) {
+            const int q = g / (kMfmas / 4);
+            if constexpr (kACols)
+              dma_cols(anew, aoff[q], q, ald);
+            else
+              dma_a_rows(4 * PAR + q, kb / 2 + 2, ald);
+            __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
           }
         }
-        if ((g & 3) == 3) {
-          if constexpr (kACols)
-            dma_cols(anew, aoff[g >> 2], g >> 2, ald);
-          else
-            dma_a_rows(4 * PAR + (g >> 2), kb / 2 + 2, ald);
-          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
-        }
+        __builtin_amdgcn_sched_barrier(0);
+        // This step's eight loads may still fly; everything earlier has landed.
+        wait_vmem_lgkm0<8>();
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      using I0 = std::integral_constant<int, 0>;
+      using I1 = std::integral_constant<int, 1>;
+      using I2 = std::integral_constant<int, 2>;
+      using I3 = std::integral_constant<int, 3>;
+      // Twelve steps bring all rings back to their first stage and slot.
+      int kb = 0;
+      for (; kb + 12 <= nsteps; kb += 12) {
+        step(kb + 0, I0(), I0(), I0());
+        step(kb + 1, I1(), I0(), I1());
+        step(kb + 2, I2(), I1(), I0());
+        step(kb + 3, I3(), I1(), I1());
+        step(kb + 4, I0(), I2(), I0());
+        step(kb + 5, I1(), I2(), I1());
+        step(kb + 6, I2(), I0(), I0());
+        step(kb + 7, I3(), I0(), I1());
+        step(kb + 8, I0(), I1(), I0());
+        step(kb + 9, I1(), I1(), I1());
+        step(kb + 10, I2(), I2(), I0());
+        step(kb + 11, I3(), I2(), I1());
       }
-      __builtin_amdgcn_sched_barrier(0);
-      // This step's eight loads may still fly; everything earlier has landed.
-      wait_vmem_lgkm0<8>();
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
+      if (kb + 0 < nsteps) step(kb + 0, I0(), I0(), I0());
+      if (kb + 1 < nsteps) step(kb + 1, I1(), I0(), I1());
+      if (kb + 2 < nsteps) step(kb + 2, I2(), I1(), I0());
+      if (kb + 3 < nsteps) step(kb + 3, I3(), I1(), I1());
+      if (kb + 4 < nsteps) step(kb + 4, I0(), I2(), I0());
+      if (kb + 5 < nsteps) step(kb + 5, I1(), I2(), I1());
+      if (kb + 6 < nsteps) step(kb + 6, I2(), I0(), I0());
+      if (kb + 7 < nsteps) step(kb + 7, I3(), I0(), I1());
+      if (kb + 8 < nsteps) step(kb + 8, I0(), I1(), I0());
+      if (kb + 9 < nsteps) step(kb + 9, I1(), I1(), I1());
+      if (kb + 10 < nsteps) step(kb + 10, I2(), I2(), I0());
     };
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
-    using I3 = std::integral_constant<int, 3>;
-    // Twelve steps bring all rings back to their first stage and slot.
-    int kb = 0;
-    for (; kb + 12 <= nsteps; kb += 12) {
-      step(kb + 0, I0(), I0(), I0());
-      step(kb + 1, I1(), I0(), I1());
-      step(kb + 2, I2(), I1(), I0());
-      step(kb + 3, I3(), I1(), I1());
-      step(kb + 4, I0(), I2(), I0());
-      step(kb + 5, I1(), I2(), I1());
-      step(kb + 6, I2(), I0(), I0());
-      step(kb + 7, I3(), I0(), I1());
-      step(kb + 8, I0(), I1(), I0());
-      step(kb + 9, I1(), I1(), I1());
-      step(kb + 10, I2(), I2(), I0());
-      step(kb + 11, I3(), I2(), I1());
-    }
-    if (kb + 0 < nsteps) step(kb + 0, I0(), I0(), I0());
-    if (kb + 1 < nsteps) step(kb + 1, I1(), I0(), I1());
-    if (kb + 2 < nsteps) step(kb + 2, I2(), I1(), I0());
-    if (kb + 3 < nsteps) step(kb + 3, I3(), I1(), I1());
-    if (kb + 4 < nsteps) step(kb + 4, I0(), I2(), I0());
-    if (kb + 5 < nsteps) step(kb + 5, I1(), I2(), I1());
-    if (kb + 6 < nsteps) step(kb + 6, I2(), I0(), I0());
-    if (kb + 7 < nsteps) step(kb + 7, I3(), I0(), I1());
-    if (kb + 8 < nsteps) step(kb + 8, I0(), I1(), I0());
-    if (kb + 9 < nsteps) step(kb + 9, I1(), I1(), I1());
-    if (kb + 10 < nsteps) step(kb + 10, I2(), I2(), I0());
+    using I2f = std::integral_constant<int, 2>;
+    using I4f = std::integral_constant<int, 4>;
+    // Half the fragments where half a tile has no live rows.
+    if (kMode == kDx && M - m0 <= kTile / 2)
+      product(I2f(), I4f());
+    else if (kMode != kDx && kMode != kDw && N - n0 <= kTile / 2)
+      product(I4f(), I2f());
+    else
+      product(I4f(), I4f());
     // Direct-to-LDS loads still in flight must land before LDS is used again or
     // the workgroup ends.
     wait_vmem_lgkm0<0>();
@@ -610,9 +629,9 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
   int tid = threadIdx.x;
   asm volatile("" : "+v"(tid));
   const int lane = tid & 63, i = lane & 31, h = lane >> 5;
-  // Accumulator element e of (mt, nt) is row 32mt + 8(e/4) + 4h + e%4, column
-  // 32nt + i of this wave's 128 x 128 block.
-  const int64_t mw = m0 + 128 * wm + 4 * h, nw = n0 + 128 * wn + i;
+  // Accumulator element e of (mt, nt) is tile row a_at(mt) + 8(e/4) + 4h + e%4, column
+  // b_at(nt) + i.
+  const int64_t mw = m0 + a_at(0) + 4 * h;
   uint16_t* const own = w == 0 ? sb0 : w == 1 ? sb1 : w == 2 ? sb2 : sb3;  // a wave's 16 KB of LDS
   if constexpr (kMode == kStats) {
     // A lane has 64 entries of the vocabulary of each of its four rows; the
@@ -646,9 +665,9 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) s += exp2_fast((acc[mt][nt][e] - from) * kLog2e);
       s += __shfl_xor(s, 32);
-      if (h == 0) red[wm * kTile + 128 * wn + 32 * nt + i] = float2{m, s};
+      if (h == 0) red[wm * kTile + b_at(nt) + i] = float2{m, s};
       // The label's logit, where this wave has it.
-      const int64_t n = nw + 32 * nt;
+      const int64_t n = n0 + b_at(nt) + i;
       const int label = n < N ? p.cols[n].label : -1;
       const int64_t away = label - (p.v0 + mw);
       const bool mine = label >= 0 && away >= 0 && away < 128 && !(away & 4);
@@ -673,14 +692,14 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     // the vocabulary for P, along the live rows for Q. The wave's block goes through
     // its own LDS, a term at a time, so that a store is 256 bytes of four rows.
     const int64_t phalf = whole_pairs(p.vocab), qhalf = whole_pairs(live);
-    const int64_t mwave = m0 + 128 * wm, nwave = n0 + 128 * wn;
+    const int64_t mwave = m0 + 128 * wm, nwave = n0 + 32 * wn;
     const bool whole = m0 + kTile <= M;
     const int left = (int)min(M - mw, (int64_t)kTile);
     int hot[4];  // the label's place among this lane's entries
     float factor[4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
-      const HeadColumn c = p.cols[nw + 32 * nt];  // whole tiles: zeros behind the live rows
+      const HeadColumn c = p.cols[n0 + b_at(nt) + i];  // whole tiles: zeros behind the live rows
       const int64_t away = c.label - (p.v0 + mw);
       hot[nt] = c.label < 0 || away < 0 || away >= kTile ? -1 : (int)away;
       factor[nt] = c.factor;
@@ -723,8 +742,8 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         for (int r = 0; r < 16; ++r) {
           const int row = row0 + 4 * r;
           const u32x4_t v = *reinterpret_cast<const u32x4_t*>(own + row * 128 + 8 * (part ^ (row & 15)));
-          if (in && 64 * pass + row < rows) *reinterpret_cast<u32x4_t*>(at) = v;
-          at += 4 * ld;
+          if (in && 128 * pass + row + (r < 8 ? 0 : 32) < rows) *reinterpret_cast<u32x4_t*>(at) = v;
+          at += (r % 8 == 7 ? 36 : 4) * ld;
         }
       }
     };
@@ -746,7 +765,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         for (int r = 0; r < 8; ++r) {
           const int row = row0 + 4 * r;
           const f32x4_t x = lds[row * 32 + ((2 * part) ^ row)], y = lds[row * 32 + ((2 * part + 1) ^ row)];
-          if (in && 32 * nt + row < rows) {
+          if (in && 64 * nt + row < rows) {
             const auto store = [&](uint16_t* to, u32x2_t a, u32x2_t b) {
               *reinterpret_cast<u32x4_t*>(to) = u32x4_t{a[0], a[1], b[0], b[1]};
             };
@@ -756,6 +775,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
           }
           at += 4 * ld;
         }
+        at += 32 * ld;
       }
     };
     const auto put = [&](uint16_t* to, int64_t plane, int terms, int64_t ld, int rows, bool in) __attribute__((always_inline)) {
@@ -765,7 +785,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         put_one(to, ld, rows, in);
     };
     if (p.P)
-      put(p.P, phalf, p.p_terms, p.ldp, (int)min(N - nwave, (int64_t)128), mwave + 8 * part < phalf);
+      put(p.P, phalf, p.p_terms, p.ldp, (int)min(N - nwave, (int64_t)kTile), mwave + 8 * part < phalf);
     if (p.Q) {
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
@@ -775,7 +795,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
           for (int e = 0; e < 16; ++e)
             acc[mt][nt][e] = (acc[mt][nt][e] - (hot[nt] == 32 * mt + 8 * (e >> 2) + (e & 3) ? 1.0f : 0.0f)) *
                              factor[nt];
-      put(p.Q, p.q_plane, p.q_terms, p.ldq, (int)min(qhalf - nwave, (int64_t)128),
+      put(p.Q, p.q_plane, p.q_terms, p.ldq, (int)min(qhalf - nwave, (int64_t)kTile),
           mwave + 8 * part < p.ldq);
     }
   } else if constexpr (kMode == kDx) {
@@ -784,7 +804,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     float* to = p.acc + ((int64_t)split * tiles + tm * tiles_n + tn) * (kTile * kTile) + 4 * tid;
 #pragma unroll
     for (int mt = 0; mt < 4; ++mt) {
-      if (m0 + 128 * wm + 32 * mt >= M) continue;  // no live row in these 32
+      if (m0 + a_at(mt) >= M) continue;  // no live row in these 32
 #pragma unroll
       for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
@@ -888,8 +908,8 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
   const int tiles_n = ceil_tile(a.K), tiles = ceil_tile(live) * tiles_n;
   const int splits = a.count[1];
   const int r = j % kTile, c = (int)(k % kTile);
-  const int tid = ((r / 128) * 2 + c / 128) * 64 + ((r / 4) % 2) * 32 + c % 32;
-  const int reg = ((r % 128 / 32) * 4 + c % 128 / 32) * 4 + r % 32 / 8;
+  const int tid = ((r / 32) % 2 * 2 + c / 128) * 64 + ((r / 4) % 2) * 32 + c % 32;
+  const int reg = ((r / 64) * 4 + c % 128 / 32) * 4 + r % 32 / 8;
   const float* from = a.acc + ((int64_t)(j / kTile) * tiles_n + k / kTile) * (kTile * kTile) + reg * 1024 + 4 * tid;
   f32x4_t sum[E];  // of a column, its four rows
 #pragma unroll
