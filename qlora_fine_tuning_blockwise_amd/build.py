@@ -11,7 +11,8 @@ LIB = os.path.join(PKG, "libqlora_amd.so")
 SOURCES = ["codebook.cpp", "api.cpp", "quantize.hip", "gemm.hip", "gemm_nt.hip", "gemm_nf4.hip", "lora.hip", "decode.hip", "merge.hip",
            "adamw.hip", "noalloc.hip", "rows_api.cpp", "embed.hip", "norm.hip", "distill.hip",
            "add_norm_api.cpp", "add_norm.hip", "clip_api.cpp", "clip.hip",
-           "head_api.cpp", "head.hip", "head_few.hip"]
+           "head_api.cpp", "head.hip", "head_few.hip",
+           "head_few_dx.hip"]
 
 # Bit-exact arithmetic: no fast-math, no FP contraction, IEEE fp32 division,
 # denormals kept. Packed-fp32 VALU forms are switched off for the device.

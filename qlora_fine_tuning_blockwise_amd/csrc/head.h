@@ -152,4 +152,28 @@ struct HeadDx {
 };
 hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st);
 
+// dX of at most kFewDxRows rows in one pass over W, at any row stride and
+// alignment, for hidden sizes of whole 16 bytes that a workgroup's waves hold.
+constexpr int64_t kFewDxRows = 16, kFewDxWidth = 4096;
+inline bool few_dx(int64_t M, int64_t K) { return M <= kFewDxRows && K <= kFewDxWidth && K % 8 == 0; }
+// Workgroups, one a CU: each leaves a sum of every live row.
+inline int few_dx_groups(int64_t V) { return V < 256 * 16 ? (int)((V + 15) / 16) : 256; }
+inline int64_t few_dx_sums(int64_t M, int64_t V, int64_t K) { return few_dx_groups(V) * ((K + 15) / 16) * 16 * M; }
+struct HeadFewDx {
+  const uint16_t* W;
+  int64_t ldw;
+  const uint16_t* x;
+  int64_t ldx, M, V, K;
+  float scale;
+  const int32_t* map;
+  const int32_t* inv;
+  const int32_t* count;
+  const HeadColumn* cols;
+  float* part;  // few_dx_sums of them
+  int groups;
+  void* dX;
+  int64_t lddx;
+};
+hipError_t launch_head_few_dx(const HeadFewDx& a, bool bf16, hipStream_t st);
+
 }  // namespace qlora

@@ -89,7 +89,9 @@ Layout bwd_layout(int64_t M, int64_t V, int64_t K, bool copy, int dx, int dw) {
   rows_layout(L, c, M, K);
   L.piece = piece_of(M, V, copy);
   if (copy) L.copy = c.take((size_t)L.piece * L.Kp * 2);
-  if (dx >= 0) {
+  if (dx >= 0 && few_dx(M, K)) {
+    L.acc = c.take((size_t)few_dx_sums(M, V, K) * 4);
+  } else if (dx >= 0) {
     L.P = c.take((size_t)L.rows_pad * L.piece * terms(dx) * 2);
     L.acc = c.take((size_t)head_sums(M, K) * kTile * kTile * 4);
   }
@@ -230,8 +232,9 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     if (!dW || accumulate) return QLORA_OK;
     return launch_status(launch_zero(dW, (size_t)V * K * (size_t)elem_bytes(grad_dtype), st));
   }
-  const bool copy = !in_place(W, ldw, K);
-  const Layout L = bwd_layout(M, V, K, copy, dX ? dx_dtype : -1, dW ? grad_dtype : -1);
+  const bool few = M <= kFewRows, once = dX && few_dx(M, K), tiles = dX && !once;
+  const bool unlike = !in_place(W, ldw, K), copy = unlike && (!few || tiles);
+  const Layout L = bwd_layout(M, V, K, unlike, dX ? dx_dtype : -1, dW ? grad_dtype : -1);
   if (!workspace || workspace_bytes < L.total) return QLORA_ERR_WORKSPACE;
   if (any_meet({dX ? matrix(dX, M, K, lddx, dx_dtype) : Span{},
                 dW ? array(dW, V * K, grad_dtype) : Span{}, bytes(workspace, L.total)},
@@ -250,7 +253,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   r.K = K;
   // The first piece's pairs of steps decide the splits, so that every piece adds to
   // the same sums.
-  r.pairs = dX ? (int)(up(V < L.piece ? V : L.piece, 2 * kStep) / (2 * kStep) * terms(dx_dtype)) : 0;
+  r.pairs = tiles ? (int)(up(V < L.piece ? V : L.piece, 2 * kStep) / (2 * kStep) * terms(dx_dtype)) : 0;
   r.map = at<int32_t>(workspace, L.map);
   r.inv = at<int32_t>(workspace, L.inv);
   r.count = at<int32_t>(workspace, L.count);
@@ -258,8 +261,28 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   uint16_t* xs = at<uint16_t>(workspace, L.xs);
   uint16_t* xr = at<uint16_t>(workspace, L.xr);
   hipError_t e = launch_head_rows(r, st);
-  const bool few = M <= kFewRows;
   if (e == hipSuccess && !few) e = launch_head_pack_rows(x, ldx, r.map, r.count, M, K, xs, st);
+  if (e == hipSuccess && once) {
+    HeadFewDx f{};
+    f.W = W;
+    f.ldw = ldw;
+    f.x = x;
+    f.ldx = ldx;
+    f.M = M;
+    f.V = V;
+    f.K = K;
+    f.scale = scale;
+    f.map = r.map;
+    f.inv = r.inv;
+    f.count = r.count;
+    f.cols = r.cols;
+    f.part = at<float>(workspace, L.acc);
+    f.groups = few_dx_groups(V);
+    f.dX = dX;
+    f.lddx = lddx;
+    e = launch_head_few_dx(f, dx_dtype == QLORA_DTYPE_BF16, st);
+  }
+  if (once && !dW) return launch_status(e);
   if (e == hipSuccess && dW)
     e = launch_head_copy(x, ldx, r.map, r.count, M, K, L.Kp, xr, st);
   HeadTiles t{};
@@ -270,7 +293,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   t.cols = r.cols;
   t.rows_pad = L.rows_pad;
   t.steps = L.Kp / kStep;
-  t.p_terms = dX ? terms(dx_dtype) : 0;
+  t.p_terms = tiles ? terms(dx_dtype) : 0;
   t.q_terms = dW ? terms(grad_dtype) : 0;
   t.ldp = L.piece * t.p_terms;
   t.ldq = L.piece;
@@ -294,7 +317,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     t.lda = ldv;
     t.b = xs;
     t.b_steps = t.steps;
-    t.P = dX ? at<uint16_t>(workspace, L.P) : nullptr;
+    t.P = tiles ? at<uint16_t>(workspace, L.P) : nullptr;
     t.Q = dW ? at<uint16_t>(workspace, L.Q) : nullptr;
     if (e == hipSuccess && few) {
       HeadFew f{};
@@ -323,7 +346,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     } else if (e == hipSuccess) {
       e = launch_head_probs(t, st);
     }
-    if (e == hipSuccess && dX) {
+    if (e == hipSuccess && tiles) {
       t.a = t.P;
       t.lda = t.ldp;
       t.b = Wv;
@@ -341,7 +364,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
       e = launch_head_dw(t, st);
     }
   }
-  if (e == hipSuccess && dX) {
+  if (e == hipSuccess && tiles) {
     const HeadDx d{t.acc, r.map, r.inv, r.count, r.cols, W, ldw, M, K, dX, lddx};
     e = launch_head_dx_finish(d, dx_dtype == QLORA_DTYPE_BF16, st);
   }

@@ -237,3 +237,36 @@ def test_head_loss_refused():
         q.qlora_head_loss_fwd(x, W, labels, scale=math.inf)
     with pytest.raises(ValueError):
         q.qlora_head_loss_fwd(x.float(), W, labels)
+
+
+@pytest.mark.parametrize("M,V,K", [(1, 1, 8), (1, 17, 16), (2, 4095, 72), (8, 4097, 1016), (9, 5000, 1024),
+                                   (16, 300, 1032), (3, 8193, 2048), (16, 4100, 2056), (7, 4111, 4088),
+                                   (8, 9000, 4096), (15, 4113, 4096), (16, 64, 4104), (17, 4100, 1024)])
+@pytest.mark.parametrize("kind", [BF16, F32], ids=["bf16", "f32"])
+def test_head_loss_gradient_of_few_rows(M, V, K, kind):
+    """Around the borders of the pass that reads W once: 16 rows, 16 entries a
+    workgroup and 256 workgroups, slices of 1024, 2048 and 4096 columns. A row for
+    each border of the vocabulary's entries whose probability stands there."""
+    say("head few bwd", M, V, K, kind)
+    x, W, labels, dloss = head_inputs(M, V, K, 400 + M, ids=I32)
+    W = (W * math.sqrt(K) / 2).to(BF16)
+    at = [v for v in (V - 1, 0, 15, 16, 4095, 4096, V - 2) if 0 <= v < V]
+    for r, v in enumerate(at[:M]):
+        x[r] = (W[v].float() * (14.0 / float((W[v].float() ** 2).sum()))).to(BF16)
+        labels[r] = (v * 7 + 3) % V
+    for odd in (False, True):
+        xv, xbuf = strided(x, 5 if odd else 8, lead=int(odd))
+        Wv, wbuf = strided(W, 3 if odd else 8, lead=int(odd))
+        stats = torch.empty(2, M, device=DEV)
+        q.qlora_head_loss_fwd(xv, Wv, labels.to(DEV), scale=0.75, stats_out=stats)
+        dXv, buf = strided(torch.zeros(M, K, dtype=kind), 1 + 2 * odd, lead=int(odd))
+        dX, none = q.qlora_head_loss_bwd(xv, Wv, labels.to(DEV), dloss.to(DEV), stats, scale=0.75, dX=dXv,
+                                         want_dw=False)
+        torch.cuda.synchronize()
+        (want, err), _ = close.head_loss_bwd(host(x), host(W), labels.numpy(), dloss.numpy(), 0.75,
+                                             3 if kind == F32 else 1)
+        check(dX, want, err, "dX")
+        assert none is None and int(torch.isnan(buf).sum()) == buf.numel() - M * K
+        again, _ = q.qlora_head_loss_bwd(xv, Wv, labels.to(DEV), dloss.to(DEV), stats, scale=0.75, dx_dtype=kind,
+                                         want_dw=False)
+        assert torch.equal(again, dX)
