@@ -36,7 +36,11 @@ constexpr int kWaves = 8, kEntries = 16;
 template <int NR, int NF, int kTerms>
 __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p) {
   constexpr int kSlice = 32 * NF, kWidth = kWaves * kSlice;
-  constexpr int kStage = NR == 8 ? (NF < 8 ? NF : 8) : 2;  // fragments that go through LDS at a time
+  constexpr int kStage = NR * NF > 128 ? 2 : NF < 8 ? NF : 8;  // fragments that go through LDS at a time
+  // The first of them as soon as the logits' product has read them: the waves' meeting
+  // then finds the next loads in flight (8 rows, 32000 x 4096: 71 instead of 76 us).
+  // Of 2 fragments that is no gain (16 rows: 89 instead of 86 us).
+  constexpr bool kEarly = kStage > 2;
   // 16-byte part c of a row r lies at c ^ (r & 7), in both.
   __shared__ __attribute__((aligned(16))) uint16_t xs[NR * kWidth];
   __shared__ __attribute__((aligned(16))) uint16_t stages[kWaves][kEntries * 32 * kStage];
@@ -91,10 +95,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p
   for (int t = 0; t < 2 * NF; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
   for (int turn = 0; c < chunks; turn ^= 1) {
     f32x4_t s[2] = {f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}};
+    const int next = c + gridDim.x;
+    const auto into_stage = [&](int f0) __attribute__((always_inline)) {
 #pragma unroll
-    for (int f = 0; f < NF; ++f)
+      for (int f = 0; f < kStage; ++f)
+        *reinterpret_cast<u32x4_t*>(put[f & 1] + 64 * (f >> 1)) = words(w[f0 + f]);
+      if (next < chunks) load(next, f0, std::integral_constant<int, kStage>());
+    };
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
       s[f & 1] = mfma_16x16x32(words(w[f]), *reinterpret_cast<const u32x4_t*>(xrow[f & 1] + 64 * (f >> 1)),
                                s[f & 1]);
+      if (kEarly && f == kStage - 1) into_stage(0);
+    }
     // Two buffers in turn: one is written again two meetings after it was read.
     logits[turn][wave][lane] = s[0] + s[1];
     __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
@@ -115,13 +128,10 @@ __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p
       prob[1] = __builtin_bit_cast(s16x4_t, term_of<1>(pr[0], pr[1], pr[2], pr[3]));
       prob[2] = __builtin_bit_cast(s16x4_t, term_of<2>(pr[0], pr[1], pr[2], pr[3]));
     }
-    c += gridDim.x;
+    c = next;
 #pragma unroll
     for (int f0 = 0; f0 < NF; f0 += kStage) {
-#pragma unroll
-      for (int f = 0; f < kStage; ++f)
-        *reinterpret_cast<u32x4_t*>(put[f & 1] + 64 * (f >> 1)) = words(w[f0 + f]);
-      if (c < chunks) load(c, f0, std::integral_constant<int, kStage>());
+      if (f0 || !kEarly) into_stage(f0);
 #pragma unroll
       for (int t = 0; t < 2 * kStage; ++t) {
         const s16x4_t a = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
