@@ -81,6 +81,9 @@ int64_t piece_of(int64_t M, int64_t V, bool copy) {
 // bf16 numbers that a probability or a logit's gradient is split into.
 int terms(int dtype) { return dtype == QLORA_DTYPE_F32 ? 3 : 1; }
 
+// Whether the backward's tile kernels read W, for logits or for dX.
+bool tiles_read_w(int64_t M, int64_t K, bool dx) { return M > kFewRows || (dx && !few_dx(M, K)); }
+
 // dx, dw: the outputs' types, negative for one that is not wanted.
 Layout bwd_layout(int64_t M, int64_t V, int64_t K, bool copy, int dx, int dw) {
   Layout L;
@@ -88,7 +91,7 @@ Layout bwd_layout(int64_t M, int64_t V, int64_t K, bool copy, int dx, int dw) {
   Carve c;
   rows_layout(L, c, M, K);
   L.piece = piece_of(M, V, copy);
-  if (copy) L.copy = c.take((size_t)L.piece * L.Kp * 2);
+  if (copy && tiles_read_w(M, K, dx >= 0)) L.copy = c.take((size_t)L.piece * L.Kp * 2);
   if (dx >= 0 && few_dx(M, K)) {
     L.acc = c.take((size_t)few_dx_sums(M, V, K) * 4);
   } else if (dx >= 0) {
@@ -233,7 +236,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     return launch_status(launch_zero(dW, (size_t)V * K * (size_t)elem_bytes(grad_dtype), st));
   }
   const bool few = M <= kFewRows, once = dX && few_dx(M, K), tiles = dX && !once;
-  const bool unlike = !in_place(W, ldw, K), copy = unlike && (!few || tiles);
+  const bool unlike = !in_place(W, ldw, K), copy = unlike && tiles_read_w(M, K, dX != nullptr);
   const Layout L = bwd_layout(M, V, K, unlike, dX ? dx_dtype : -1, dW ? grad_dtype : -1);
   if (!workspace || workspace_bytes < L.total) return QLORA_ERR_WORKSPACE;
   if (any_meet({dX ? matrix(dX, M, K, lddx, dx_dtype) : Span{},

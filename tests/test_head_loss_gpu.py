@@ -270,3 +270,45 @@ def test_head_loss_gradient_of_few_rows(M, V, K, kind):
         again, _ = q.qlora_head_loss_bwd(xv, Wv, labels.to(DEV), dloss.to(DEV), stats, scale=0.75, dx_dtype=kind,
                                          want_dw=False)
         assert torch.equal(again, dX)
+
+
+@pytest.mark.parametrize("M,V,K", [(8, 40000, 64), (16, 33000, 72), (40, 40001, 24)])
+def test_head_loss_both_gradients_of_few_rows(M, V, K):
+    """The gradient of W in pieces beside the rows' in one pass, from a W that the
+    tiles would copy."""
+    say("head few both", M, V, K)
+    x, W, labels, dloss = head_inputs(M, V, K, 450 + M)
+    Wv, wbuf = strided(W, 3, lead=1)
+    stats = torch.empty(2, M, device=DEV)
+    q.qlora_head_loss_fwd(x.to(DEV), Wv, labels.to(DEV), stats_out=stats)
+    for kind in (BF16, F32):
+        dX, dW = q.qlora_head_loss_bwd(x.to(DEV), Wv, labels.to(DEV), dloss.to(DEV), stats, dx_dtype=kind,
+                                       grad_dtype=kind)
+        (wX, eX), (wW, eW) = close.head_loss_bwd(host(x), host(W), labels.numpy(), dloss.numpy(), 1.0,
+                                                 3 if kind == F32 else 1)
+        check(dX, wX, eX, "dX")
+        check(dW, wW, eW, "dW")
+        alone, _ = q.qlora_head_loss_bwd(x.to(DEV), Wv, labels.to(DEV), dloss.to(DEV), stats, dx_dtype=kind,
+                                         want_dw=False)
+        assert torch.equal(alone, dX)
+
+
+@pytest.mark.parametrize("rows", [1, 31, 32, 33, 63, 64, 65, 96, 97, 127, 128, 129, 161, 255])
+def test_head_loss_of_a_last_tile(rows):
+    """Every count of groups of 32 live rows that a last tile can have."""
+    M, V, K = 256 + rows, 260, 64
+    say("head last tile", M, V, K)
+    x, W, labels, dloss = head_inputs(M, V, K, 480 + rows, dead=0.0)
+    dloss[:] = 1.0 / M
+    stats = torch.empty(2, M, device=DEV)
+    args = x.to(DEV), W.to(DEV), labels.to(DEV)
+    loss = q.qlora_head_loss_fwd(*args, stats_out=stats)
+    want, err, wstats, e_stats = close.head_loss_fwd(host(x), host(W), labels.numpy())
+    check(loss, want, err, "loss")
+    check(stats, wstats, e_stats, "stats")
+    for kind in (BF16, F32):
+        dX, dW = q.qlora_head_loss_bwd(*args, dloss.to(DEV), stats, dx_dtype=kind, grad_dtype=kind)
+        (wX, eX), (wW, eW) = close.head_loss_bwd(host(x), host(W), labels.numpy(), dloss.numpy(), 1.0,
+                                                 3 if kind == F32 else 1)
+        check(dX, wX, eX, "dX")
+        check(dW, wW, eW, "dW")
