@@ -609,7 +609,8 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
 /* Device workspace, in bytes, of qlora_head_loss_bwd for these outputs (dx_dtype,
  * grad_dtype: their types, negative for one that is not wanted): the
  * probabilities of one piece of the vocabulary, 128 MB of them at most up to
- * 32768 rows, and its products' operands. */
+ * 32768 rows, and its products' operands; for dX of at most 16 rows 256 sums of
+ * each element instead. */
 size_t qlora_head_loss_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K, int w_copy,
                                            int dx_dtype, int grad_dtype);
 
@@ -624,9 +625,8 @@ size_t qlora_head_loss_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K, int 
  *          accumulate != 0: dW's sums are added to what it holds (one rounding).
  * The products take probabilities (for dX) and logit gradients (for dW) in bf16,
  * one rounding each, for bf16 outputs, and as the sum of three bf16 numbers for
- * fp32 ones (24 bits), which cost those products three times. A probability below 2^-126 counts as 0.
- * M == 0 writes zero dW (unless it
- * accumulates). The other arguments and errors as in the forward. */
+ * fp32 ones (24 bits), which cost those products three times. A probability below
+ * 2^-126 counts as 0. M == 0 writes zero dW (unless it accumulates). The other arguments and errors as in the forward. */
 int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64_t ldw, int64_t M,
                         int64_t V, int64_t K, const void* labels, int ids_dtype, float scale,
                         const float* stats, const float* dloss, void* dX, int64_t lddx,

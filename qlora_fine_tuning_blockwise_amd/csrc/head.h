@@ -153,7 +153,9 @@ struct HeadDx {
 hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st);
 
 // dX of at most kFewDxRows rows in one pass over W, at any row stride and
-// alignment, for hidden sizes of whole 16 bytes that a workgroup's waves hold.
+// alignment, for hidden sizes of whole 16 bytes that a workgroup's waves hold
+// (32000 x 4096: 8 rows 71 us where logits and product apart take 109, 16 rows 86
+// against 98; 32000 x 2048: 45 and 52 against 63).
 constexpr int64_t kFewDxRows = 16, kFewDxWidth = 4096;
 inline bool few_dx(int64_t M, int64_t K) { return M <= kFewDxRows && K <= kFewDxWidth && K % 8 == 0; }
 // Workgroups, one a CU: each leaves a sum of every live row.
