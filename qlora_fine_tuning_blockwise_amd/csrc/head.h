@@ -91,7 +91,7 @@ hipError_t launch_head_dx(const HeadTiles& a, hipStream_t st);
 hipError_t launch_head_dw(const HeadTiles& a, hipStream_t st);
 // Splits of the live rows' gradient at most, and tiles times splits at most
 // where there is more than one.
-constexpr int kMostSplits = 16, kMostSums = 512;
+constexpr int kMostSplits = 64, kMostSums = 512;
 // Sums of 256 x 256 that acc holds: tiles times splits, at most, for any count of
 // live rows.
 inline int64_t head_sums(int64_t rows_most, int64_t K) {
@@ -105,8 +105,10 @@ inline int64_t head_sums(int64_t rows_most, int64_t K) {
 // entries of the vocabulary (few_entries): part[row][parts]. Probabilities: of live rows, as
 // launch_head_probs leaves them; p_plane: elements between P's terms.
 constexpr int64_t kFewRows = 64;
-// Entries of the vocabulary that a workgroup takes.
-inline int64_t few_entries(int64_t V) { return V >= 192 * 128 ? 128 : 32; }
+// Entries of the vocabulary that a workgroup takes: 128, or 32 where those leave CUs
+// idle. More than 32 rows of x are worth sharing sooner (64 rows, 20000 x 1024: 20.7
+// against 26.5 us, 12000 x 2048: 33 against 25; 32 rows, 20000 x 1024: level).
+inline int64_t few_entries(int64_t V, int64_t M) { return V >= (M > 32 ? 128 : 192) * 128 ? 128 : 32; }
 struct HeadFew {
   const uint16_t* W;  // the piece's rows
   int64_t ldw;

@@ -51,19 +51,22 @@ __device__ __forceinline__ int ceil_tile(int64_t n) { return (int)((n + kTile - 
 // share of the reduction and the time of 50 pairs besides (first loads, 256 KB of
 // sums read and written, and the clock, which falls as more CUs multiply: 1536 x
 // 4096 in pieces of 500 pairs takes as long in 192 workgroups of two splits as in
-// 480 of five, and 3% longer in 768 of eight). A wave weighs all of them at once.
+// 480 of five, and 3% longer in 768 of eight), and a split's sums half a pair to be
+// joined. One tile of 1542 pairs is best in many (127 rows, 32896 x 64, fp32: 106 us of
+// 16 splits, 69 of 55, 65 of 64), four of 313 pairs in fewer (20 rows, 20000 x 1024:
+// 42 us of 16, 40 of 32, 46 of 64). A wave weighs all of them at once.
 __device__ __forceinline__ int dx_splits(int tiles, int pairs) {
   const int s = (threadIdx.x & 63) + 1;
   int best = 0x7FFFFFFF;  // the cost, then the number of splits
   if (s == 1 || (s <= kMostSplits && tiles * s <= kMostSums && s <= pairs)) {
-    const int64_t cost = (int64_t)((tiles * s + 255) / 256) * ((pairs + s - 1) / s + 50);
-    best = (int)(cost < (1 << 26) ? cost : (1 << 26) - 1) * 16 + (s - 1);
+    const int64_t cost = (int64_t)((tiles * s + 255) / 256) * ((pairs + s - 1) / s + 50) + s / 2;
+    best = (int)(cost < (1 << 24) ? cost : (1 << 24) - 1) * kMostSplits + (s - 1);
   }
 #pragma unroll
   for (int d = 32; d; d >>= 1) best = min(best, __shfl_xor(best, d));
-  return best % 16 + 1;
+  return best % kMostSplits + 1;
 }
-static_assert(kMostSplits <= 16, "splits of a key");
+static_assert(kMostSplits <= 64, "a lane each");
 
 // ------------------------------------------------------------- live rows
 constexpr int kRowThreads = 1024;

@@ -47,7 +47,7 @@ void rows_layout(Layout& L, Carve& c, int64_t M, int64_t K) {
   L.xs = c.take((size_t)L.rows_pad * L.Kp * 2);
 }
 
-int64_t few_parts(int64_t V) { return (V + few_entries(V) - 1) / few_entries(V); }
+int64_t few_parts(int64_t V, int64_t M) { return (V + few_entries(V, M) - 1) / few_entries(V, M); }
 
 Layout fwd_layout(int64_t M, int64_t V, int64_t K, bool copy) {
   Layout L;
@@ -55,7 +55,7 @@ Layout fwd_layout(int64_t M, int64_t V, int64_t K, bool copy) {
   Carve c;
   if (M <= kFewRows) {  // one pass over W where it lies
     L.at_label = c.take((size_t)M * 4);
-    L.part = c.take((size_t)few_parts(V) * M * sizeof(float2));
+    L.part = c.take((size_t)few_parts(V, M) * M * sizeof(float2));
     L.total = c.off;
     return L;
   }
@@ -148,12 +148,12 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     f.M = M;
     f.K = K;
     f.vocab = V;
-    f.entries = few_entries(V);
+    f.entries = few_entries(V, M);
     f.scale = scale;
     f.labels = labels;
     f.ids64 = ids_dtype == QLORA_DTYPE_I64;
     f.part = at<float2>(workspace, L.part);
-    f.parts = few_parts(V);
+    f.parts = few_parts(V, M);
     f.at_label = at<float>(workspace, L.at_label);
     hipError_t e = launch_head_few_stats(f, st);
     if (e == hipSuccess)
@@ -332,7 +332,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
       f.K = K;
       f.v0 = v0;
       f.vocab = t.vocab;
-      f.entries = few_entries(t.vocab);
+      f.entries = few_entries(t.vocab, M);
       f.scale = scale;
       f.map = r.map;
       f.count = r.count;
