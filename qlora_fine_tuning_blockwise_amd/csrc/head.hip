@@ -53,8 +53,8 @@ __device__ __forceinline__ int ceil_tile(int64_t n) { return (int)((n + kTile - 
 // 4096 in pieces of 500 pairs takes as long in 192 workgroups of two splits as in
 // 480 of five, and 3% longer in 768 of eight), and a split's sums half a pair to be
 // joined. One tile of 1542 pairs is best in many (127 rows, 32896 x 64, fp32: 106 us of
-// 16 splits, 69 of 55, 65 of 64), four of 313 pairs in fewer (20 rows, 20000 x 1024:
-// 42 us of 16, 40 of 32, 46 of 64). A wave weighs all of them at once.
+// 16 splits, 69 of 47, 65 of 64), four of 313 pairs in fewer (20 rows, 20000 x 1024:
+// 42 us of 16, 40 of 21, 46 of 64). A wave weighs all of them at once.
 __device__ __forceinline__ int dx_splits(int tiles, int pairs) {
   const int s = (threadIdx.x & 63) + 1;
   int best = 0x7FFFFFFF;  // the cost, then the number of splits
