@@ -625,8 +625,11 @@ size_t qlora_head_loss_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K, int 
  *          accumulate != 0: dW's sums are added to what it holds (one rounding).
  * The products take probabilities (for dX) and logit gradients (for dW) in bf16,
  * one rounding each, for bf16 outputs, and as the sum of three bf16 numbers for
- * fp32 ones (24 bits), which cost those products three times. A probability below
- * 2^-126 counts as 0. M == 0 writes zero dW (unless it accumulates). The other arguments and errors as in the forward. */
+ * fp32 ones (24 bits), which cost those products three times. The label's own
+ * probability is not among those of dX: p - 1 there is formed and multiplied by
+ * W_label in fp32, so that a row whose label is likely keeps its gradient's digits.
+ * A probability below 2^-126 counts as 0. M == 0 writes zero dW (unless it
+ * accumulates). The other arguments and errors as in the forward. */
 int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64_t ldw, int64_t M,
                         int64_t V, int64_t K, const void* labels, int ids_dtype, float scale,
                         const float* stats, const float* dloss, void* dX, int64_t lddx,

@@ -105,10 +105,12 @@ def head_loss_fwd(x, W, labels, scale=1.0):
     return np.where(live, loss, 0.0), err * live, stats, np.concatenate([e_m, e_L], 1).T * live
 
 
-def head_loss_bwd(x, W, labels, dloss, scale=1.0, terms=1):
+def head_loss_bwd(x, W, labels, dloss, scale=1.0, terms=1, exact_logits=False):
     """(dX, err), (dW, err), for statistics as an fp32 forward gives them. terms:
     into how many bf16 numbers a probability (for dX) and a logit's gradient (for
-    dW) are split before the matrix products: 1 for bf16 outputs, 3 for fp32."""
+    dW) are split before the matrix products: 1 for bf16 outputs, 3 for fp32. The
+    label's own probability is not split for dX: p - 1 and its product are fp32.
+    exact_logits: inputs whose logits and all of their partial sums fp32 holds."""
     V, K = W.shape
     live, ids = _live(labels, V)
     live = live & (np.asarray(dloss) != 0)
@@ -116,6 +118,8 @@ def head_loss_bwd(x, W, labels, dloss, scale=1.0, terms=1):
     W = W.astype(np.float64)
     M = xs.shape[0]
     z, e = _logits(xs, W, scale)
+    if exact_logits:
+        e = np.zeros_like(e)
     m, L, p, e_m, e_L, rel = _softmax(z, e)
     f = np.where(live, dloss.astype(np.float64) * scale, 0.0)[:, None]
     lost = BF16 ** terms
@@ -126,9 +130,13 @@ def head_loss_bwd(x, W, labels, dloss, scale=1.0, terms=1):
     hot[np.arange(M), ids] = 1.0
     # sums of fp32 products in the matrix units, as the logits', and over pieces
     adds = lambda n: 2 * U * (n * terms / 8 + 64)  # noqa: E731
-    dX = f * (p @ W - W[ids])
-    e_dX = np.abs(f) * ((e_p + p * (lost + adds(V))) @ np.abs(W)
-                        + 3 * U * (np.abs(p @ W) + np.abs(W[ids]))) + 2 * U * np.abs(dX)
+    others = np.where(hot > 0, 0.0, p)
+    rest = np.take_along_axis(p - hot, ids[:, None], 1)
+    dX = f * (others @ W + rest * W[ids])
+    # What is rounded before the products is all but the label's entry; at the
+    # label the probability's own error remains, and the subtraction's.
+    e_dX = np.abs(f) * ((e_p + np.where(hot > 0, 0.0, p + e_p) * (lost + adds(V))) @ np.abs(W)
+                        + 3 * U * (np.abs(others @ W) + np.abs(rest * W[ids]))) + 2 * U * np.abs(dX)
     d = f * (p - hot)
     e_d = np.abs(f) * (e_p + U * np.abs(p - hot)) + 2 * U * np.abs(d)
     dW = d.T @ xs

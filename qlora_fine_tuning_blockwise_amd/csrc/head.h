@@ -68,9 +68,11 @@ struct HeadTiles {
   const HeadColumn* cols;
   float2* part;
   int64_t rows_pad;
-  float* at_label;
-  // probabilities P and the logits' gradients Q, live rows by vocabulary; the
-  // terms of P lie one behind another in a row, those of Q a plane apart
+  float* at_label;  // statistics: the labels' logits
+  // probabilities P (0 at the row's label) and the logits' gradients Q, live rows by
+  // vocabulary; the terms of P lie one behind another in a row, those of Q a plane
+  // apart
+  float* rest;  // the labels' probabilities less 1, of live rows; NULL without P
   uint16_t* P;
   int64_t ldp;
   int p_terms;
@@ -123,6 +125,7 @@ struct HeadFew {
   const int32_t* map;
   const int32_t* count;
   const HeadColumn* cols;
+  float* rest;
   uint16_t* P;
   int64_t ldp, p_plane;
   int p_terms;
@@ -140,9 +143,11 @@ hipError_t launch_head_few_loss(const float2* part, int64_t parts, const float* 
 hipError_t launch_head_loss(const float2* part, int64_t tiles, int64_t rows_pad,
                             const float* at_label, const int32_t* inv, int64_t M, float* loss,
                             float* stats, hipStream_t st);
-// dX of all M rows: factor (sum of the splits - the label's row of W), or 0.
+// dX of all M rows: factor (sum of the splits + rest times the label's row of W),
+// or 0.
 struct HeadDx {
   const float* acc;
+  const float* rest;
   const int32_t* map;
   const int32_t* inv;
   const int32_t* count;
@@ -156,8 +161,8 @@ hipError_t launch_head_dx_finish(const HeadDx& a, bool bf16, hipStream_t st);
 
 // dX of at most kFewDxRows rows in one pass over W, at any row stride and
 // alignment, for hidden sizes of whole 16 bytes that a workgroup's waves hold
-// (32000 x 4096: 8 rows 71 us where logits and product apart take 109, 16 rows 86
-// against 98; 32000 x 2048: 45 and 52 against 63).
+// (32000 x 4096: 8 rows 68 us where logits and product apart take 109, 16 rows 84
+// against 98; 32000 x 2048: 42 and 48 against 63).
 constexpr int64_t kFewDxRows = 16, kFewDxWidth = 4096;
 inline bool few_dx(int64_t M, int64_t K) { return M <= kFewDxRows && K <= kFewDxWidth && K % 8 == 0; }
 // Workgroups, one a CU: each leaves a sum of every live row.
@@ -174,6 +179,7 @@ struct HeadFewDx {
   const int32_t* count;
   const HeadColumn* cols;
   float* part;  // few_dx_sums of them
+  float* rest;  // the live rows' p - 1 at their labels
   int groups;
   void* dX;
   int64_t lddx;

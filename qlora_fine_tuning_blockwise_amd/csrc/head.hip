@@ -4,7 +4,7 @@
 //   z_v  = s sum_k x_k W_vk,  m = max z,  L = log sum_v exp(z_v - m)
 //   loss = L + (m - z_label)
 //   p_v  = exp(z_v - m) exp(-L)
-//   dX   = dloss s (sum_v p_v W_v - W_label)
+//   dX   = dloss s (sum over v != label of p_v W_v + (p_label - 1) W_label)
 //   dW_v = sum over the rows of dloss s (p_v - [v = label]) x
 // A row whose label lies outside of the vocabulary carries no loss.
 //
@@ -20,12 +20,15 @@
 // tile and leave as probabilities in bf16, then the piece's part of the rows'
 // gradients and of W's is a product each.
 //
-// Roundings to bf16: the products' operands have to be bf16. dX is formed from
-// the probabilities alone and the label's row of W is subtracted in fp32 at
-// the end, so that what is rounded (2^-8 of a probability at most) is a part of
-// a small mean of W's rows, not of the label's row. For fp32 gradients a
-// value is split into three bf16 numbers (24 bits, as fp32 has) and the products
-// have three times the terms.
+// Roundings to bf16: the products' operands have to be bf16. The label's
+// probability never is one: its entry of dX's product is 0, p_label - 1 is formed
+// in fp32 and multiplied by the label's row of W in fp32 at the end. What is
+// rounded (2^-8 of a probability at most) are the other entries, which add up to
+// 1 - p_label: dX is as near for a label of probability 0.999 as for one of 0.5
+// (where p_label was rounded with the others and 1 subtracted afterwards, 0.9965
+// cost a fourth of dX and 0.9986 all of it). dW takes p_label - 1 itself, rounded
+// once. For fp32 gradients a value is split into three bf16 numbers (24 bits, as
+// fp32 has) and the products have three times the terms.
 //
 // The tile loop is the dense stage's of the linear layer (gemm_nt.hip has its
 // description): 256 x 256 tiles, four waves of 128 x 128 on
@@ -704,7 +707,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
     const bool whole = m0 + kTile <= M;
     const int left = (int)min(M - mw, (int64_t)kTile);
     int hot[4];  // the label's place among this lane's entries
-    float factor[4];
+    float rest[4], factor[4];
 #pragma unroll
     for (int nt = 0; nt < 4; ++nt) {
       const HeadColumn c = p.cols[n0 + b_at(nt) + i];  // whole tiles: zeros behind the live rows
@@ -727,6 +730,23 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
 #pragma unroll
           for (int e = 0; e < 16; ++e)
             if (32 * mt + 8 * (e >> 2) + (e & 3) >= left) acc[mt][nt][e] = 0.0f;
+    }
+    // p - 1 at a label, which leaves the others; few waves have one.
+#pragma unroll
+    for (int nt = 0; nt < 4; ++nt) {
+      rest[nt] = 0.0f;
+      const bool mine = hot[nt] >= 0 && hot[nt] < 128 && !(hot[nt] & 4);
+      if (!__ballot(mine)) continue;
+#pragma unroll
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (hot[nt] == 32 * mt + 8 * (e >> 2) + (e & 3)) {
+            rest[nt] = acc[mt][nt][e];
+            acc[mt][nt][e] = 0.0f;
+          }
+      rest[nt] -= 1.0f;
+      if (mine && p.rest) p.rest[n0 + b_at(nt) + i] = rest[nt];
     }
     const int part = lane & 15, row0 = lane >> 4;
     // One term: bf16 in LDS, 64 rows at a time.
@@ -801,7 +821,7 @@ __global__ __launch_bounds__(256, 1) void head_tile_kernel(HeadTiles p) {
         for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
           for (int e = 0; e < 16; ++e)
-            acc[mt][nt][e] = (acc[mt][nt][e] - (hot[nt] == 32 * mt + 8 * (e >> 2) + (e & 3) ? 1.0f : 0.0f)) *
+            acc[mt][nt][e] = (hot[nt] == 32 * mt + 8 * (e >> 2) + (e & 3) ? rest[nt] : acc[mt][nt][e]) *
                              factor[nt];
       put(p.Q, p.q_plane, p.q_terms, p.ldq, (int)min(qhalf - nwave, (int64_t)kTile),
           mwave + 8 * part < p.ldq);
@@ -905,9 +925,13 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
   if (j >= live) return;
   // The labels' rows of W, requested before the sums.
   HeadColumn col[4];
+  float rest[4];
   Vec<true, E> w[4];
 #pragma unroll
-  for (int e = 0; e < 4; ++e) col[e] = a.cols[j + e < live ? j + e : j];
+  for (int e = 0; e < 4; ++e) {
+    col[e] = a.cols[j + e < live ? j + e : j];
+    rest[e] = a.rest[j + e < live ? j + e : j];
+  }
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const uint16_t* from = a.W + (int64_t)col[e].label * a.ldw + k;
@@ -933,7 +957,7 @@ __global__ __launch_bounds__(256) void head_dx_finish_kernel(HeadDx a) {
     float o[E], v[E];
     to_float<true, E>(w[row], o);
 #pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = (sum[e][row] - o[e]) * col[row].factor;
+    for (int e = 0; e < E; ++e) v[e] = fmaf(rest[row], o[e], sum[e][row]) * col[row].factor;
     put(a.map[j + row], v);
   }
 }

@@ -34,7 +34,7 @@ int64_t copy_rows(int64_t V, int64_t Kp) {
 struct Layout {
   int64_t rows_pad = 0, Kp = 0, piece = 0;
   size_t map = 0, inv = 0, count = 0, cols = 0, xs = 0, at_label = 0, part = 0, copy = 0;
-  size_t P = 0, Q = 0, xr = 0, acc = 0, total = 0;
+  size_t P = 0, Q = 0, xr = 0, acc = 0, rest = 0, total = 0;
 };
 
 void rows_layout(Layout& L, Carve& c, int64_t M, int64_t K) {
@@ -98,6 +98,7 @@ Layout bwd_layout(int64_t M, int64_t V, int64_t K, bool copy, int dx, int dw) {
     L.P = c.take((size_t)L.rows_pad * L.piece * terms(dx) * 2);
     L.acc = c.take((size_t)head_sums(M, K) * kTile * kTile * 4);
   }
+  if (dx >= 0) L.rest = c.take((size_t)M * 4);
   if (dw >= 0) {
     L.Q = c.take((size_t)L.rows_pad * L.piece * terms(dw) * 2);
     L.xr = c.take((size_t)L.rows_pad * L.Kp * 2);
@@ -280,6 +281,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     f.count = r.count;
     f.cols = r.cols;
     f.part = at<float>(workspace, L.acc);
+    f.rest = at<float>(workspace, L.rest);
     f.groups = few_dx_groups(V);
     f.dX = dX;
     f.lddx = lddx;
@@ -302,6 +304,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   t.ldq = L.piece;
   t.q_plane = L.rows_pad * L.piece;
   t.acc = at<float>(workspace, L.acc);
+  t.rest = tiles ? at<float>(workspace, L.rest) : nullptr;
   t.dW = dW;
   t.dw_bf16 = grad_dtype == QLORA_DTYPE_BF16;
   t.accumulate = accumulate != 0;
@@ -337,6 +340,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
       f.map = r.map;
       f.count = r.count;
       f.cols = r.cols;
+      f.rest = t.rest;
       f.P = t.P;
       f.ldp = t.ldp;
       f.p_plane = up(t.vocab, 2 * kStep);
@@ -368,7 +372,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     }
   }
   if (e == hipSuccess && tiles) {
-    const HeadDx d{t.acc, r.map, r.inv, r.count, r.cols, W, ldw, M, K, dX, lddx};
+    const HeadDx d{t.acc, t.rest, r.map, r.inv, r.count, r.cols, W, ldw, M, K, dX, lddx};
     e = launch_head_dx_finish(d, dx_dtype == QLORA_DTYPE_BF16, st);
   }
   return launch_status(e);

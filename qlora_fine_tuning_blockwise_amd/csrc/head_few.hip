@@ -193,11 +193,23 @@ __global__ __launch_bounds__(64 * kWaves) void head_few_kernel(HeadFew p) {
         pr[e] = in && v + e < p.vocab
                     ? exp2_fast(fmaf(acc[t][e], p.scale, -c.most) * kLog2e) * c.over
                     : 0.0f;
+      // The label's probability is none of P's entries: p - 1 stays in fp32.
+      const int64_t away = c.label - (p.v0 + v);
+      const bool mine = in && away >= 0 && away < 4;
+      const int hot = mine ? (int)away : -1;
+      float rest = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (hot == e) {
+          rest = pr[e] - 1.0f;
+          pr[e] = 0.0f;
+        }
+      if (mine && p.rest) p.rest[row] = rest;
       if (p.P && in && v < p.p_plane) store_terms(p.P + row * p.ldp + v, p.p_plane, p.p_terms, pr);
       if (p.Q) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          pr[e] = (pr[e] - (in && p.v0 + v + e == c.label ? 1.0f : 0.0f)) * c.factor;
+          pr[e] = (hot == e ? rest : pr[e]) * c.factor;
         store_terms(p.Q + row * p.ldq + v, p.q_plane, p.q_terms, pr);
       }
     }

@@ -2,7 +2,8 @@
 // W: with the statistics of the forward a probability is final as soon as its
 // logit is, so that a row of W serves the logit and its part of the gradient while
 // it is on the chip.
-//   P = exp(scale x W' - m) exp(-L),  sum = P W;  dX = dloss scale (sum - W_label)
+//   P = exp(scale x W' - m) exp(-L), but 0 at the label;  sum = P W
+//   dX = dloss scale (sum + (p_label - 1) W_label), the latter in fp32
 //
 // Memory bounds it. A workgroup takes 16 entries of the vocabulary at a time, a
 // wave a slice of the hidden size: its 16 rows of W come straight from memory into
@@ -13,9 +14,11 @@
 // product takes the probabilities. A part of W is requested for the next 16
 // entries as soon as it has left its registers. The sums stay in registers to the
 // end; each workgroup writes them once, and a second kernel joins them in order.
-// 8 rows, 32000 x 4096: 60 us and 7 us for the join (the logits in one pass over W
+// 8 rows, 32000 x 4096: 57 us and 7 us for the join (the logits in one pass over W
 // and the product in another: 48 and 46 us); 1 row of 128000 x 4096: the call takes
-// 200 us, 5.2 TB/s.
+// 190 us, 5.5 TB/s. The loop has no register to spare at 4096 columns: what it can
+// form anew it does not keep, since a register that is spilled is read back behind
+// W's loads and waits for them (16 rows 123 instead of 84 us).
 #include <type_traits>
 
 #include "head_terms.h"
@@ -39,10 +42,12 @@ constexpr int kWaves = 8, kEntries = 16;
 template <int NR, int NF, int kTerms>
 __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p) {
   constexpr int kSlice = 32 * NF, kWidth = kWaves * kSlice;
-  constexpr int kStage = NR * NF > 128 ? 2 : NF < 8 ? NF : 8;  // fragments that go through LDS at a time
+  // Fragments that go through LDS at a time (of 8 all at once: 8 rows, 32000 x 2048 48
+  // instead of 41.5 us).
+  constexpr int kStage = NR * NF > 128 ? 2 : NF < 16 ? 4 : 8;
   // The first of them as soon as the logits' product has read them: the waves' meeting
-  // then finds the next loads in flight (8 rows, 32000 x 4096: 71 instead of 76 us).
-  // Of 2 fragments that is no gain (16 rows: 89 instead of 86 us).
+  // then finds the next loads in flight (8 rows, 32000 x 4096: 5 us). Of 2 fragments that is no
+  // gain (16 rows: 3 us slower).
   constexpr bool kEarly = kStage > 2;
   // 16-byte part c of a row r lies at c ^ (r & 7), in both.
   __shared__ __attribute__((aligned(16))) uint16_t xs[NR * kWidth];
@@ -60,16 +65,25 @@ __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p
     constexpr int kCount = decltype(count)::value;
     const int64_t v = (int64_t)c * kEntries + i;
     const uint16_t* from = p.W + (v < p.V ? v : p.V - 1) * p.ldw;
+    from += k0 + 8 * g;
     if (whole) {
-      from += k0 + 8 * g;
 #pragma unroll
       for (int f = 0; f < kCount; ++f) w[f0 + f] = load_vec<true, 8, true>(from + 32 * (f0 + f));
     } else {  // behind the hidden size its last columns, which x has zeros for
+      int last = K - 8 - (k0 + 8 * g);
+      asm volatile("" : "+v"(last));  // the places are formed here, not kept through the loop
 #pragma unroll
-      for (int f = 0; f < kCount; ++f)
-        w[f0 + f] = load_vec<true, 8, true>(from + min(k0 + 32 * (f0 + f) + 8 * g, K - 8));
+      for (int f = 0; f < kCount; ++f) w[f0 + f] = load_vec<true, 8, true>(from + min(32 * (f0 + f), last));
     }
   };
+  // Of this lane's row, the label counted from its four entries.
+  float most = 0.0f, over = 0.0f, at_label = 0.0f;
+  int label = -kEntries;
+  if (i < live) {
+    const HeadColumn col = p.cols[i];
+    most = col.most, over = col.over, label = col.label - 4 * g;
+  }
+  bool found = false;  // at_label is the label's probability
   int c = blockIdx.x;
   load(c, 0, std::integral_constant<int, NF>());
   // This wave's slice of the live rows, which no other wave reads.
@@ -80,7 +94,6 @@ __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p
                                              : zero_vec<true, 8>();
     *reinterpret_cast<u32x4_t*>(&xs[r * kWidth + k0 + 8 * (part ^ (r & 7))]) = words(v);
   }
-  const HeadColumn col = i < live ? p.cols[i] : HeadColumn{0.0f, 0.0f, 0.0f, -1};
   // Of what is read and written, the places in the first parts; 64 elements on, the
   // swizzle is the same.
   const uint16_t* const xrow[2] = {&xs[(i % NR) * kWidth + k0 + 8 * (g ^ (i & 7))],
@@ -96,6 +109,8 @@ __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p
   f32x4_t acc[2 * NF];  // of 16 columns each: element e is column 4g + e, live row i
 #pragma unroll
   for (int t = 0; t < 2 * NF; ++t) acc[t] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+  // Waited for here: in the loop their wait would be one for the next part of W too.
+  asm volatile("" : "+v"(most), "+v"(over), "+v"(label));
   for (int turn = 0; c < chunks; turn ^= 1) {
     f32x4_t s[2] = {f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}, f32x4_t{0.0f, 0.0f, 0.0f, 0.0f}};
     const int next = c + gridDim.x;
@@ -119,12 +134,19 @@ __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p
     f32x4_t z = logits[turn][0][lane];
 #pragma unroll
     for (int o = 1; o < kWaves; ++o) z += logits[turn][o][lane];
-    // Element e is entry 4g + e, live row i.
-    const int64_t v = (int64_t)c * kEntries + 4 * g;
+    // Element e is entry 4g + e, live row i (past the live rows anything: what becomes
+    // of it stays in its column, which is not stored).
+    const int first = c * kEntries, left = (int)min(p.V - first, (int64_t)kEntries) - 4 * g;
     float pr[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      pr[e] = i < live && v + e < p.V ? exp2_fast(fmaf(z[e], p.scale, -col.most) * kLog2e) * col.over : 0.0f;
+    for (int e = 0; e < 4; ++e) {
+      pr[e] = exp2_fast(fmaf(z[e], p.scale, -most) * kLog2e) * over;
+      pr[e] = e < left ? pr[e] : 0.0f;
+      const bool hot = label == first + e;
+      at_label = hot ? pr[e] : at_label;
+      found |= hot;
+      pr[e] = hot ? 0.0f : pr[e];
+    }
     s16x4_t prob[kTerms];
     prob[0] = __builtin_bit_cast(s16x4_t, term_of<0>(pr[0], pr[1], pr[2], pr[3]));
     if constexpr (kTerms > 1) {
@@ -145,6 +167,7 @@ __global__ __launch_bounds__(64 * kWaves, 1) void head_few_dx_kernel(HeadFewDx p
       }
     }
   }
+  if (wave == 0 && found) p.rest[i] = at_label - 1.0f;  // all waves have the same
   // [workgroup][16 columns][row][column of 16]
   if (i >= live) return;
   const int all = (K + 15) / 16;
@@ -184,10 +207,11 @@ __global__ __launch_bounds__(256) void head_few_dx_join_kernel(HeadFewDx p) {
 #pragma unroll
   for (int r = 1; r < 8; ++r) sum += red[r][threadIdx.x];
   const HeadColumn col = p.cols[m];
+  const float rest = p.rest[m];
   float at_label[4], v[4];
   to_float<true, 4>(load_vec<true, 4>(p.W + (int64_t)col.label * p.ldw + k), at_label);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) v[e] = (sum[e] - at_label[e]) * col.factor;
+  for (int e = 0; e < 4; ++e) v[e] = fmaf(rest, at_label[e], sum[e]) * col.factor;
   store(p.map[m], v);
 }
 
