@@ -8,6 +8,17 @@
 
 namespace qlora {
 
+// A launch holds fewer than 2^32 threads along a dimension: workgroups of 256 that
+// take n items in a row go on along the second one.
+inline dim3 linear_grid(int64_t n) {
+  constexpr int64_t kMost = (int64_t)1 << 23;
+  const int64_t blocks = (n + 255) / 256, y = (blocks + kMost - 1) / kMost;
+  return dim3((unsigned)(y > 1 ? kMost : blocks), (unsigned)(y > 1 ? y : 1));
+}
+__device__ __forceinline__ int64_t linear_thread() {
+  return ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256 + threadIdx.x;
+}
+
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8_t;
 typedef __attribute__((ext_vector_type(4))) float f32x4_t;
 typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;

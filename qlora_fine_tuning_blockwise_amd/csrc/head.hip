@@ -135,7 +135,7 @@ __global__ __launch_bounds__(256) void head_pack_rows_kernel(const uint16_t* src
   const int64_t steps = (K + kStep - 1) / kStep, vecs = steps * 4;
   const int64_t n = count ? *count : rows;
   const int64_t end = (n + kTile - 1) / kTile * kTile;
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t at = linear_thread();
   const int64_t j = at / vecs, c = at - j * vecs;
   if (j >= end) return;
   Vec<true, 8> v = zero_vec<true, 8>();
@@ -156,7 +156,7 @@ __global__ __launch_bounds__(256) void head_copy_kernel(const uint16_t* src, int
                                                         uint16_t* out) {
   const int64_t n = count ? *count : rows;
   const int64_t end = count ? (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
-  const int64_t vecs = Kp / 8, at = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t vecs = Kp / 8, at = linear_thread();
   const int64_t r = at / vecs, c = (at - r * vecs) * 8;
   if (r >= end) return;
   Vec<true, 8> v = zero_vec<true, 8>();
@@ -982,8 +982,8 @@ hipError_t launch_head_pack_rows(const uint16_t* src, int64_t ld, const int32_t*
                                  const int32_t* count, int64_t rows, int64_t K, uint16_t* out,
                                  hipStream_t st) {
   const int64_t vecs = (K + kStep - 1) / kStep * 4;
-  hipLaunchKernelGGL(head_pack_rows_kernel, dim3(blocks_of(tiles_of(rows) * kTile * vecs)), dim3(256),
-                     0, st, src, ld, map, count, rows, K, out);
+  hipLaunchKernelGGL(head_pack_rows_kernel, linear_grid(tiles_of(rows) * kTile * vecs), dim3(256), 0,
+                     st, src, ld, map, count, rows, K, out);
   return hipGetLastError();
 }
 
@@ -991,8 +991,8 @@ hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
                             const int32_t* count, int64_t rows, int64_t K, int64_t Kp, uint16_t* out,
                             hipStream_t st) {
   const int64_t most = count ? (rows + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
-  hipLaunchKernelGGL(head_copy_kernel, dim3(blocks_of(most * (Kp / 8))), dim3(256), 0, st, src, ld,
-                     map, count, rows, K, Kp, out);
+  hipLaunchKernelGGL(head_copy_kernel, linear_grid(most * (Kp / 8)), dim3(256), 0, st, src, ld, map,
+                     count, rows, K, Kp, out);
   return hipGetLastError();
 }
 

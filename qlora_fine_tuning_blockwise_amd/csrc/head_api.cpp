@@ -47,6 +47,7 @@ void rows_layout(Layout& L, Carve& c, int64_t M, int64_t K) {
   L.xs = c.take((size_t)L.rows_pad * L.Kp * 2);
 }
 
+constexpr int64_t kFewEntries = (int64_t)1 << 29;  // of the vocabulary in a launch of few rows
 int64_t few_parts(int64_t V, int64_t M) { return (V + few_entries(V, M) - 1) / few_entries(V, M); }
 
 Layout fwd_layout(int64_t M, int64_t V, int64_t K, bool copy) {
@@ -142,13 +143,11 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (M <= kFewRows) {
     HeadFew f{};
-    f.W = W;
     f.ldw = ldw;
     f.x = x;
     f.ldx = ldx;
     f.M = M;
     f.K = K;
-    f.vocab = V;
     f.entries = few_entries(V, M);
     f.scale = scale;
     f.labels = labels;
@@ -156,7 +155,14 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     f.part = at<float2>(workspace, L.part);
     f.parts = few_parts(V, M);
     f.at_label = at<float>(workspace, L.at_label);
-    hipError_t e = launch_head_few_stats(f, st);
+    // Four threads an entry: fewer than 2^32 of them a launch.
+    hipError_t e = hipSuccess;
+    for (int64_t v0 = 0; v0 < V && e == hipSuccess; v0 += kFewEntries) {
+      f.W = W + v0 * ldw;
+      f.v0 = v0;
+      f.vocab = V - v0 < kFewEntries ? V - v0 : kFewEntries;
+      e = launch_head_few_stats(f, st);
+    }
     if (e == hipSuccess)
       e = launch_head_few_loss(f.part, f.parts, f.at_label, labels, f.ids64, M, V, loss, stats, st);
     return launch_status(e);
@@ -185,9 +191,9 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   t.part = at<float2>(workspace, L.part);
   t.rows_pad = L.rows_pad;
   t.at_label = at<float>(workspace, L.at_label);
-  // Pieces of W that are copied, or all of it (grids stay below 2^22 workgroups).
-  int64_t step = L.piece;
-  if (!copy) step = ((int64_t)1 << 22) / (L.rows_pad / kTile) * kTile;
+  // Pieces of W that are copied, or all of it; grids stay below 2^22 workgroups.
+  int64_t step = ((int64_t)1 << 22) / (L.rows_pad / kTile) * kTile;
+  if (copy && L.piece < step) step = L.piece;
   for (int64_t v0 = 0; v0 < V && e == hipSuccess; v0 += step) {
     t.v0 = v0;
     t.vocab = V - v0 < step ? V - v0 : step;
