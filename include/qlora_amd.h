@@ -594,7 +594,9 @@ size_t qlora_head_loss_fwd_workspace_bytes(int64_t M, int64_t V, int64_t K, int 
  *   stats  fp32 [2,M] or NULL; when given it receives the rows' largest logits,
  *          then log sum_v exp(z_v - largest) (for the backward).
  * A row whose label lies outside of [0, V) has loss 0 and stats 0; its x takes
- * part in nothing, and a batch costs what its other rows do. Products are exact
+ * part in nothing. A batch of more than 64 rows costs what its other rows do; one of
+ * at most 64 costs a pass over W whatever their number, unless there are none, and
+ * then W is not read. Products are exact
  * and sums fp32. NaN and infinities in x stay in their row; one in W reaches
  * every row. QLORA_ERR_SHAPE unless 1 <= V < 2^31 - 1, 1 <= K <=
  * QLORA_MAX_HEAD_WIDTH, V*K <= 2^40, M <= QLORA_MAX_SORTED and the strides hold

@@ -46,7 +46,8 @@ hipError_t launch_head_pack_rows(const uint16_t* src, int64_t ld, const int32_t*
                                  const int32_t* count, int64_t rows, int64_t K, uint16_t* out,
                                  hipStream_t st);
 // out[j] = row map[j] of src (row j without a map) with zeros behind its K columns
-// up to Kp; with `count` for j < *count, and rows of zeros up to two whole steps.
+// up to Kp; for j < rows, nothing where *count is 0; with a map for j < *count, and
+// rows of zeros up to two whole steps.
 hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
                             const int32_t* count, int64_t rows, int64_t K, int64_t Kp, uint16_t* out,
                             hipStream_t st);
@@ -115,7 +116,7 @@ struct HeadFew {
   const uint16_t* W;  // the piece's rows
   int64_t ldw;
   const uint16_t* x;
-  int64_t ldx, M, K, v0, vocab, entries;
+  int64_t ldx, M, K, V, v0, vocab, entries;  // v0, vocab: the piece
   float scale;
   const void* labels;
   bool ids64;

@@ -148,14 +148,15 @@ __global__ __launch_bounds__(256) void head_pack_rows_kernel(const uint16_t* src
   *reinterpret_cast<u32x4_t*>(to) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
 }
 
-// A thread copies 8 columns of a row: rows map[j] (or j) of src with zeros behind
-// its K columns, and whole rows of zeros up to two whole steps.
+// A thread copies 8 columns of a row with zeros behind its K columns: rows map[j] of
+// src for the live ones, *count, and whole rows of zeros up to two whole steps; or
+// all rows, where any is live.
 __global__ __launch_bounds__(256) void head_copy_kernel(const uint16_t* src, int64_t ld,
                                                         const int32_t* map, const int32_t* count,
                                                         int64_t rows, int64_t K, int64_t Kp,
                                                         uint16_t* out) {
-  const int64_t n = count ? *count : rows;
-  const int64_t end = count ? (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
+  const int64_t live = *count, n = map ? live : live ? rows : 0;
+  const int64_t end = map ? (n + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : n;
   const int64_t vecs = Kp / 8, at = linear_thread();
   const int64_t r = at / vecs, c = (at - r * vecs) * 8;
   if (r >= end) return;
@@ -990,7 +991,7 @@ hipError_t launch_head_pack_rows(const uint16_t* src, int64_t ld, const int32_t*
 hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
                             const int32_t* count, int64_t rows, int64_t K, int64_t Kp, uint16_t* out,
                             hipStream_t st) {
-  const int64_t most = count ? (rows + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
+  const int64_t most = map ? (rows + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
   hipLaunchKernelGGL(head_copy_kernel, linear_grid(most * (Kp / 8)), dim3(256), 0, st, src, ld, map,
                      count, rows, K, Kp, out);
   return hipGetLastError();

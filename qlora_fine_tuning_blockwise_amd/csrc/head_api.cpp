@@ -148,6 +148,7 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     f.ldx = ldx;
     f.M = M;
     f.K = K;
+    f.V = V;
     f.entries = few_entries(V, M);
     f.scale = scale;
     f.labels = labels;
@@ -201,7 +202,7 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     t.lda = ldw;
     if (copy) {
       uint16_t* Wc = at<uint16_t>(workspace, L.copy);
-      e = launch_head_copy(t.a, ldw, nullptr, nullptr, t.vocab, K, L.Kp, Wc, st);
+      e = launch_head_copy(t.a, ldw, nullptr, r.count, t.vocab, K, L.Kp, Wc, st);
       t.a = Wc;
       t.lda = L.Kp;
     }
@@ -321,7 +322,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
     int64_t ldv = ldw;
     if (copy) {
       uint16_t* Wc = at<uint16_t>(workspace, L.copy);
-      e = launch_head_copy(Wv, ldw, nullptr, nullptr, t.vocab, K, L.Kp, Wc, st);
+      e = launch_head_copy(Wv, ldw, nullptr, r.count, t.vocab, K, L.Kp, Wc, st);
       Wv = Wc;
       ldv = L.Kp;
     }
@@ -339,6 +340,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
       f.ldx = ldx;
       f.M = M;
       f.K = K;
+      f.V = V;
       f.v0 = v0;
       f.vocab = t.vocab;
       f.entries = few_entries(t.vocab, M);

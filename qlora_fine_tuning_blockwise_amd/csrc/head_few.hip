@@ -43,6 +43,13 @@ __global__ __launch_bounds__(64 * kWaves) void head_few_kernel(HeadFew p) {
   __shared__ float2 red[kProbs ? 1 : kWaves * 16 * NT];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, i = lane & 15, g = lane >> 4;
   const int rows = kProbs ? *p.count : (int)p.M;
+  // Without a live row nothing is read of W.
+  if constexpr (kProbs) {
+    if (rows == 0) return;
+  } else {
+    const int64_t label = lane < rows ? load_index(p.labels, p.ids64, lane) : -1;
+    if (!__ballot(label >= 0 && label < p.V)) return;
+  }
   const int64_t v0 = (int64_t)blockIdx.x * kEntries + 16 * wave;  // in the piece
   const int64_t K = p.K;
   // This lane's row of W; past the piece the last one, whose results are not used.

@@ -114,3 +114,26 @@ def test_head_loss_without_rows_past_one_launch():
     dW = torch.ones(V, K, device=DEV)
     q.qlora_head_loss_bwd(x, W, labels, none, torch.empty(2, 0, device=DEV), want_dx=False, dW=dW)
     assert int(dW.count_nonzero()) == 0
+
+
+@pytest.mark.parametrize("M,K", [(1, 64), (16, 64), (40, 100), (64, 64), (100, 100)])
+def test_head_loss_does_no_work_without_labels(M, K):
+    """No row has a label: W is neither multiplied nor copied, so that the
+    workspace's end, where the sums of a few rows or a copy of W would lie, stays as
+    it was. With one label it does not."""
+    V = 5000
+    x, W = torch.ones(M, K, dtype=BF16, device=DEV), torch.ones(V, K, dtype=BF16, device=DEV)
+    labels, dloss = torch.full((M,), -100, device=DEV), torch.ones(M, device=DEV)
+    need = q.qlora_head_loss_fwd_workspace_bytes(M, V, K, K % 32 != 0)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    end = ws if M <= 64 else ws[-V * K * 2:]
+    stats = torch.empty(2, M, device=DEV)
+    for labelled in (0, 1):
+        if labelled:
+            labels[M // 2] = 4999
+        ws.fill_(7)
+        loss = q.qlora_head_loss_fwd(x, W, labels, stats_out=stats, workspace=ws)
+        assert bool((end == 7).all()) == (not labelled)
+        assert int(loss.count_nonzero()) == labelled
+        _, dW = q.qlora_head_loss_bwd(x, W, labels, dloss, stats)
+        assert bool(dW.any()) == bool(labelled)
