@@ -609,10 +609,16 @@ int qlora_head_loss_fwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
                         void* stream);
 
 /* Device workspace, in bytes, of qlora_head_loss_bwd for these outputs (dx_dtype,
- * grad_dtype: their types, negative for one that is not wanted): the
- * probabilities of one piece of the vocabulary, 128 MB of them at most up to
- * 32768 rows, and its products' operands; for dX of at most 16 rows 256 sums of
- * each element instead. */
+ * grad_dtype: their types, negative for one that is not wanted). For up to 32768
+ * rows, in MB of 2^20 bytes:
+ *   each output: the probabilities or logit gradients of one piece of the
+ *     vocabulary, at most 128 MB for bf16 and 384 MB for fp32;
+ *   dX: its sums, at most 128 MB or, if that is more, 256 KB for each 256 x 256
+ *     elements;
+ *   the rows of x twice, of whole 32 elements and 256 rows, and 32 bytes a row;
+ *   w_copy: at most 32768 rows of W, of whole 32 elements.
+ * dX of at most 16 rows (K <= 4096, K % 8 == 0) needs 256 sums of 4 bytes of each
+ * element in whole 16 columns in place of its probabilities and sums. */
 size_t qlora_head_loss_bwd_workspace_bytes(int64_t M, int64_t V, int64_t K, int w_copy,
                                            int dx_dtype, int grad_dtype);
 
