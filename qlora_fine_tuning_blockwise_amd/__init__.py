@@ -907,9 +907,12 @@ def qlora_head_loss_bwd(x: torch.Tensor, W: torch.Tensor, labels: torch.Tensor,
 class TensorList:
     """Tensors as qlora_grad_norm and qlora_grad_scale take them: contiguous,
     fp32 or bf16, on one device. A program whose gradients stay where they are
-    makes the list once (qlora_tensor_list), outside of a graph's capture; it
-    holds the tensors, which must keep their storage, and a table of their pieces
-    on the device, with which a call is one launch for all of them."""
+    makes the list once (qlora_tensor_list), outside of a graph's capture. It is a
+    list of the memory in which they lie then: it holds that memory, and a table
+    of its pieces on the device, with which a call is one launch for all of
+    them. A tensor that is given other memory later (set_, or a new .grad) is not in
+    the list with it; memory that is moved under its tensors (a storage that is
+    resized) is refused by every later call. A captured graph has no such check."""
 
     def __init__(self, tensors, table=True):
         self.tensors = tuple(tensors)
@@ -924,6 +927,13 @@ class TensorList:
                 raise ValueError(f"tensors: on {t.device} and on {self.device}")
             d.data, d.n, d.dtype, d.reserved = t.data_ptr(), t.numel(), _FLOATS[t.dtype], 0
         self.address = ctypes.addressof(self.array)
+        # Each storage once: the views of one buffer are checked at once (448 storages
+        # of their own take some 60 us a call).
+        held = {}
+        for t in self.tensors if table else ():
+            s = t.untyped_storage()
+            held.setdefault(s.data_ptr(), s)
+        self.storages = [(s, p) for p, s in held.items()]
         lib, count = _lib.load(), len(self.tensors)
         self.workspace_bytes = int(lib.qlora_grad_norm_workspace_bytes(self.address, count))
         self.table = None
@@ -937,6 +947,13 @@ class TensorList:
     def __len__(self):
         return len(self.tensors)
 
+    def in_place(self) -> "TensorList":
+        """The list itself, if its memory is still where it was."""
+        for s, p in self.storages:
+            if s.data_ptr() != p:
+                raise ValueError("tensors: a storage of the list was moved since the list was made")
+        return self
+
 
 def qlora_tensor_list(tensors) -> TensorList:
     """The tensors as a list that a program keeps (see TensorList)."""
@@ -945,7 +962,7 @@ def qlora_tensor_list(tensors) -> TensorList:
 
 def _tensors(tensors) -> TensorList:
     """A list that the program keeps, or one for this call alone."""
-    return tensors if isinstance(tensors, TensorList) else TensorList(tensors, table=False)
+    return tensors.in_place() if isinstance(tensors, TensorList) else TensorList(tensors, table=False)
 
 
 def qlora_grad_norm_workspace_bytes(grads) -> int:
