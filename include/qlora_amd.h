@@ -674,8 +674,8 @@ size_t qlora_grad_norm_workspace_bytes(const qlora_tensor* grads, int64_t count)
  *           then, instead of one for all);
  *   result  fp32 [2], device;  max_norm >= 0 (infinity: the factor is 1).
  * Squares and sums are in 64 bits, so values of every size have their norm. A
- * norm that is infinite gives the factor 0, a NaN gives NaN: a caller that skips
- * such steps looks at the norm. A tensor that is listed twice counts twice. No
+ * norm that is infinite gives the factor 0 (1 if max_norm is infinite too), a NaN
+ * gives NaN: a caller that skips such steps looks at the norm. A tensor that is listed twice counts twice. No
  * elements: norm 0, factor 1. QLORA_ERR_INVALID_ARG for count < 0, n < 0,
  * reserved != 0, a NULL array, max_norm < 0 or NaN, and a result or workspace over
  * a tensor or the table; QLORA_ERR_SHAPE past QLORA_MAX_TENSORS tensors or 2^40

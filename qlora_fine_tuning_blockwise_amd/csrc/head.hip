@@ -36,7 +36,8 @@
 // pairs of steps, b in a ring of four steps. The matrix units bound it: 1536 rows,
 // 128000 x 4096, forward 1250 us (1290 TFLOP/s), dX 2740 us (1175 TFLOP/s of two
 // products); 1500 rows, 32003 x 2048: logits 202, dX 165, dW 206 us. A step of a
-// tile takes 0.55 us, its first loads and its end 9 us (statistics) to 11 us.
+// tile takes 0.55 us, its first loads and its end 9 us (statistics) to 11 us. The
+// build for dX keeps 16 registers in scratch, outside of the steps.
 #include <type_traits>
 
 #include "head_terms.h"

@@ -280,7 +280,9 @@ hipError_t bwd(const NormBwd& a, unsigned grid, hipStream_t st) {
 // 27.2, 256 x 2 40; 2048 x 8192 1024 x 1 27.6, 512 x 2 39. Rows past 8192 need 16
 // elements a thread all the same: those builds sit at the limit of 128 registers
 // and, but for the one that is bf16 throughout, keep 4 to 28 more in scratch
-// (2048 x 16384 bf16 48 us for 201 MB, fp32 95 us for 403 MB).
+// (2048 x 16384 bf16 48 us for 201 MB, fp32 95 us for 403 MB). With dH all of them do,
+// bf16 throughout 6 registers and the others 24 to 99 (2048 x 16384 bf16 61 us for 268
+// MB, fp32 130 us for 537 MB, bf16 with dH and dX in fp32 133 us for 403 MB).
 template <bool XB, bool YB, bool DB, bool kAdd = false>
 hipError_t bwd_width(const NormBwd& a, unsigned grid, hipStream_t st) {
   if (a.N < (XB && YB && DB ? 8 : 4)) return bwd<XB, YB, DB, kAdd, 64, 1, true>(a, grid, st);
