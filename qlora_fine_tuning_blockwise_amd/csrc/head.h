@@ -52,6 +52,9 @@ hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
                             const int32_t* count, int64_t rows, int64_t K, int64_t Kp, uint16_t* out,
                             hipStream_t st);
 
+// Zeros in 4-byte aligned memory, a multiple of two bytes (dW without rows).
+hipError_t launch_head_zero(void* p, int64_t bytes, hipStream_t st);
+
 // A product's tiles; what a and b are depends on the launch.
 struct HeadTiles {
   const uint16_t* a;  // 16-byte aligned rows

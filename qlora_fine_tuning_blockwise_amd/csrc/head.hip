@@ -170,6 +170,15 @@ __global__ __launch_bounds__(256) void head_copy_kernel(const uint16_t* src, int
   *reinterpret_cast<u32x4_t*>(out + at * 8) = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
 }
 
+// Zeros, two elements of 16 bits a thread; an odd number of them ends in one.
+__global__ __launch_bounds__(256) void head_zero_kernel(uint32_t* p, int64_t halves) {
+  const int64_t i = linear_thread();
+  if (2 * i + 1 < halves)
+    p[i] = 0u;
+  else if (2 * i < halves)
+    reinterpret_cast<uint16_t*>(p)[2 * i] = 0;
+}
+
 // ------------------------------------------------------------------ tiles
 constexpr int kOp = kTile * kStep;  // bf16 elements of one step of an operand (16 KB)
 constexpr int kPair = 2 * kOp;      // of two steps
@@ -995,6 +1004,12 @@ hipError_t launch_head_copy(const uint16_t* src, int64_t ld, const int32_t* map,
   const int64_t most = map ? (rows + 2 * kStep - 1) / (2 * kStep) * (2 * kStep) : rows;
   hipLaunchKernelGGL(head_copy_kernel, linear_grid(most * (Kp / 8)), dim3(256), 0, st, src, ld, map,
                      count, rows, K, Kp, out);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_zero(void* p, int64_t bytes, hipStream_t st) {
+  hipLaunchKernelGGL(head_zero_kernel, linear_grid((bytes / 2 + 1) / 2), dim3(256), 0, st,
+                     static_cast<uint32_t*>(p), bytes / 2);
   return hipGetLastError();
 }
 

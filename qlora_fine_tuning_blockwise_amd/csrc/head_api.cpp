@@ -241,7 +241,7 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (M == 0) {  // no rows: the gradient of W is zero
     if (!dW || accumulate) return QLORA_OK;
-    return launch_status(launch_zero(dW, (size_t)V * K * (size_t)elem_bytes(grad_dtype), st));
+    return launch_status(launch_head_zero(dW, V * K * elem_bytes(grad_dtype), st));
   }
   const bool few = M <= kFewRows, once = dX && few_dx(M, K), tiles = dX && !once;
   const bool unlike = !in_place(W, ldw, K), copy = unlike && tiles_read_w(M, K, dX != nullptr);

@@ -918,13 +918,9 @@ __global__ __launch_bounds__(256) void colred_finalize_kernel(FinJob j0, FinJob 
     static_cast<float*>(out)[o] = v;
 }
 
-// 4 bytes a thread; bf16 elements of an odd number end in two.
-__global__ __launch_bounds__(256) void zero_kernel(uint32_t* __restrict__ p, int64_t halves) {
-  const int64_t i = linear_thread();
-  if (2 * i + 1 < halves)
-    p[i] = 0u;
-  else if (2 * i < halves)
-    reinterpret_cast<uint16_t*>(p)[2 * i] = 0;
+__global__ __launch_bounds__(256) void zero_kernel(uint32_t* __restrict__ p, int64_t words) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < words) p[i] = 0u;
 }
 
 }  // namespace
@@ -1128,10 +1124,10 @@ hipError_t launch_colred_finalize2(const float* part0, int64_t C0, bool transpos
 }
 
 hipError_t launch_zero(void* p, size_t bytes, hipStream_t st) {
-  const int64_t halves = (int64_t)(bytes / 2);
-  if (halves == 0) return hipSuccess;
-  hipLaunchKernelGGL(zero_kernel, linear_grid((halves + 1) / 2), dim3(256), 0, st,
-                     static_cast<uint32_t*>(p), halves);
+  const int64_t words = (int64_t)(bytes / 4);
+  if (words == 0) return hipSuccess;
+  hipLaunchKernelGGL(zero_kernel, dim3((unsigned)((words + 255) / 256)), dim3(256), 0, st,
+                     static_cast<uint32_t*>(p), words);
   return hipGetLastError();
 }
 
