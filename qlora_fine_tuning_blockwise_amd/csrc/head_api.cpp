@@ -241,6 +241,8 @@ int qlora_head_loss_bwd(const uint16_t* x, int64_t ldx, const uint16_t* W, int64
   hipStream_t st = static_cast<hipStream_t>(stream);
   if (M == 0) {  // no rows: the gradient of W is zero
     if (!dW || accumulate) return QLORA_OK;
+    if (W && meet(array(dW, V * K, grad_dtype), matrix(W, V, K, ldw, QLORA_DTYPE_BF16)))
+      return QLORA_ERR_INVALID_ARG;
     return launch_status(launch_head_zero(dW, V * K * elem_bytes(grad_dtype), st));
   }
   const bool few = M <= kFewRows, once = dX && few_dx(M, K), tiles = dX && !once;
