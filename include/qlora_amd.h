@@ -699,8 +699,8 @@ int qlora_grad_scale(const qlora_tensor* grads, const qlora_tensor* out, int64_t
                      const void* table, const void* out_table, const float* factor, void* stream);
 
 /* qlora_adamw_step on the gradient grad * factor, each product rounded to fp32
- * before the step's first operation; factor is fp32 on the device (NULL:
- * QLORA_ERR_INVALID_ARG): clipping without a pass over the gradients. Everything
+ * before the step's first operation; factor is fp32 on the device (NULL or
+ * within an array that the step writes: QLORA_ERR_INVALID_ARG): clipping without a pass over the gradients. Everything
  * else as qlora_adamw_step. */
 int qlora_adamw_step_scaled(float* param, const void* grad, int grad_dtype, const float* factor,
                             float* exp_avg, float* exp_avg_sq, uint16_t* param_bf16, int64_t n,

@@ -266,6 +266,10 @@ int qlora_adamw_step_scaled(float* param, const void* grad, int grad_dtype, cons
     if (p && !(p = reached(p))) return QLORA_ERR_INVALID_ARG;
     if (p && !aligned16(p)) return QLORA_ERR_ALIGN;  // the mapped address, too
   }
+  // Every workgroup reads the factor: not from what others have written.
+  const Span f = span_of(factor, 4);
+  for (int i : {0, 2, 3, 4})
+    if (meet(span_of(view[i], n * (i == 4 ? 2 : 4)), f)) return QLORA_ERR_INVALID_ARG;
   const double b1t = std::pow(beta1, (double)step), b2t = std::pow(beta2, (double)step);
   AdamScalars s;
   s.b1 = (float)beta1;

@@ -86,3 +86,20 @@ def test_infinite_norm_and_infinite_bound():
             assert float(q.qlora_grad_norm([t], bound)[1]) == want
             t[9] = torch.nan
             assert bool(torch.isnan(q.qlora_grad_norm([t], bound)).all())
+
+
+@pytest.mark.parametrize("place", range(4))
+def test_factor_within_what_the_step_writes(place):
+    """Refused, and nothing is written; within the gradient, which is only read, it
+    is taken."""
+    n = 1000
+    written = [torch.full((n,), 0.5, device=DEV) for _ in range(3)] + [torch.full((n,), 0.5, dtype=BF16, device=DEV)]
+    grad = torch.full((n,), 0.25, device=DEV)
+    for at in (0, n // 2 - 1):
+        factor = written[place].view(F32)[at:at + 1]
+        with pytest.raises(RuntimeError):
+            q.qlora_adamw_step(written[0], grad, written[1], written[2], 1, 1e-3, param_bf16=written[3],
+                               grad_factor=factor)
+        assert all(bool((t == 0.5).all()) for t in written)
+    q.qlora_adamw_step(written[0], grad, written[1], written[2], 1, 1e-3, param_bf16=written[3], grad_factor=grad[7:8])
+    assert not bool((written[0] == 0.5).any())
